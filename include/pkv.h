@@ -318,6 +318,87 @@ pkv_status pkv_run_decode_static(pkv_handle_t h, const void *q, const void *kv_l
                                  const int32_t *paged_kv_last_page_len, int batch, int window_left, float sm_scale,
                                  pkv_stream_t stream);
 
+/* ---- latent attention ---- */
+
+/*
+ * Attention whose keys and values come from one vector per token, [latent | rope], shared by
+ * all heads.  It has a handle type of its own, used like the ordinary one (one per issuing
+ * thread; errors, streams, workspaces and plan reuse as described at the top of this file).
+ *
+ * Absorbed form (serving): the paged cache keeps the vectors themselves.  One layer slice is
+ * [num_cache_pages, page_size, latent_dim + rope_dim] bf16, contiguous, 16-byte aligned.  A
+ * head's query is [q W_uk^T | q_rope] (latent_dim + rope_dim values), its keys are the cached
+ * vectors, its values their first latent_dim columns; the caller multiplies the output by W_uv.
+ * Rows, new tokens, causal, window_left and lse mean what they mean for pkv_plan in prefill
+ * mode; every row may have any number of new tokens, one (a decode step) included.
+ *
+ * Expanded form (prompts): contiguous per-head keys [k_nope | k_rope], k_rope shared by all
+ * heads, and per-head values, both made from the latent vectors by the caller; segments as in
+ * pkv_plan_dense.
+ *
+ * Widths: latent_dim 512, rope_dim 64, nope_dim 128, v_dim 128 (0 selects these); others are
+ * PKV_ERR_UNSUPPORTED.  page_size: a power of two from 8 to 1024.  num_heads: 1 to 1024.
+ */
+typedef struct pkv_latent_s *pkv_latent_t;
+typedef struct {
+    int num_heads;
+    int latent_dim, rope_dim; /* the cached vector */
+    int nope_dim, v_dim;      /* the expanded heads: key without rope, value */
+    int page_size;
+    int max_batch;
+    int max_total_tokens;
+    int max_num_pages;
+    int num_cache_pages;
+    int sm_count;    /* SMs the work split targets; 0 = query the current device */
+    int enable_nvtx;
+} pkv_latent_config;
+
+pkv_status pkv_latent_create(const pkv_latent_config *cfg, pkv_latent_t *out);
+void pkv_latent_destroy(pkv_latent_t h);
+/* As pkv_last_error (h == NULL: the last failed pkv_latent_create on this thread). */
+const char *pkv_latent_last_error(pkv_latent_t h);
+/* Bytes of workspace a plan needs at the handle's maxima: mode PKV_MODE_PREFILL for
+ * pkv_latent_plan, PKV_MODE_DENSE for pkv_latent_plan_dense. */
+pkv_status pkv_latent_workspace_size(pkv_latent_t h, int mode, size_t *bytes);
+/*
+ * Plan a paged step (HOST index arrays of the post-append state; qo_indptr NULL = one new
+ * token per row).  sm_scale must be > 0: the width it comes from is the expanded head's, which
+ * the cached vector does not tell.  causal 0 or 1.
+ */
+pkv_status pkv_latent_plan(pkv_latent_t h, const int32_t *qo_indptr, const int32_t *paged_kv_indptr,
+                           const int32_t *paged_kv_indices, const int32_t *paged_kv_last_page_len, int batch,
+                           int causal, int window_left, float sm_scale, void *workspace, size_t workspace_bytes,
+                           pkv_stream_t stream);
+/*
+ * Write the step's new vectors into their slots (as pkv_kv_append_planned): c_new [T,
+ * latent_dim] and rope_new [T, rope_dim] device bf16, rows *_stride elements apart (multiples of
+ * 8, at least the width), 16-byte aligned.  Nothing else in the slice is touched.
+ */
+pkv_status pkv_latent_append_planned(pkv_latent_t h, const void *c_new, int64_t c_stride, const void *rope_new,
+                                     int64_t rope_stride, void *cache_layer, void *workspace, pkv_stream_t stream);
+/*
+ * Attention of the planned step: q device bf16 [T, num_heads, latent_dim + rope_dim]; out
+ * device bf16 [T, num_heads, latent_dim]; lse device fp32 [T, num_heads] or NULL.
+ */
+pkv_status pkv_latent_run(pkv_latent_t h, const void *q, const void *cache_layer, void *out, float *lse,
+                          void *workspace, pkv_stream_t stream);
+pkv_status pkv_latent_plan_dense(pkv_latent_t h, const int32_t *cu_q, const int32_t *cu_k, int batch, int causal,
+                                 int window_left, float sm_scale, void *workspace, size_t workspace_bytes,
+                                 pkv_stream_t stream);
+/*
+ * q [cu_q[batch], num_heads, nope_dim + rope_dim] and out [.., num_heads, v_dim], contiguous;
+ * k_nope [cu_k[batch], num_heads, nope_dim] and v [cu_k[batch], num_heads, v_dim] with token and
+ * head strides in elements (the two halves of one projection's output need no copy); k_rope
+ * [cu_k[batch], rope_dim] with a token stride.  Device bf16, 16-byte aligned, strides multiples
+ * of 8 and at least the width of what they step over.  lse fp32 [cu_q[batch], num_heads] or NULL.
+ */
+pkv_status pkv_latent_run_dense(pkv_latent_t h, const void *q, const void *k_nope, int64_t kn_token_stride,
+                                int64_t kn_head_stride, const void *k_rope, int64_t kr_token_stride, const void *v,
+                                int64_t v_token_stride, int64_t v_head_stride, void *out, float *lse,
+                                void *workspace, pkv_stream_t stream);
+/* As pkv_check_device_error. */
+pkv_status pkv_latent_check_device_error(pkv_latent_t h, void *workspace, pkv_stream_t stream, int *code);
+
 /* ---- host-only planning queries (no CUDA call; usable on a machine without a GPU) ---- */
 
 /*

@@ -24,7 +24,10 @@ STATUS_NAMES = ["OK", "INVALID", "UNSUPPORTED", "WORKSPACE", "TOO_MANY_PREFILL_R
 EXPORTS = ["pkv_create", "pkv_destroy", "pkv_last_error", "pkv_workspace_size", "pkv_plan", "pkv_kv_append", "pkv_kv_append_planned",
            "pkv_run_decode", "pkv_run_prefill", "pkv_run_mixed", "pkv_check_device_error", "pkv_append_slots",
            "pkv_mixed_layout", "pkv_decode_split", "pkv_decode_head_rows", "pkv_run_decode_static", "pkv_context_only_views",
-           "pkv_plan_dense", "pkv_run_dense", "pkv_gather_kv", "pkv_run_decode_append", "pkv_selftest_wait_timeout"]
+           "pkv_plan_dense", "pkv_run_dense", "pkv_gather_kv", "pkv_run_decode_append", "pkv_selftest_wait_timeout",
+           "pkv_latent_create", "pkv_latent_destroy", "pkv_latent_last_error", "pkv_latent_workspace_size",
+           "pkv_latent_plan", "pkv_latent_append_planned", "pkv_latent_run", "pkv_latent_plan_dense",
+           "pkv_latent_run_dense", "pkv_latent_check_device_error"]
 
 
 class PkvError(RuntimeError):
@@ -41,6 +44,12 @@ class Config(ctypes.Structure):
         "enable_nvtx")]
 
 
+class LatentConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "num_heads", "latent_dim", "rope_dim", "nope_dim", "v_dim", "page_size", "max_batch", "max_total_tokens",
+        "max_num_pages", "num_cache_pages", "sm_count", "enable_nvtx")]
+
+
 _lib = None
 
 
@@ -52,7 +61,7 @@ def load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise FileNotFoundError(f"{path} is missing: build it with `python -m paged_kv_attention_gqa_gb300.build`")
     lib = ctypes.CDLL(path)
-    vp, i, i32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p
+    vp, i, i32p, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64
     sig = {
         "pkv_create": ([ctypes.POINTER(Config), ctypes.POINTER(vp)], i),
         "pkv_destroy": ([vp], None),
@@ -76,6 +85,16 @@ def load(path: str = LIB_PATH):
         "pkv_plan_dense": ([vp, i32p, i32p, i, i, i, ctypes.c_float, vp, ctypes.c_size_t, vp], i),
         "pkv_run_dense": ([vp, vp, vp, vp, vp, vp, vp, vp], i),
         "pkv_gather_kv": ([vp, vp, vp, i, vp, vp, vp], i),
+        "pkv_latent_create": ([ctypes.POINTER(LatentConfig), ctypes.POINTER(vp)], i),
+        "pkv_latent_destroy": ([vp], None),
+        "pkv_latent_last_error": ([vp], ctypes.c_char_p),
+        "pkv_latent_workspace_size": ([vp, i, ctypes.POINTER(ctypes.c_size_t)], i),
+        "pkv_latent_plan": ([vp, i32p, i32p, i32p, i32p, i, i, i, ctypes.c_float, vp, ctypes.c_size_t, vp], i),
+        "pkv_latent_append_planned": ([vp, vp, i64, vp, i64, vp, vp, vp], i),
+        "pkv_latent_run": ([vp, vp, vp, vp, vp, vp, vp], i),
+        "pkv_latent_plan_dense": ([vp, i32p, i32p, i, i, i, ctypes.c_float, vp, ctypes.c_size_t, vp], i),
+        "pkv_latent_run_dense": ([vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp], i),
+        "pkv_latent_check_device_error": ([vp, vp, vp, ctypes.POINTER(i)], i),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -107,6 +126,25 @@ def _stream(stream):
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _check_tensor(name, t, dtype, shape, contiguous=True):
+    """The operators that take tensors' shapes on trust in C check them here: type, shape (None = any
+    size), device (the current one) and layout."""
+    import torch
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _stride(t, dim, least):
+    """Stride of one dimension in elements; of a dimension of one entry, which is never stepped, the least."""
+    return t.stride(dim) if t.shape[dim] > 1 else least
 
 
 class Handle:
@@ -233,6 +271,120 @@ class Handle:
         self._check(self.lib.pkv_decode_head_rows(self.h, _p(kvp), _p(kvi), _p(lpl), batch, int(window_left),
                                                   _p(rows), ctypes.byref(nc)))
         return rows[: 4 * nc.value].reshape(-1, 4)
+
+
+class LatentHandle:
+    """Latent attention (pkv_latent_*): keys and values from one vector [latent | rope] per token.  The
+    absorbed form runs over a paged cache [pages, page_size, 576]; the expanded form over contiguous
+    per-head keys and values (see include/pkv.h)."""
+
+    LATENT, ROPE, NOPE, V = 512, 64, 128, 128
+
+    def __init__(self, *, num_heads, page_size, max_batch, max_total_tokens, max_num_pages, num_cache_pages,
+                 latent_dim=512, rope_dim=64, nope_dim=128, v_dim=128, sm_count=0, enable_nvtx=False):
+        self.lib = load()
+        self.cfg = LatentConfig(num_heads, latent_dim, rope_dim, nope_dim, v_dim, page_size, max_batch,
+                                max_total_tokens, max_num_pages, num_cache_pages, sm_count, int(enable_nvtx))
+        h = ctypes.c_void_p()
+        st = self.lib.pkv_latent_create(ctypes.byref(self.cfg), ctypes.byref(h))
+        if st != OK:
+            raise PkvError(st, self.lib.pkv_latent_last_error(None).decode())
+        self.h = h
+        self._tokens = self._keys = 0
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.lib.pkv_latent_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _check(self, st):
+        if st != OK:
+            raise PkvError(st, self.lib.pkv_latent_last_error(self.h).decode())
+
+    def workspace_size(self, mode: int) -> int:
+        """mode: MODE_PREFILL for plan(), MODE_DENSE for plan_dense()."""
+        n = ctypes.c_size_t()
+        self._check(self.lib.pkv_latent_workspace_size(self.h, mode, ctypes.byref(n)))
+        return n.value
+
+    def plan(self, qo_indptr, kv_indptr, kv_indices, last_page_len, *, workspace, sm_scale, causal=True,
+             window_left=-1, stream=None):
+        """qo_indptr None: one new token per row."""
+        arrs = [_i32(qo_indptr), _i32(kv_indptr), _i32(kv_indices), _i32(last_page_len)]
+        batch = len(arrs[1]) - 1
+        self._check(self.lib.pkv_latent_plan(self.h, *(_p(a) for a in arrs), batch, int(bool(causal)), int(window_left),
+                                             float(sm_scale), _dptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _stream(stream)))
+        self._tokens = batch if arrs[0] is None else int(arrs[0][-1])
+
+    def append_planned(self, c_new, rope_new, cache_layer, *, workspace, stream=None):
+        """The step's new vectors into their slots: c_new [T, 512] and rope_new [T, 64], rows may be strided."""
+        import torch
+        _check_tensor("c_new", c_new, torch.bfloat16, (self._tokens, self.LATENT), contiguous=False)
+        _check_tensor("rope_new", rope_new, torch.bfloat16, (self._tokens, self.ROPE), contiguous=False)
+        self._check_cache(cache_layer)
+        if c_new.stride(1) != 1 or rope_new.stride(1) != 1:
+            raise ValueError("c_new and rope_new must have unit stride in their last dimension")
+        self._check(self.lib.pkv_latent_append_planned(
+            self.h, _dptr(c_new), _stride(c_new, 0, self.LATENT), _dptr(rope_new), _stride(rope_new, 0, self.ROPE),
+            _dptr(cache_layer), _dptr(workspace), _stream(stream)))
+
+    def _check_cache(self, cache_layer):
+        import torch
+        _check_tensor("cache_layer", cache_layer, torch.bfloat16,
+                      (self.cfg.num_cache_pages, self.cfg.page_size, self.LATENT + self.ROPE))
+
+    def _check_out(self, out, lse, width):
+        import torch
+        _check_tensor("out", out, torch.bfloat16, (self._tokens, self.cfg.num_heads, width))
+        if lse is not None:
+            _check_tensor("lse", lse, torch.float32, (self._tokens, self.cfg.num_heads))
+
+    def run(self, q, cache_layer, out, lse=None, *, workspace, stream=None):
+        """Absorbed form: q [T, heads, 576], out [T, heads, 512], lse [T, heads]."""
+        import torch
+        _check_tensor("q", q, torch.bfloat16, (self._tokens, self.cfg.num_heads, self.LATENT + self.ROPE))
+        self._check_cache(cache_layer)
+        self._check_out(out, lse, self.LATENT)
+        self._check(self.lib.pkv_latent_run(self.h, _dptr(q), _dptr(cache_layer), _dptr(out), _dptr(lse),
+                                            _dptr(workspace), _stream(stream)))
+
+    def plan_dense(self, cu_q, cu_k, *, workspace, sm_scale, causal=True, window_left=-1, stream=None):
+        cq, ck = _i32(cu_q), _i32(cu_k)
+        self._check(self.lib.pkv_latent_plan_dense(self.h, _p(cq), _p(ck), len(cq) - 1, int(bool(causal)),
+                                                   int(window_left), float(sm_scale), _dptr(workspace),
+                                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+        self._tokens, self._keys = int(cq[-1]), int(ck[-1])
+
+    def run_dense(self, q, k_nope, k_rope, v, out, lse=None, *, workspace, stream=None):
+        """Expanded form: q [T, heads, 192], k_nope and v [keys, heads, 128], k_rope [keys, 64] (these three
+        with any token and head strides), out [T, heads, 128], lse [T, heads]."""
+        import torch
+        bf, H = torch.bfloat16, self.cfg.num_heads
+        _check_tensor("q", q, bf, (self._tokens, H, self.NOPE + self.ROPE))
+        _check_tensor("k_nope", k_nope, bf, (self._keys, H, self.NOPE), contiguous=False)
+        _check_tensor("k_rope", k_rope, bf, (self._keys, self.ROPE), contiguous=False)
+        _check_tensor("v", v, bf, (self._keys, H, self.V), contiguous=False)
+        if k_nope.stride(2) != 1 or k_rope.stride(1) != 1 or v.stride(2) != 1:
+            raise ValueError("k_nope, k_rope and v must have unit stride in their last dimension")
+        self._check_out(out, lse, self.V)
+        self._check(self.lib.pkv_latent_run_dense(
+            self.h, _dptr(q), _dptr(k_nope), _stride(k_nope, 0, self.NOPE), _stride(k_nope, 1, self.NOPE), _dptr(k_rope),
+            _stride(k_rope, 0, self.ROPE), _dptr(v), _stride(v, 0, self.V), _stride(v, 1, self.V), _dptr(out), _dptr(lse),
+            _dptr(workspace), _stream(stream)))
+
+    def check_device_error(self, workspace, stream=None) -> int:
+        code = ctypes.c_int()
+        st = self.lib.pkv_latent_check_device_error(self.h, _dptr(workspace), _stream(stream), ctypes.byref(code))
+        if st not in (OK, ERR_DEVICE):
+            self._check(st)
+        return code.value
 
 
 def append_slots(page_size, qo_indptr, kv_indptr, kv_indices, last_page_len):

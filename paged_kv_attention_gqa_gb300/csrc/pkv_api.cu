@@ -2,7 +2,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cmath>
@@ -12,48 +11,12 @@
 #include <string>
 
 #include "../../include/pkv.h"
+#include "handle.h"
 #include "launch.h"
 #include "plan.h"
 
 using pkv::Plan;
 using pkv::Shape;
-
-struct pkv_handle_s {
-    Shape shape{};
-    std::string err;
-    Plan plan;
-    // the image buffer of the previous plan, handed to the next one so that building its
-    // image reuses memory already mapped (the staged plan keeps no image)
-    std::vector<uint8_t> spare_image;
-    void *planned_ws = nullptr;
-    // Page-locked staging ring (PinnedIndexRing: depth 2; a set is rewritten only after
-    // the copy out of it has completed, fenced by an event recorded after that copy).
-    void *pinned[2] = {nullptr, nullptr};
-    size_t pinned_bytes[2] = {0, 0};
-    cudaEvent_t fence[2] = {nullptr, nullptr};
-    bool fence_live[2] = {false, false};
-    int ring_at = 0;
-    // side stream + fork/join events of the mixed step's concurrent passes
-    cudaStream_t side = nullptr;
-    cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
-    // last encoded tensor maps (re-encoded when the layer pointer changes)
-    const void *tm_dec_ptr = nullptr, *tm_pf_ptr = nullptr, *tm_q_ptr = nullptr;
-    int tm_q_rows = -1;
-    CUtensorMap tm_dec{}, tm_pf{}, tm_q{};
-    bool nvtx = false;  // one NVTX range per call (pkv_config.enable_nvtx)
-};
-
-// The NVTX range of one call on a handle with enable_nvtx set: opened here, closed when
-// the call returns.
-struct NvtxCall {
-    bool on;
-    NvtxCall(const pkv_handle_s *h, const char *name) : on(h && h->nvtx) {
-        if (on) nvtxRangePushA(name);
-    }
-    ~NvtxCall() {
-        if (on) nvtxRangePop();
-    }
-};
 
 static thread_local std::string g_create_err;
 
@@ -112,13 +75,7 @@ extern "C" pkv_status pkv_create(const pkv_config *cfg, pkv_handle_t *out) {
 
 extern "C" void pkv_destroy(pkv_handle_t h) {
     if (!h) return;
-    for (int i = 0; i < 2; ++i) {
-        if (h->fence[i]) {
-            if (h->fence_live[i]) cudaEventSynchronize(h->fence[i]);
-            cudaEventDestroy(h->fence[i]);
-        }
-        if (h->pinned[i]) cudaFreeHost(h->pinned[i]);
-    }
+    h->staging.release();
     if (h->side) {
         cudaStreamSynchronize(h->side);
         cudaStreamDestroy(h->side);
@@ -137,6 +94,53 @@ extern "C" pkv_status pkv_workspace_size(pkv_handle_t h, int mode, size_t *bytes
     return PKV_OK;
 }
 
+cudaError_t PkvStaging::copy(const void *image, size_t nbytes, void *workspace, cudaStream_t st, const char **what) {
+    const int set = ring_at;
+    ring_at ^= 1;
+    cudaError_t e;
+    if (!fence[set]) {
+        *what = "event create";
+        e = cudaEventCreateWithFlags(&fence[set], cudaEventDisableTiming);
+        if (e != cudaSuccess) return e;
+    }
+    if (fence_live[set]) {
+        // the copy that last read this set must have completed before we rewrite it
+        *what = "staging fence";
+        e = cudaEventSynchronize(fence[set]);
+        if (e != cudaSuccess) return e;
+        fence_live[set] = false;
+    }
+    if (pinned_bytes[set] < nbytes) {
+        if (pinned[set]) cudaFreeHost(pinned[set]);
+        pinned[set] = nullptr;
+        pinned_bytes[set] = 0;
+        const size_t want = pkv::align_up(nbytes > (1u << 20) ? nbytes : (1u << 20), 1u << 20);
+        *what = "pinned staging alloc";
+        e = cudaHostAlloc(&pinned[set], want, cudaHostAllocDefault);
+        if (e != cudaSuccess) return e;
+        pinned_bytes[set] = want;
+    }
+    std::memcpy(pinned[set], image, nbytes);
+    *what = "plan H2D";
+    e = cudaMemcpyAsync(workspace, pinned[set], nbytes, cudaMemcpyHostToDevice, st);
+    if (e != cudaSuccess) return e;
+    *what = "staging fence record";
+    e = cudaEventRecord(fence[set], st);
+    if (e != cudaSuccess) return e;
+    fence_live[set] = true;
+    return cudaSuccess;
+}
+
+void PkvStaging::release() {
+    for (int i = 0; i < 2; ++i) {
+        if (fence[i]) {
+            if (fence_live[i]) cudaEventSynchronize(fence[i]);
+            cudaEventDestroy(fence[i]);
+        }
+        if (pinned[i]) cudaFreeHost(pinned[i]);
+    }
+}
+
 // Copy a plan's integer image into the workspace through the page-locked ring (one
 // async H2D) and make it the handle's current plan.
 static pkv_status stage_plan(pkv_handle_t h, Plan &plan, void *workspace, size_t workspace_bytes,
@@ -146,36 +150,10 @@ static pkv_status stage_plan(pkv_handle_t h, Plan &plan, void *workspace, size_t
                     "workspace of " + std::to_string(workspace_bytes) + " bytes is too small: this plan needs " +
                         std::to_string(plan.lay.total) + " bytes (pkv_workspace_size gives the bound at the maxima)");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int set = h->ring_at;
-    h->ring_at ^= 1;
-    cudaError_t e;
-    if (!h->fence[set]) {
-        e = cudaEventCreateWithFlags(&h->fence[set], cudaEventDisableTiming);
-        if (e != cudaSuccess) return cuda_fail(h, e, "event create");
-    }
-    if (h->fence_live[set]) {
-        // the copy that last read this set must have completed before we rewrite it
-        e = cudaEventSynchronize(h->fence[set]);
-        if (e != cudaSuccess) return cuda_fail(h, e, "staging fence");
-        h->fence_live[set] = false;
-    }
-    const size_t nbytes = plan.image.size();
-    if (h->pinned_bytes[set] < nbytes) {
-        if (h->pinned[set]) cudaFreeHost(h->pinned[set]);
-        h->pinned[set] = nullptr;
-        h->pinned_bytes[set] = 0;
-        const size_t want = pkv::align_up(nbytes > (1u << 20) ? nbytes : (1u << 20), 1u << 20);
-        e = cudaHostAlloc(&h->pinned[set], want, cudaHostAllocDefault);
-        if (e != cudaSuccess) return cuda_fail(h, e, "pinned staging alloc");
-        h->pinned_bytes[set] = want;
-    }
-    std::memcpy(h->pinned[set], plan.image.data(), nbytes);
+    const char *what = "";
+    const cudaError_t e = h->staging.copy(plan.image.data(), plan.image.size(), workspace, st, &what);
+    if (e != cudaSuccess) return cuda_fail(h, e, what);
     h->spare_image.swap(plan.image);
-    e = cudaMemcpyAsync(workspace, h->pinned[set], nbytes, cudaMemcpyHostToDevice, st);
-    if (e != cudaSuccess) return cuda_fail(h, e, "plan H2D");
-    e = cudaEventRecord(h->fence[set], st);
-    if (e != cudaSuccess) return cuda_fail(h, e, "staging fence record");
-    h->fence_live[set] = true;
     h->plan = std::move(plan);
     h->planned_ws = workspace;
     return PKV_OK;
@@ -206,7 +184,7 @@ extern "C" pkv_status pkv_plan(pkv_handle_t h, int mode, const int32_t *qo_indpt
     return stage_plan(h, plan, workspace, workspace_bytes, stream);
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 pkv::encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -236,7 +214,7 @@ static pkv_status encode_kv(pkv_handle_t h, const void *kv_layer, int box_rows, 
 // rows, box_heads heads), heads outermost so that one head's rows land contiguously.
 static pkv_status encode_rows(pkv_handle_t h, const void *kv_layer, long long rows, int box_rows, int box_heads,
                               CUtensorMap *tm) {
-    auto fn = encode_fn();
+    auto fn = pkv::encode_fn();
     if (!fn) return fail(h, PKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const Shape &s = h->shape;
     if (reinterpret_cast<uintptr_t>(kv_layer) % 16) return fail(h, PKV_ERR_INVALID, "kv_layer must be 16-byte aligned");
@@ -256,7 +234,7 @@ static pkv_status encode_rows(pkv_handle_t h, const void *kv_layer, long long ro
 // tokens) lands as 128 query rows (token-major, head-minor) of 128 bytes, 128-byte swizzled.
 static pkv_status q_map(pkv_handle_t h, const void *q, int rows) {
     if (h->tm_q_ptr == q && h->tm_q_rows == rows) return PKV_OK;
-    auto fn = encode_fn();
+    auto fn = pkv::encode_fn();
     if (!fn) return fail(h, PKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const Shape &s = h->shape;
     const int g = s.group();
