@@ -69,7 +69,8 @@ typedef enum {
     PKV_ERR_DEVICE = 7                 /* a kernel recorded a device-side error (wait limit hit) */
 } pkv_status;
 
-enum { PKV_MODE_DECODE = 0, PKV_MODE_PREFILL = 1, PKV_MODE_MIXED = 2, PKV_MODE_DENSE = 3 };
+enum { PKV_MODE_DECODE = 0, PKV_MODE_PREFILL = 1, PKV_MODE_MIXED = 2, PKV_MODE_DENSE = 3,
+       PKV_MODE_EVICT = 4, PKV_MODE_DECODE_WEIGHTS = 5, PKV_MODE_WEIGHTS = 6 };
 enum { PKV_NON_CAUSAL = 0, PKV_CAUSAL = 1, PKV_CONTEXT_ONLY = 2 };
 
 /*
@@ -317,6 +318,58 @@ pkv_status pkv_run_decode_static(pkv_handle_t h, const void *q, const void *kv_l
                                  const int32_t *paged_kv_indptr, const int32_t *paged_kv_indices,
                                  const int32_t *paged_kv_last_page_len, int batch, int window_left, float sm_scale,
                                  pkv_stream_t stream);
+
+/* ---- eviction by accumulated attention weight ---- */
+
+/*
+ * A score per cache slot, `scores` fp32 [num_cache_pages, page_size] (device, one slice per layer
+ * beside the layer's K/V), adds up the softmax weights that the slot's key received, summed over
+ * the query heads.  A step sets, for every position j of every row,
+ *   scores[slot of j] = (j is one of the step's new tokens, j >= L - n ? 0 : decay * old)
+ *                       + sum over the row's queries and heads of exp(sm_scale q k_j - lse),
+ * a key that a query does not see adding nothing.  decay: finite, >= 0; at 0 the old score is not
+ * read.  Slots that hold none of the rows' tokens are left alone.  No page may be listed twice
+ * (PKV_ERR_INVALID: its slots have one score).  The sums are made in a fixed order: the same
+ * call gives the same bits.  Not on graph_static handles (PKV_ERR_UNSUPPORTED).
+ *
+ * pkv_run_decode_weights: pkv_run_decode of a PKV_MODE_DECODE_WEIGHTS plan (pkv_plan; as a decode
+ * plan, with workspace for the step's logits) that also updates the scores; lse is required.
+ * pkv_kv_append_planned takes such a plan too.
+ */
+pkv_status pkv_run_decode_weights(pkv_handle_t h, const void *q, const void *kv_layer, void *out, float *lse,
+                                  float *scores, float decay, void *workspace, pkv_stream_t stream);
+/*
+ * The same update for rows of any number of query tokens whose lse is known (pkv_run_prefill): a
+ * whole prompt, or its last n tokens as the observers of all of it.  The plan is
+ * pkv_plan(PKV_MODE_WEIGHTS, qo_indptr, ...) with the causal (0 or 1), window_left and sm_scale of
+ * the attention that made the lse; q device bf16 [T, Hq, D], lse device fp32 [T, Hq].  Reads K
+ * alone.  page_size 8 or more (else PKV_ERR_UNSUPPORTED).
+ */
+pkv_status pkv_run_weights(pkv_handle_t h, const void *q, const float *lse, const void *kv_layer, float *scores,
+                           float decay, void *workspace, pkv_stream_t stream);
+/*
+ * Plan an eviction: row r keeps keep[r] tokens if it has more (L_r > keep[r] >= num_sink +
+ * num_recent), else it is left alone.  Kept are its first num_sink and last num_recent tokens and,
+ * of those between, the ones with the highest scores (of equal scores the lowest position; NaN
+ * ranks below every number).  They are gathered in position order into new pages: dst_indptr
+ * [batch + 1] and dst_indices list, row by row, ceil(keep[r] / page_size) page ids for every row
+ * that is cut (none for the others), all different and no page of any row of the plan.  The old
+ * pages are not written, so rows may share them (a common prefix); after the run the caller
+ * replaces the row's page list by the new one (length keep[r]) and frees the old pages.  All
+ * arrays are HOST int32.  Makes the handle's current plan, as pkv_plan does.
+ */
+pkv_status pkv_plan_evict(pkv_handle_t h, const int32_t *paged_kv_indptr, const int32_t *paged_kv_indices,
+                          const int32_t *paged_kv_last_page_len, int batch, const int32_t *keep, int num_sink,
+                          int num_recent, const int32_t *dst_indptr, const int32_t *dst_indices, void *workspace,
+                          size_t workspace_bytes, pkv_stream_t stream);
+/*
+ * Run it on one layer: K, V and scores of the kept tokens are copied to the new pages, and
+ * kept (device int32, sum over the rows of min(keep[r], L_r) entries, row after row) receives
+ * their positions in ascending order (0 .. L_r - 1 for a row left alone).  Every layer
+ * chooses by its own scores.
+ */
+pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t *kept, void *workspace,
+                         pkv_stream_t stream);
 
 /* ---- latent attention ---- */
 

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libpkv.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_TOO_MANY_PREFILL_ROWS, ERR_NOT_PLANNED, ERR_CUDA, ERR_DEVICE = range(8)
 MODE_DECODE, MODE_PREFILL, MODE_MIXED, MODE_DENSE = 0, 1, 2, 3
+MODE_EVICT, MODE_DECODE_WEIGHTS, MODE_WEIGHTS = 4, 5, 6
 NON_CAUSAL, CAUSAL, CONTEXT_ONLY = 0, 1, 2
 STATUS_NAMES = ["OK", "INVALID", "UNSUPPORTED", "WORKSPACE", "TOO_MANY_PREFILL_ROWS", "NOT_PLANNED", "CUDA", "DEVICE"]
 
@@ -25,7 +26,7 @@ EXPORTS = ["pkv_create", "pkv_destroy", "pkv_last_error", "pkv_workspace_size", 
            "pkv_run_decode", "pkv_run_prefill", "pkv_run_mixed", "pkv_check_device_error", "pkv_append_slots",
            "pkv_mixed_layout", "pkv_decode_split", "pkv_decode_head_rows", "pkv_run_decode_static", "pkv_context_only_views",
            "pkv_plan_dense", "pkv_run_dense", "pkv_gather_kv", "pkv_run_decode_append", "pkv_selftest_wait_timeout",
-           "pkv_latent_create", "pkv_latent_destroy", "pkv_latent_last_error", "pkv_latent_workspace_size",
+           "pkv_run_decode_weights", "pkv_run_weights", "pkv_plan_evict", "pkv_run_evict", "pkv_latent_create", "pkv_latent_destroy", "pkv_latent_last_error", "pkv_latent_workspace_size",
            "pkv_latent_plan", "pkv_latent_append_planned", "pkv_latent_run", "pkv_latent_plan_dense",
            "pkv_latent_run_dense", "pkv_latent_check_device_error"]
 
@@ -85,6 +86,10 @@ def load(path: str = LIB_PATH):
         "pkv_plan_dense": ([vp, i32p, i32p, i, i, i, ctypes.c_float, vp, ctypes.c_size_t, vp], i),
         "pkv_run_dense": ([vp, vp, vp, vp, vp, vp, vp, vp], i),
         "pkv_gather_kv": ([vp, vp, vp, i, vp, vp, vp], i),
+        "pkv_run_decode_weights": ([vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp], i),
+        "pkv_run_weights": ([vp, vp, vp, vp, vp, ctypes.c_float, vp, vp], i),
+        "pkv_plan_evict": ([vp, i32p, i32p, i32p, i, i32p, i, i, i32p, i32p, vp, ctypes.c_size_t, vp], i),
+        "pkv_run_evict": ([vp, vp, vp, vp, vp, vp], i),
         "pkv_latent_create": ([ctypes.POINTER(LatentConfig), ctypes.POINTER(vp)], i),
         "pkv_latent_destroy": ([vp], None),
         "pkv_latent_last_error": ([vp], ctypes.c_char_p),
@@ -163,6 +168,7 @@ class Handle:
             raise PkvError(st, self.lib.pkv_last_error(None).decode())
         self.h = h
         self._keep = []
+        self._planned_tokens = self._kept = 0
 
     def close(self):
         if getattr(self, "h", None):
@@ -194,6 +200,7 @@ class Handle:
                                float(sm_scale), _dptr(workspace), workspace.numel() * workspace.element_size(),
                                _stream(stream))
         self._check(st)
+        self._planned_tokens = batch if arrs[0] is None else int(arrs[0][-1])
 
     def kv_append(self, k, v, num_new_tokens, kv_layer, qo_indptr, kv_indptr, kv_indices, last_page_len, batch,
                   stream=None):
@@ -234,6 +241,59 @@ class Handle:
     def run_dense(self, q, k, v, out, lse=None, *, workspace, stream=None):
         self._check(self.lib.pkv_run_dense(self.h, _dptr(q), _dptr(k), _dptr(v), _dptr(out), _dptr(lse),
                                            _dptr(workspace), _stream(stream)))
+
+    def _check_layer(self, kv_layer, scores):
+        import torch
+        c = self.cfg
+        _check_tensor("kv_layer", kv_layer, torch.bfloat16,
+                      (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim))
+        _check_tensor("scores", scores, torch.float32, (c.num_cache_pages, c.page_size))
+
+    def _check_q(self, q, lse):
+        import torch
+        tokens = self._planned_tokens
+        _check_tensor("q", q, torch.bfloat16, (tokens, self.cfg.num_qo_heads, self.cfg.head_dim))
+        _check_tensor("lse", lse, torch.float32, (tokens, self.cfg.num_qo_heads))
+
+    def run_decode_weights(self, q, kv_layer, out, lse, scores, *, decay=1.0, workspace, stream=None):
+        """run_decode of a MODE_DECODE_WEIGHTS plan that also adds every key's softmax weight, summed over
+        the query heads, into scores [pages, page_size] (fp32): decay * old + new, the row's newest
+        token from nothing."""
+        self._check_layer(kv_layer, scores)
+        self._check_q(q, lse)
+        _check_tensor("out", out, q.dtype, tuple(q.shape))
+        self._check(self.lib.pkv_run_decode_weights(self.h, _dptr(q), _dptr(kv_layer), _dptr(out), _dptr(lse),
+                                                    _dptr(scores), float(decay), _dptr(workspace), _stream(stream)))
+
+    def run_weights(self, q, lse, kv_layer, scores, *, decay=1.0, workspace, stream=None):
+        """The same scores from the queries and the lse of a prefill (MODE_WEIGHTS plans)."""
+        self._check_layer(kv_layer, scores)
+        self._check_q(q, lse)
+        self._check(self.lib.pkv_run_weights(self.h, _dptr(q), _dptr(lse), _dptr(kv_layer), _dptr(scores), float(decay),
+                                             _dptr(workspace), _stream(stream)))
+
+    def plan_evict(self, kv_indptr, kv_indices, last_page_len, keep, dst_indptr, dst_indices, *, num_sink=0,
+                   num_recent=0, workspace, stream=None):
+        """Row r keeps keep[r] tokens if it has more: the first num_sink, the last num_recent and the
+        best-scored between; they move to the new pages dst_indices[dst_indptr[r]:dst_indptr[r + 1]]."""
+        a = [_i32(x) for x in (kv_indptr, kv_indices, last_page_len, keep, dst_indptr, dst_indices)]
+        batch = len(a[0]) - 1
+        if len(a[3]) != batch or len(a[4]) != batch + 1:
+            raise ValueError("keep has one entry per row, dst_indptr one more")
+        self._check(self.lib.pkv_plan_evict(self.h, _p(a[0]), _p(a[1]), _p(a[2]), batch, _p(a[3]), int(num_sink),
+                                            int(num_recent), _p(a[4]), _p(a[5]), _dptr(workspace),
+                                            workspace.numel() * workspace.element_size(), _stream(stream)))
+        pages = np.diff(a[0])
+        lens = np.where(pages > 0, (pages - 1) * self.cfg.page_size + a[2], 0)
+        self._kept = int(np.minimum(lens, a[3]).sum())
+
+    def run_evict(self, kv_layer, scores, kept, *, workspace, stream=None):
+        """Move the kept tokens of one layer; kept (int32) receives their positions, row after row."""
+        import torch
+        self._check_layer(kv_layer, scores)
+        _check_tensor("kept", kept, torch.int32, (self._kept,))
+        self._check(self.lib.pkv_run_evict(self.h, _dptr(kv_layer), _dptr(scores), _dptr(kept), _dptr(workspace),
+                                           _stream(stream)))
 
     def gather_kv(self, kv_layer, pages, num_tokens, k_out, v_out, stream=None):
         """pages: a device int32 tensor of page ids."""

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "../../include/pkv.h"
+#include "evict.h"
 #include "plan.h"
 
 // Page-locked staging ring (PinnedIndexRing: depth 2; a set is rewritten only after
@@ -32,6 +33,8 @@ struct pkv_handle_s {
     // the image buffer of the previous plan, handed to the next one so that building its
     // image reuses memory already mapped (the staged plan keeps no image)
     std::vector<uint8_t> spare_image;
+    pkv::WeightsPlan weights;  // the score arrays of DECODE_WEIGHTS / WEIGHTS plans
+    pkv::EvictPlan evict;      // EVICT plans
     void *planned_ws = nullptr;
     PkvStaging staging;
     // side stream + fork/join events of the mixed step's concurrent passes

@@ -89,8 +89,8 @@ extern "C" const char *pkv_last_error(pkv_handle_t h) { return h ? h->err.c_str(
 
 extern "C" pkv_status pkv_workspace_size(pkv_handle_t h, int mode, size_t *bytes) {
     if (!h || !bytes) return fail(h, PKV_ERR_INVALID, "null argument");
-    if (mode < PKV_MODE_DECODE || mode > PKV_MODE_DENSE) return fail(h, PKV_ERR_INVALID, "unknown mode");
-    *bytes = pkv::workspace_bound(h->shape, mode);
+    if (mode < PKV_MODE_DECODE || mode > PKV_MODE_WEIGHTS) return fail(h, PKV_ERR_INVALID, "unknown mode");
+    *bytes = mode >= PKV_MODE_EVICT ? pkv::evict_workspace_bound(h->shape, mode) : pkv::workspace_bound(h->shape, mode);
     return PKV_OK;
 }
 
@@ -174,9 +174,20 @@ extern "C" pkv_status pkv_plan(pkv_handle_t h, int mode, const int32_t *qo_indpt
     std::string err;
     Plan plan;
     plan.image.swap(h->spare_image);
-    int rc = pkv::make_plan(h->shape, mode, qo_indptr, kv_indptr, kv_indices, last_page_len, batch, causal,
-                            window_left, sm_scale, plan, err);
+    pkv::WeightsPlan weights;
+    int rc = 0;
+    try {
+        rc = mode == PKV_MODE_DECODE_WEIGHTS || mode == PKV_MODE_WEIGHTS
+                 ? pkv::make_weights_plan(h->shape, mode, qo_indptr, kv_indptr, kv_indices, last_page_len, batch, causal,
+                                          window_left, sm_scale, plan, weights, err)
+                 : pkv::make_plan(h->shape, mode, qo_indptr, kv_indptr, kv_indices, last_page_len, batch, causal,
+                                  window_left, sm_scale, plan, err);
+    } catch (const std::exception &ex) {  // no C++ exception crosses the C boundary
+        rc = PKV_ERR_INVALID;
+        err = ex.what();
+    }
     h->planned_ws = nullptr;
+    h->weights = weights;
     if (rc) {
         h->spare_image.swap(plan.image);
         return fail(h, (pkv_status)rc, err);
@@ -232,20 +243,25 @@ static pkv_status encode_rows(pkv_handle_t h, const void *kv_layer, long long ro
 
 // Tensor map over q viewed as [tokens][Hq][D]: a box of (64 columns, g heads, 128 / g
 // tokens) lands as 128 query rows (token-major, head-minor) of 128 bytes, 128-byte swizzled.
-static pkv_status q_map(pkv_handle_t h, const void *q, int rows) {
-    if (h->tm_q_ptr == q && h->tm_q_rows == rows) return PKV_OK;
+static pkv_status encode_q(pkv_handle_t h, const void *q, int rows, int box_tokens, CUtensorMap *tm) {
     auto fn = pkv::encode_fn();
     if (!fn) return fail(h, PKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const Shape &s = h->shape;
-    const int g = s.group();
     cuuint64_t dims[3] = {(cuuint64_t)s.head_dim, (cuuint64_t)s.num_qo_heads, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)s.head_dim * 2, (cuuint64_t)s.num_qo_heads * s.head_dim * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(pkv::kPrefillRowsPerTile / g)};
+    cuuint32_t box[3] = {64, (cuuint32_t)s.group(), (cuuint32_t)box_tokens};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(&h->tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+    CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(h, PKV_ERR_CUDA, "cuTensorMapEncodeTiled (q) failed (" + std::to_string((int)r) + ")");
+    return PKV_OK;
+}
+
+static pkv_status q_map(pkv_handle_t h, const void *q, int rows) {
+    if (h->tm_q_ptr == q && h->tm_q_rows == rows) return PKV_OK;
+    const pkv_status st = encode_q(h, q, rows, pkv::kPrefillRowsPerTile / h->shape.group(), &h->tm_q);
+    if (st != PKV_OK) return st;
     h->tm_q_ptr = q;
     h->tm_q_rows = rows;
     return PKV_OK;
@@ -307,7 +323,9 @@ extern "C" pkv_status pkv_kv_append_planned(pkv_handle_t h, const void *k, const
                                             void *workspace, pkv_stream_t stream) {
     NvtxCall nvtx_range(h, "pkv_kv_append_planned");
     pkv_status st = check_planned(h, workspace, PKV_MODE_DECODE, PKV_MODE_PREFILL);
-    if (st != PKV_OK && h && h->plan.mode == PKV_MODE_MIXED && h->planned_ws == workspace) st = PKV_OK;
+    if (st != PKV_OK && h && (h->plan.mode == PKV_MODE_MIXED || h->plan.mode == PKV_MODE_DECODE_WEIGHTS) &&
+        h->planned_ws == workspace)
+        st = PKV_OK;
     if (st != PKV_OK) return st;
     if (h->plan.num_append && (!k || !v || !kv_layer)) return fail(h, PKV_ERR_INVALID, "null k, v or kv_layer");
     if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(kv_layer)) % 16)
@@ -623,4 +641,102 @@ extern "C" pkv_status pkv_gather_kv(pkv_handle_t h, const void *kv_layer, const 
     cudaError_t e = pkv::launch_gather(h->shape, kv_layer, pages, num_tokens, k_out, v_out,
                                        static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(h, e, "gather launch");
+}
+
+// ---------------- eviction by accumulated attention weight ----------------
+
+static pkv_status check_scores(pkv_handle_t h, const float *scores, float decay) {
+    if (!scores) return fail(h, PKV_ERR_INVALID, "null scores");
+    if (reinterpret_cast<uintptr_t>(scores) % 4) return fail(h, PKV_ERR_INVALID, "scores must be 4-byte aligned");
+    if (!(decay >= 0.f) || std::isinf(decay)) return fail(h, PKV_ERR_INVALID, "decay must be finite and >= 0");
+    return PKV_OK;
+}
+
+extern "C" pkv_status pkv_run_decode_weights(pkv_handle_t h, const void *q, const void *kv_layer, void *out, float *lse,
+                                             float *scores, float decay, void *workspace, pkv_stream_t stream) {
+    NvtxCall nvtx_range(h, "pkv_run_decode_weights");
+    pkv_status st = check_planned(h, workspace, PKV_MODE_DECODE_WEIGHTS);
+    if (st != PKV_OK) return st;
+    if (h->plan.batch == 0) return PKV_OK;
+    if ((st = check_io(h, q, kv_layer, out)) != PKV_OK || (st = check_scores(h, scores, decay)) != PKV_OK) return st;
+    if (!lse || reinterpret_cast<uintptr_t>(lse) % 4) return fail(h, PKV_ERR_INVALID, "lse is required, 4-byte aligned");
+    if ((st = dec_map(h, kv_layer)) != PKV_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = pkv::launch_decode_weights(h->shape, h->plan, h->weights, h->tm_dec, workspace, q,
+                                               const_cast<void *>(kv_layer), out, lse, s);
+    if (e != cudaSuccess) return cuda_fail(h, e, "decode launch");
+    e = pkv::launch_decode_scores(h->shape, h->plan, h->weights, workspace, lse, scores, decay, s);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(h, e, "score launch");
+}
+
+extern "C" pkv_status pkv_run_weights(pkv_handle_t h, const void *q, const float *lse, const void *kv_layer,
+                                      float *scores, float decay, void *workspace, pkv_stream_t stream) {
+    NvtxCall nvtx_range(h, "pkv_run_weights");
+    pkv_status st = check_planned(h, workspace, PKV_MODE_WEIGHTS);
+    if (st != PKV_OK) return st;
+    if (h->weights.tiles == 0) return PKV_OK;
+    if ((st = check_scores(h, scores, decay)) != PKV_OK) return st;
+    const int T = h->plan.num_tokens;
+    if (T > 0 && (!q || !lse || !kv_layer)) return fail(h, PKV_ERR_INVALID, "null q, lse or kv_layer");
+    if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(lse) % 4)
+        return fail(h, PKV_ERR_INVALID, "q must be 16-byte aligned, lse 4-byte");
+    CUtensorMap tk{}, tq{};
+    if (T > 0) {
+        const Shape &s = h->shape;
+        const int box = s.page_size < pkv::kWeightKeys ? s.page_size : pkv::kWeightKeys;
+        if ((st = encode_kv(h, kv_layer, box, 1, &tk)) != PKV_OK) return st;
+        if ((st = encode_q(h, q, T, h->weights.box_tokens, &tq)) != PKV_OK) return st;
+    }
+    cudaError_t e = pkv::launch_weights(h->shape, h->plan, h->weights, tk, tq, workspace, lse, scores, decay,
+                                        static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(h, e, "weights launch");
+}
+
+extern "C" pkv_status pkv_plan_evict(pkv_handle_t h, const int32_t *kv_indptr, const int32_t *kv_indices,
+                                     const int32_t *last_page_len, int batch, const int32_t *keep, int num_sink,
+                                     int num_recent, const int32_t *dst_indptr, const int32_t *dst_indices,
+                                     void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    NvtxCall nvtx_range(h, "pkv_plan_evict");
+    if (!h) return fail(h, PKV_ERR_INVALID, "null handle");
+    if (!workspace) return fail(h, PKV_ERR_INVALID, "null workspace");
+    if (reinterpret_cast<uintptr_t>(workspace) % pkv::kAlign)
+        return fail(h, PKV_ERR_INVALID, "workspace must be 256-byte aligned");
+    std::string err;
+    pkv::EvictPlan ep;
+    ep.image.swap(h->spare_image);
+    int rc;
+    try {
+        rc = pkv::make_evict_plan(h->shape, kv_indptr, kv_indices, last_page_len, batch, keep, num_sink, num_recent,
+                                  dst_indptr, dst_indices, ep, err);
+    } catch (const std::exception &ex) {  // no C++ exception crosses the C boundary
+        rc = PKV_ERR_INVALID;
+        err = ex.what();
+    }
+    h->planned_ws = nullptr;
+    Plan plan;
+    plan.image.swap(ep.image);
+    if (rc) {
+        h->spare_image.swap(plan.image);
+        return fail(h, (pkv_status)rc, err);
+    }
+    plan.mode = PKV_MODE_EVICT;
+    plan.batch = batch;
+    plan.lay.total = ep.total;
+    h->evict = ep;
+    return stage_plan(h, plan, workspace, workspace_bytes, stream);
+}
+
+extern "C" pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t *kept, void *workspace,
+                                    pkv_stream_t stream) {
+    NvtxCall nvtx_range(h, "pkv_run_evict");
+    pkv_status st = check_planned(h, workspace, PKV_MODE_EVICT);
+    if (st != PKV_OK) return st;
+    if (h->evict.kept == 0) return PKV_OK;  // no row has a token to keep
+    if (!kv_layer || !kept) return fail(h, PKV_ERR_INVALID, "null kv_layer or kept");
+    if ((st = check_scores(h, scores, 0.f)) != PKV_OK) return st;
+    if (reinterpret_cast<uintptr_t>(kv_layer) % 16 || reinterpret_cast<uintptr_t>(kept) % 4)
+        return fail(h, PKV_ERR_INVALID, "kv_layer must be 16-byte aligned, kept 4-byte");
+    cudaError_t e = pkv::launch_evict(h->shape, h->evict, workspace, kv_layer, scores, kept,
+                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(h, e, "evict launch");
 }

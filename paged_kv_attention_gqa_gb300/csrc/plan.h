@@ -54,7 +54,8 @@ struct DecodeTile {
     int32_t partial;     // split-KV partial slot, -1 = this piece is the whole row
     int32_t merge_row;   // the row's MergeRow when it is cut, else -1
     int32_t append_token;  // fused append: the row's new token (last piece only), else -1
-    int32_t pad[2];
+    int32_t logit_base;    // DECODE_WEIGHTS plans: the row's first logit, in units of 16 keys
+    int32_t pad;
 };
 static_assert(sizeof(DecodeTile) == 48, "DecodeTile is 12 ints");
 

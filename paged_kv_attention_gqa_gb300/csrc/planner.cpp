@@ -272,7 +272,7 @@ void decode_split(const Shape &s, int rows, const int32_t *kvp, const int32_t *l
                 t.partial = -1;
                 t.merge_row = -1;
                 t.append_token = -1;
-                t.pad[0] = t.pad[1] = 0;
+                t.logit_base = t.pad = 0;
                 if (row_count[r]++ == 0) row_first[r] = (int)tiles.size();
                 tiles.push_back(t);
                 used += take;
