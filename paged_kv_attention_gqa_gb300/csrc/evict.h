@@ -22,20 +22,26 @@ struct WeightsTile {
     int32_t kv_base;     // offset of the row's first page in the plan's page list
     int32_t length;      // L
     int32_t key0;        // first key
-    int32_t lo;          // decode: first visible position (earlier keys have no logits)
     int32_t new_begin;   // L - n: the row's new tokens, whose scores start from nothing
     int32_t q_begin;     // first query token
     int32_t n_q;         // n
-    int32_t logit_base;  // decode: first logit of the row, in units of 16 keys
+    int32_t first;       // DECODE_WEIGHTS: first visible position; WEIGHTS: the tile's first part
+    int32_t base;        // DECODE_WEIGHTS: the row's first logit, in units of 16 keys; WEIGHTS: its parts
 };
 static_assert(sizeof(WeightsTile) == 32, "WeightsTile is 8 ints");
 
+// Work of one CTA at a time (WEIGHTS): kv heads [h0, h0 + nh) of a tile with the query tokens
+// [i0, i1) of its row, in `blocks` blocks.
+struct WeightsItem {
+    int32_t tile, h0, nh, i0, i1, blocks, part, pad;
+};
+static_assert(sizeof(WeightsItem) == 32, "WeightsItem is 8 ints");
+
 struct WeightsPlan {
-    size_t off_pages = 0, off_tiles = 0, off_part = 0;  // in the workspace
+    size_t off_pages = 0, off_tiles = 0, off_items = 0, off_part = 0;  // in the workspace
     size_t off_logits = 0;      // decode: float[num_qo_heads][logit_stride]
     long long logit_stride = 0;
-    int tiles = 0;
-    int hsplit = 1;             // WEIGHTS: CTAs that share a tile's kv heads
+    int tiles = 0, items = 0;
     int box_tokens = 1;         // WEIGHTS: query tokens of one block
 };
 

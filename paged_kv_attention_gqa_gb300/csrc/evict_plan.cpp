@@ -31,14 +31,45 @@ static int distinct_pages(const Shape &s, const int32_t *kvi, int nnz, std::vect
 
 static int keys16(int L) { return (L + 15) / 16; }
 
-// CTAs that share the kv heads of a WEIGHTS tile: a divisor of the head count, as many as it takes to
-// give every SM two CTAs.
-static int head_split(const Shape &s, long long tiles) {
-    const long long want = (2ll * std::max(1, s.sm_count)) / std::max(1ll, tiles);
-    int best = 1;
-    for (int d = 1; d <= s.num_kv_heads && d <= want; ++d)
-        if (s.num_kv_heads % d == 0) best = d;
-    return best;
+// The (kv head, query block) pairs of the WEIGHTS tiles cut into items of about an eighth of an SM's
+// share, longest first: a CTA per SM takes items round robin.  An item is a run of whole heads of one
+// tile, or a run of blocks of one head where a head alone has more.
+static void weight_items(const Shape &s, int causal, int window, int bt, std::vector<WeightsTile> &tiles,
+                         std::vector<WeightsItem> &items) {
+    struct Range {
+        int i0, i1, nb;
+    };
+    std::vector<Range> ranges(tiles.size());
+    long long total = 0;
+    for (size_t t = 0; t < tiles.size(); ++t) {
+        const WeightsTile &w = tiles[t];
+        // the tokens that may see a key of the tile (token i sits at position new_begin + i)
+        const int i0 = causal ? std::max(0, w.key0 - w.new_begin) : 0;
+        const int i1 = window >= 0 ? (int)std::min<long long>(w.n_q, (long long)w.key0 + kWeightKeys + window - w.new_begin)
+                                   : w.n_q;
+        ranges[t] = Range{i0, std::max(i0, i1), i1 > i0 ? (i1 - i0 + bt - 1) / bt : 0};
+        total += (long long)ranges[t].nb * s.num_kv_heads;
+    }
+    const int cap = (int)std::max<long long>(1, total / (8ll * std::max(1, s.sm_count)));
+    items.clear();
+    for (size_t t = 0; t < tiles.size(); ++t) {
+        const Range &r = ranges[t];
+        tiles[t].first = (int)items.size();
+        auto add = [&](int h0, int nh, int a, int b) {
+            items.push_back(WeightsItem{(int)t, h0, nh, a, b, (b - a + bt - 1) / bt, (int)items.size(), 0});
+        };
+        if (r.nb > 0 && r.nb <= cap) {
+            const int nh = std::min(s.num_kv_heads, cap / r.nb);
+            for (int h = 0; h < s.num_kv_heads; h += nh) add(h, std::min(nh, s.num_kv_heads - h), r.i0, r.i1);
+        } else if (r.nb > 0) {
+            const int chunks = (r.nb + cap - 1) / cap, step = (r.nb + chunks - 1) / chunks * bt;
+            for (int h = 0; h < s.num_kv_heads; ++h)
+                for (int a = r.i0; a < r.i1; a += step) add(h, 1, a, std::min(r.i1, a + step));
+        }
+        tiles[t].base = (int)items.size() - tiles[t].first;
+    }
+    std::stable_sort(items.begin(), items.end(),
+                     [](const WeightsItem &a, const WeightsItem &b) { return a.nh * a.blocks > b.nh * b.blocks; });
 }
 
 int make_weights_plan(const Shape &s, int mode, const int32_t *qo, const int32_t *kvp, const int32_t *kvi,
@@ -75,7 +106,7 @@ int make_weights_plan(const Shape &s, int mode, const int32_t *qo, const int32_t
         most = std::max(most, n);
         const int lo = decode && window_left >= 0 ? std::max(0, L - 1 - window_left) : 0;
         for (int k = 0; k < L; k += kWeightKeys)
-            tiles.push_back(WeightsTile{kvp[r], L, k, lo, L - n, decode ? r : qo[r], n, base[r]});
+            tiles.push_back(WeightsTile{kvp[r], L, k, L - n, decode ? r : qo[r], n, lo, base[r]});
     }
     w = WeightsPlan();
     w.tiles = (int)tiles.size();
@@ -106,13 +137,16 @@ int make_weights_plan(const Shape &s, int mode, const int32_t *qo, const int32_t
     plan.causal = causal;
     plan.window_left = window_left;
     plan.sm_scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt((float)s.head_dim);
-    w.hsplit = head_split(s, w.tiles);
     w.box_tokens = std::min(kPrefillRowsPerTile / s.group(), most);
+    std::vector<WeightsItem> items;
+    weight_items(s, causal, window_left, w.box_tokens, tiles, items);
+    w.items = (int)items.size();
     size_t at = kAlign;
     w.off_pages = put(at, (size_t)nnz * 4);
     w.off_tiles = put(at, tiles.size() * sizeof(WeightsTile));
+    w.off_items = put(at, items.size() * sizeof(WeightsItem));
     plan.lay.int_bytes = at;
-    w.off_part = put(at, (size_t)w.tiles * w.hsplit * kWeightKeys * 4);
+    w.off_part = put(at, items.size() * kWeightKeys * 4);
     plan.lay.total = at;
     image.assign(plan.lay.int_bytes, 0);
     PlanHeader hdr{};
@@ -122,6 +156,7 @@ int make_weights_plan(const Shape &s, int mode, const int32_t *qo, const int32_t
     std::memcpy(image.data(), &hdr, sizeof hdr);
     if (nnz) std::memcpy(image.data() + w.off_pages, kvi, (size_t)nnz * 4);
     if (!tiles.empty()) std::memcpy(image.data() + w.off_tiles, tiles.data(), tiles.size() * sizeof(WeightsTile));
+    if (!items.empty()) std::memcpy(image.data() + w.off_items, items.data(), items.size() * sizeof(WeightsItem));
     plan.image.swap(image);
     return PKV_OK;
 }
@@ -240,7 +275,11 @@ size_t evict_workspace_bound(const Shape &s, int mode) {
     size_t at = kAlign;
     put(at, nnz * 4);
     put(at, tiles * sizeof(WeightsTile));
-    put(at, (tiles + 2 * (size_t)std::max(1, s.sm_count)) * kWeightKeys * 4);
+    // an item is at least half an eighth of an SM's share, but for the last one of each tile (and one
+    // block of one head where the share is less)
+    const size_t items = 16 * (size_t)std::max(1, s.sm_count) + 2 * tiles;
+    put(at, items * sizeof(WeightsItem));
+    put(at, items * kWeightKeys * 4);
     return at;
 }
 
