@@ -19,7 +19,7 @@ constexpr int kLatentRope = 64;                      // the rope part of the key
 constexpr int kLatentWidth = kLatentDim + kLatentRope;
 constexpr int kLatentNope = 128, kLatentV = 128;     // the expanded heads: key without rope, value
 constexpr int kLatentRows = 64;                      // query rows (token, head) of one work unit
-constexpr int kLatentKeys = 64;                      // keys of one tile
+constexpr int kLatentKeys = 32;                      // keys of one tile
 constexpr int kLatentMinPage = 8;                    // a TMA box fills whole 8-row swizzle atoms
 
 struct LatentShape {
@@ -47,7 +47,7 @@ struct LatentTile {
     int32_t pos0;     // row f sits at position pos0 + f / H
     int32_t length;   // L of the sequence
     int32_t kv_base;  // offset of the sequence's first page in the plan's page list
-    int32_t tile0;    // first key tile (keys tile0 * 64 ..)
+    int32_t tile0;    // first key tile (keys tile0 * kLatentKeys ..)
     int32_t ntiles;   // >= 1
     int32_t partial;  // split-KV partial slot, -1 = this piece is the whole unit
 };

@@ -23,8 +23,8 @@ static Shape as_shape(const LatentShape &s) {
     return b;
 }
 
-// Key tiles a CTA is given at least.
-static constexpr int kMinTiles = 1;
+// Key tiles a CTA is given at least (fewer would only add pieces to join).
+static constexpr int kMinTiles = 2;
 
 namespace {
 struct Unit {
