@@ -19,7 +19,7 @@ constexpr int kLatentRope = 64;                      // the rope part of the key
 constexpr int kLatentWidth = kLatentDim + kLatentRope;
 constexpr int kLatentNope = 128, kLatentV = 128;     // the expanded heads: key without rope, value
 constexpr int kLatentRows = 64;                      // query rows (token, head) of one work unit
-constexpr int kLatentKeys = 32;                      // keys of one tile
+constexpr int kLatentKeys = 64;                      // keys of one tile
 constexpr int kLatentMinPage = 8;                    // a TMA box fills whole 8-row swizzle atoms
 
 struct LatentShape {
@@ -27,8 +27,10 @@ struct LatentShape {
     int max_batch = 0, max_total_tokens = 0, max_num_pages = 0, num_cache_pages = 0;
     int sm_count = 0;
     int page_shift() const { return __builtin_ctz((unsigned)page_size); }
-    // rows of one TMA box of the cache: a whole page up to one key tile
+    // rows of one TMA box of the cache: a whole page up to one key tile; a box of a whole tile takes all
+    // columns, a smaller one 64
     int box_rows() const { return page_size < kLatentKeys ? page_size : kLatentKeys; }
+    int box_chunks() const { return page_size < kLatentKeys ? 1 : kLatentWidth / 64; }
 };
 
 // First bytes of a latent plan in the workspace.
@@ -64,6 +66,7 @@ struct LatentPlan {
     int causal = 1, window_left = -1;
     int box_q = 64;         // rows of one TMA box of q
     int ctas = 0, num_partials = 0, num_merge = 0, pf_tiles = 0;
+    int max_pieces = 0;     // of the unit that is cut most
     size_t off_append = 0, off_pages = 0, off_tiles = 0, off_cta = 0, off_merge = 0, off_part_o = 0, off_part_lse = 0;
     size_t total = 0;
     PlanLayout dense_lay;   // dense plans: PlanHeader and PrefillTiles, as the other dense plans
@@ -78,8 +81,8 @@ int make_latent_dense_plan(const LatentShape &s, const int32_t *cu_q, const int3
                            int window_left, float sm_scale, LatentPlan &plan, std::string &err);
 size_t latent_workspace_bound(const LatentShape &s, bool dense);
 
-// Launchers.  `tm_cache`: boxes of (64 columns, box_rows() rows) of the layer slice viewed as
-// [pages * page_size][576]; `tm_q`: boxes of (64 columns, box_q rows) of q viewed as [T * H][576].
+// Launchers.  `tm_cache`: boxes of (64 columns, box_rows() rows, box_chunks() chunks) of the layer slice
+// viewed as [9 chunks][pages * page_size][64] (chunks outermost, so that one chunk's rows land together); `tm_q`: boxes of (64 columns, box_q rows) of q viewed as [T * H][576].
 cudaError_t launch_latent(const LatentShape &s, const LatentPlan &p, const CUtensorMap &tm_cache,
                           const CUtensorMap &tm_q, void *ws, void *out, float *lse, cudaStream_t st);
 // Expanded form: boxes of 64 columns x 128 rows of q [H][T][192], k_nope [H][keys][128], k_rope

@@ -176,13 +176,13 @@ extern "C" pkv_status pkv_latent_append_planned(pkv_latent_t h, const void *c_ne
 }
 
 // Tensor map over a bf16 tensor of `rank` dims (innermost first; strides in elements of dims 1..) with
-// boxes of 64 columns x box_rows rows of dim 1, 128-byte swizzle.
+// boxes of 64 columns x box_rows of dim 1 x box_outer of dim 2, 128-byte swizzle.
 static pkv_status encode(pkv_latent_t h, const void *base, int rank, const long long *dims, const long long *strides,
-                         int box_rows, CUtensorMap *tm) {
+                         int box_rows, CUtensorMap *tm, int box_outer = 1) {
     auto fn = pkv::encode_fn();
     if (!fn) return fail(h, PKV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     cuuint64_t d[3], st[2];
-    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_outer}, es[3] = {1, 1, 1};
     for (int i = 0; i < rank; ++i) d[i] = (cuuint64_t)dims[i];
     for (int i = 0; i + 1 < rank; ++i) st[i] = (cuuint64_t)strides[i] * 2;
     const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, st, box, es,
@@ -204,10 +204,11 @@ extern "C" pkv_status pkv_latent_run(pkv_latent_t h, const void *q, const void *
             return fail(h, PKV_ERR_INVALID, "q, cache_layer and out must be 16-byte aligned (lse 4-byte)");
         const LatentShape &s = h->shape;
         CUtensorMap tc, tq;
-        const long long cd[2] = {pkv::kLatentWidth, (long long)s.num_cache_pages * s.page_size};
+        const long long cd[3] = {64, (long long)s.num_cache_pages * s.page_size, pkv::kLatentWidth / 64};
+        const long long cs[2] = {pkv::kLatentWidth, 64};
         const long long qd[2] = {pkv::kLatentWidth, (long long)h->plan.num_tokens * s.num_heads};
         const long long stride[1] = {pkv::kLatentWidth};
-        if ((st = encode(h, cache_layer, 2, cd, stride, s.box_rows(), &tc)) != PKV_OK) return st;
+        if ((st = encode(h, cache_layer, 3, cd, cs, s.box_rows(), &tc, s.box_chunks())) != PKV_OK) return st;
         if ((st = encode(h, q, 2, qd, stride, h->plan.box_q, &tq)) != PKV_OK) return st;
         const cudaError_t e =
             pkv::launch_latent(s, h->plan, tc, tq, workspace, out, lse, static_cast<cudaStream_t>(stream));

@@ -24,7 +24,7 @@ static Shape as_shape(const LatentShape &s) {
 }
 
 // Key tiles a CTA is given at least (fewer would only add pieces to join).
-static constexpr int kMinTiles = 2;
+static constexpr int kMinTiles = 1;
 
 namespace {
 struct Unit {
@@ -179,6 +179,8 @@ int make_latent_plan(const LatentShape &s, const int32_t *qo, const int32_t *kvp
     plan.ctas = tiles.empty() ? 0 : (int)cta.size() - 1;
     plan.num_partials = parts;
     plan.num_merge = (int)merges.size();
+    plan.max_pieces = 0;
+    for (const LatentMerge &m : merges) plan.max_pieces = std::max(plan.max_pieces, (int)m.count);
     plan.pf_tiles = 0;
     size_t at = kAlign;
     plan.off_append = put(at, rows.size() * 4);
