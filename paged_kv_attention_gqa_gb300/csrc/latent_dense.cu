@@ -6,14 +6,17 @@
 // Bounded by the tensor cores: 640 operations per query, key and head, on operands that fit L2.  A
 // work tile is two query tiles of 128 tokens of one head that share every 128-key tile, one CTA per
 // SM, in the division of the two-query-tile prefill kernel:
-//  * warp 8 copies Q0 and Q1 once, then streams the K/V tiles as 64-column chunks of 128 keys (16 KB:
+//  * warp 16 copies Q0 and Q1 once, then streams the K/V tiles as 64-column chunks of 128 keys (16 KB:
 //    two of k_nope, one of k_rope, two of v) through one ring of eight; a chunk is refilled as soon as
 //    the MMAs of both query tiles that read it are done;
-//  * warps 9 and 10 issue the MMAs of Q0 and Q1: S = Q K^T (12 k-steps, N = 128), then O += P V (P from
+//  * warps 17 and 18 issue the MMAs of Q0 and Q1: S = Q K^T (12 k-steps, N = 128), then O += P V (P from
 //    tensor memory; N = 64 per chunk, which runs at the full rate: measured 32 cycles a k-step), with
 //    S0, S1, O0, O1 in 128 tensor-memory columns each;
-//  * warps 0-3 and 4-7 run the softmax of Q0 and Q1 by turns, so that each runs under the other tile's
-//    MMAs.  The running maximum moves, and O is rescaled, only when it grows by more than 2^8.
+//  * warps 0-7 and 8-15 run the softmax of Q0 and Q1 by turns, so that each runs under the other tile's
+//    MMAs.  A query's 128 scores are shared by two threads, two warps per SM sub-partition, which halves
+//    the phases of a turn that leave the exponential unit idle (one thread a query: 305 us on four
+//    prompts of 801 to 4,093 tokens and 32 heads).  The two agree on the maximum through shared memory
+//    only when it has to move: it moves, and O is rescaled, when it grows by more than 2^8.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,11 +29,11 @@ namespace pkv {
 namespace dev {
 
 constexpr int kLdKeys = 128, kLdQueries = 128;
-constexpr int kLdThreads = 384;
-// Registers: 384 x 168 at launch = 64,512; the softmax groups take most of warp group 2's share
-// (128 x 96 + 256 x 200 = 63,488).
-constexpr int kLdLaunchRegs = 168, kLdSoftmaxRegs = 200, kLdOtherRegs = 96;
-static_assert(128 * kLdOtherRegs + 256 * kLdSoftmaxRegs <= kLdThreads * kLdLaunchRegs, "setmaxnreg split fits the launch");
+constexpr int kLdThreads = 640;
+// Registers: 640 x 96 at launch = 61,440; the softmax groups take most of warp group 4's share
+// (128 x 56 + 512 x 104 = 60,416).
+constexpr int kLdLaunchRegs = 96, kLdSoftmaxRegs = 104, kLdOtherRegs = 56;
+static_assert(128 * kLdOtherRegs + 512 * kLdSoftmaxRegs <= kLdThreads * kLdLaunchRegs, "setmaxnreg split fits the launch");
 constexpr float kLdRescale = 8.f;  // log2
 constexpr float kLdLn2 = 0.6931471805599453f;
 
@@ -40,7 +43,8 @@ struct LdSmem {
     static constexpr uint32_t Q_OFF = 0;
     static constexpr uint32_t RING_OFF = 2 * QC * CHUNK;
     static constexpr uint32_t BAR_OFF = RING_OFF + SLOTS * CHUNK;
-    static constexpr uint32_t BYTES = BAR_OFF + 256;
+    static constexpr uint32_t EXCH_OFF = BAR_OFF + 256;  // per query tile and query: a maximum
+    static constexpr uint32_t BYTES = EXCH_OFF + 2 * 128 * 4;
 };
 static_assert(1024 + LdSmem::BYTES <= 227 * 1024, "the expanded latent kernel fits shared memory");
 
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     uint64_t *s_full = bars + 18;    // [2] S_X(j) in tensor memory
     uint64_t *p_full = bars + 20;    // [2] P_X(j) written (and O_X rescaled if it had to be)
     uint64_t *pv_done = bars + 22;   // [2] PV_X(j) completed
-    uint64_t *v_tail = bars + 24;    // warp 9 zeroed the value rows past the segment (at most once)
+    uint64_t *v_tail = bars + 24;    // warp 17 zeroed the value rows past the segment (at most once)
     uint64_t *turn = bars + 25;      // [2] the softmax group of Q_X may start its next tile
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 27);
 
@@ -83,9 +87,9 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(&q_full[x], 1);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 4);
+            mbar_init(&p_full[x], 8);
             mbar_init(&pv_done[x], 1);
-            mbar_init(&turn[x], 4);
+            mbar_init(&turn[x], 8);
         }
         for (int s = 0; s < L::SLOTS; ++s) {
             mbar_init(&kv_full[s], 1);
@@ -94,7 +98,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         mbar_init(v_tail, 1);
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(tmem_holder, 512);
         tmem_relinquish();
     }
@@ -107,9 +111,9 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     auto S_col = [tmem](int x) { return tmem + 128u * (uint32_t)x; };
     auto O_col = [tmem](int x) { return tmem + 256u + 128u * (uint32_t)x; };
 
-    if (warp >= 8) {
+    if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLdOtherRegs));
-        if (warp == 8) {
+        if (warp == 16) {
             // ------------------------------------------------ copies: one thread, one box per chunk
             if (lane == 0) {
                 prefetch_tmap(&tm_q);
@@ -149,9 +153,9 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 for (uint32_t d = i > L::SLOTS ? i - L::SLOTS : 0; d < i; ++d)
                     mbar_wait(&kv_full[d % L::SLOTS], (d / L::SLOTS) & 1, err, kErrWaitDrain);
             }
-        } else if (warp == 9 || (warp == 10 && two)) {
-            // ------------------------------------------------ MMAs: warp 9 for Q0, warp 10 for Q1
-            const int x = warp - 9;
+        } else if (warp == 17 || (warp == 18 && two)) {
+            // ------------------------------------------------ MMAs: warp 17 for Q0, warp 18 for Q1
+            const int x = warp - 17;
             constexpr uint32_t ID_S = idesc_bf16_f32(128, kLdKeys, 0, 0);
             constexpr uint32_t ID_O = idesc_bf16_f32(128, 64, 0, 1);
             const uint64_t dQ = smem_desc(smem_u32(sm + L::Q_OFF + x * L::QC * L::CHUNK), 16, 1024, kSwizzle128B);
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 if (!ok) break;
                 mma_commit_elect(&s_full[x]);
                 // Value rows past the segment's end belong to the next segment (or are zero past the
-                // tensor): their P is 0, but 0 * NaN would reach O.  Warp 9 zeroes them; warp 10 waits
+                // tensor): their P is 0, but 0 * NaN would reach O.  Warp 17 zeroes them; warp 18 waits
                 // for that on the one tile that has them.
                 const int key0 = (kt0 + j) * kLdKeys;
                 const bool tail = key0 + kLdKeys > t.length;
@@ -220,11 +224,13 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLdSoftmaxRegs));
-        // ------------------------------------------------ softmax + epilogue (warps 0-7)
-        const int x = warp >> 2;               // query tile of this warp group
+        // ------------------------------------------------ softmax + epilogue (warps 0-15)
+        const int x = warp >> 3;               // query tile of this warp's group
+        const int hf = (warp >> 2) & 1;        // which 64 of a tile's keys, of P's columns and of O's
         const int m = (warp & 3) * 32 + lane;  // query = TMEM lane
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         if (x == 0 || two) {
+            float *const exch = reinterpret_cast<float *>(sm + L::EXCH_OFF) + x * 128;
             const int tok = x * kLdQueries + m;  // token within the work tile
             const bool live = tok < t.n_q;
             const int pos = t.pos0 + tok;
@@ -232,95 +238,96 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             const int hi = min(causal == 1 ? pos : t.length - 1, t.length - 1);
             const int lo = window_left >= 0 ? max(0, pos - window_left) : 0;
             const float sl = a.hdr->scale_log2;
-            const uint32_t Sx = S_col(x) + lane_off, Ox = O_col(x) + lane_off;
-            float m_run = -INFINITY, l_run = 0.f;
+            const uint32_t Sx = S_col(x) + lane_off, Ox = O_col(x) + lane_off + 64u * hf;
+            float m_run = -INFINITY, l_run = 0.f;  // l_run: this half's keys
+            // a wait that gives up clears ok; the warps still walk their tiles, without further waits, so that
+            // they keep meeting at their barriers (which have no time limit)
             bool ok = true;
             for (int j = 0; j < nt; ++j) {
-                const int key0 = (kt0 + j) * kLdKeys;
+                const int key0 = (kt0 + j) * kLdKeys + 64 * hf;
                 // group 1 starts tile j after group 0 finished it, group 0 tile j + 1 after group 1 tile j
-                if (two && (x == 1 || j > 0) && !mbar_wait(&turn[x], (x ? j : j - 1) & 1, err, kErrWaitFull)) {
-                    ok = false;
-                    break;
-                }
-                if (!mbar_wait(&s_full[x], j & 1, err, kErrWaitFull)) {
-                    ok = false;
-                    break;
-                }
+                if (two && (x == 1 || j > 0)) ok = ok && mbar_wait(&turn[x], (x ? j : j - 1) & 1, err, kErrWaitFull);
+                ok = ok && mbar_wait(&s_full[x], j & 1, err, kErrWaitFull);
+                __syncwarp();
                 tc_fence_after();
-                uint32_t r0[32], r1[32], r2[32], r3[32];
-                tmem_ld32(Sx, r0);
-                tmem_ld32(Sx + 32, r1);
-                tmem_ld32(Sx + 64, r2);
-                tmem_ld32(Sx + 96, r3);
+                uint32_t r0[32], r1[32];
+                tmem_ld32(Sx + 64u * hf, r0);
+                tmem_ld32(Sx + 64u * hf + 32, r1);
                 tmem_wait_ld();
-                float sv[kLdKeys];
+                float sv[64];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     sv[c] = __uint_as_float(r0[c]);
                     sv[32 + c] = __uint_as_float(r1[c]);
-                    sv[64 + c] = __uint_as_float(r2[c]);
-                    sv[96 + c] = __uint_as_float(r3[c]);
                 }
-                if (key0 < lo || key0 + kLdKeys - 1 > hi) {
+                if (key0 < lo || key0 + 63 > hi) {
 #pragma unroll
-                    for (int c = 0; c < kLdKeys; ++c) {
+                    for (int c = 0; c < 64; ++c) {
                         const int k = key0 + c;
-                        sv[c] = (k >= lo && k <= hi) ? sv[c] : -INFINITY;
+                        sv[c] = ((k >= lo) & (k <= hi)) ? sv[c] : -INFINITY;
                     }
                 }
-                float m8[8];
+                float m4[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) m8[c] = fmaxf(sv[2 * c], sv[2 * c + 1]);
+                for (int c = 0; c < 4; ++c) m4[c] = fmaxf(sv[2 * c], sv[2 * c + 1]);
 #pragma unroll
-                for (int c = 16; c < kLdKeys; c += 16)
+                for (int c = 8; c < 64; c += 8)
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) m8[q] = max3f(m8[q], sv[c + 2 * q], sv[c + 2 * q + 1]);
+                    for (int q = 0; q < 4; ++q) m4[q] = max3f(m4[q], sv[c + 2 * q], sv[c + 2 * q + 1]);
                 // rows past the tile's tokens hold another segment's queries: they move no maximum
-                const float m_tile =
-                    live ? max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * sl
-                         : -INFINITY;
-                // each row moves its maximum by its own growth alone, so that a row's bits do not
-                // depend on its neighbours
-                const bool grow = m_tile > m_run + kLdRescale;
-                const bool warp_grow = __any_sync(0xffffffffu, grow) && j > 0;
+                const float m_half = live ? max3f(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * sl : -INFINITY;
+                // whether any query of the group moves its maximum.  The barrier also says that every
+                // thread holds its scores: the second half's P goes over columns of the first half's S
+                unsigned any;
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 256, p;\n\t"
+                             "selp.u32 %0, 1, 0, q;\n\t}"
+                             : "=r"(any)
+                             : "r"((unsigned)(m_half > m_run + kLdRescale)), "r"(1 + x)
+                             : "memory");
                 float alpha = 1.f;
-                if (grow) {
-                    alpha = ex2_ftz(m_run - m_tile);  // 0 when m_run = -inf
-                    m_run = m_tile;
+                bool grow = false;
+                if (any) {
+                    // the first half's maximum to the second, the joint one back.  Each query moves its
+                    // maximum by its own growth alone, so that its bits do not depend on its neighbours
+                    if (hf == 0) exch[m] = m_half;
+                    named_barrier_sync(1 + x, 256);
+                    float m_tile = hf ? fmaxf(m_half, exch[m]) : 0.f;
+                    if (hf) exch[m] = m_tile;
+                    named_barrier_sync(1 + x, 256);
+                    if (!hf) m_tile = exch[m];
+                    grow = m_tile > m_run + kLdRescale;
+                    if (grow) {
+                        alpha = ex2_ftz(m_run - m_tile);  // 0 when m_run = -inf
+                        m_run = m_tile;
+                    }
                 }
                 // p = 2^(s * sl - m), two columns per packed FMA; P goes back over S as packed bf16
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
                 const uint64_t sl2 = f2_make(sl, sl), nm2 = f2_make(-mref, -mref);
                 uint64_t acc[4] = {0, 0, 0, 0};
+                uint32_t pk[32];
 #pragma unroll
-                for (int hlf = 0; hlf < 2; ++hlf) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int e = hlf * 64 + 2 * c;
-                        float x0, x1;
-                        f2_split(ffma2(f2_make(sv[e], sv[e + 1]), sl2, nm2), x0, x1);
-                        const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
-                        acc[c & 3] = fadd2(acc[c & 3], f2_make(p0, p1));
-                        pk[c] = pack_bf16(p0, p1);
-                    }
-                    tmem_st32(Sx + hlf * 32, pk);
+                for (int c = 0; c < 32; ++c) {
+                    float x0, x1;
+                    f2_split(ffma2(f2_make(sv[2 * c], sv[2 * c + 1]), sl2, nm2), x0, x1);
+                    const float p0 = ex2_ftz(x0), p1 = ex2_ftz(x1);
+                    acc[c & 3] = fadd2(acc[c & 3], f2_make(p0, p1));
+                    pk[c] = pack_bf16(p0, p1);
                 }
+                tmem_st32(Sx + 32u * hf, pk);
                 float u0, u1;
                 f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u0, u1);
                 l_run = l_run * alpha + (u0 + u1);
                 __syncwarp();
                 if (two && lane == 0) mbar_arrive(&turn[1 - x]);  // the other group's turn
                 tmem_wait_st();
-                if (warp_grow) {
+                if (__any_sync(0xffffffffu, grow) && j > 0) {
                     // O holds P_0..P_{j-1} V: wait for the last of those MMAs, then scale O's rows
-                    if (!mbar_wait(&pv_done[x], (j - 1) & 1, err, kErrWaitFull)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = ok && mbar_wait(&pv_done[x], (j - 1) & 1, err, kErrWaitFull);
+                    __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kLatentV; c0 += 32) {
+                    for (int c0 = 0; c0 < 64; c0 += 32) {
                         uint32_t o[32];
                         tmem_ld32(Ox + c0, o);
                         tmem_wait_ld();
@@ -334,13 +341,20 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
-            if (ok && mbar_wait(&pv_done[x], (nt - 1) & 1, err, kErrWaitFull)) {
+            // the two halves' sums, through the query tile's shared memory: nothing reads Q_X any more
+            ok = ok && mbar_wait(&pv_done[x], (nt - 1) & 1, err, kErrWaitFull);
+            __syncwarp();
+            float *const sums = reinterpret_cast<float *>(sm + L::Q_OFF + x * L::QC * L::CHUNK);
+            if (ok) sums[hf * 128 + m] = l_run;
+            named_barrier_sync(1 + x, 256);
+            const float l = l_run + sums[(1 - hf) * 128 + m];
+            if (__all_sync(0xffffffffu, ok)) {
                 tc_fence_after();
-                const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 const size_t row = (size_t)(t.q_begin + tok) * a.num_heads + t.kv_head;
-                __nv_bfloat16 *orow = a.out + row * kLatentV;
+                __nv_bfloat16 *orow = a.out + row * kLatentV + 64 * hf;
 #pragma unroll 1
-                for (int c0 = 0; c0 < kLatentV; c0 += 32) {
+                for (int c0 = 0; c0 < 64; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(Ox + c0, o);
                     tmem_wait_ld();
@@ -355,14 +369,14 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                             dst[c] = make_uint4(pkd[4 * c], pkd[4 * c + 1], pkd[4 * c + 2], pkd[4 * c + 3]);
                     }
                 }
-                if (live && a.lse) a.lse[row] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLdLn2;
+                if (hf == 0 && live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLdLn2;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace dev
