@@ -120,31 +120,45 @@ def _p(a):
 
 
 def _dptr(t):
-    """Device pointer of a torch tensor (or None)."""
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """Device pointer of a torch tensor (or None), as the integer that ctypes takes for a void *."""
+    return None if t is None else t.data_ptr()
+
+
+_torch = None       # torch, imported by the first call that needs it
+_raw_stream = None  # the current stream of a device as an integer
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _torch = torch
+    # torch.cuda.current_stream() builds a Stream object (3 us); the integer alone takes 0.2 us
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return torch
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        torch = _torch or _load_torch()
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
-def _check_tensor(name, t, dtype, shape, contiguous=True):
-    """The operators that take tensors' shapes on trust in C check them here: type, shape (None = any
-    size), device (the current one) and layout."""
-    import torch
+def _check_tensor(name, t, dtype, shape, device, contiguous=True):
+    """The operators that take tensors' shapes on trust in C check them here: type, shape, device (the
+    current one, by its index) and layout."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and (not contiguous or t.is_contiguous()):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _stride(t, dim, least):
@@ -243,34 +257,37 @@ class Handle:
                                            _dptr(workspace), _stream(stream)))
 
     def _check_layer(self, kv_layer, scores):
-        import torch
-        c = self.cfg
+        """Checks the slices; returns torch and the current device."""
+        torch, c = _torch or _load_torch(), self.cfg
+        device = torch.cuda.current_device()
         _check_tensor("kv_layer", kv_layer, torch.bfloat16,
-                      (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim))
-        _check_tensor("scores", scores, torch.float32, (c.num_cache_pages, c.page_size))
+                      (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim), device)
+        _check_tensor("scores", scores, torch.float32, (c.num_cache_pages, c.page_size), device)
+        return torch, device
 
-    def _check_q(self, q, lse):
-        import torch
-        tokens = self._planned_tokens
-        _check_tensor("q", q, torch.bfloat16, (tokens, self.cfg.num_qo_heads, self.cfg.head_dim))
-        _check_tensor("lse", lse, torch.float32, (tokens, self.cfg.num_qo_heads))
+    def _check_q(self, q, lse, torch, device):
+        tokens, heads = self._planned_tokens, self.cfg.num_qo_heads
+        _check_tensor("q", q, torch.bfloat16, (tokens, heads, self.cfg.head_dim), device)
+        _check_tensor("lse", lse, torch.float32, (tokens, heads), device)
 
     def run_decode_weights(self, q, kv_layer, out, lse, scores, *, decay=1.0, workspace, stream=None):
         """run_decode of a MODE_DECODE_WEIGHTS plan that also adds every key's softmax weight, summed over
         the query heads, into scores [pages, page_size] (fp32): decay * old + new, the row's newest
         token from nothing."""
-        self._check_layer(kv_layer, scores)
-        self._check_q(q, lse)
-        _check_tensor("out", out, q.dtype, tuple(q.shape))
-        self._check(self.lib.pkv_run_decode_weights(self.h, _dptr(q), _dptr(kv_layer), _dptr(out), _dptr(lse),
-                                                    _dptr(scores), float(decay), _dptr(workspace), _stream(stream)))
+        torch, device = self._check_layer(kv_layer, scores)
+        self._check_q(q, lse, torch, device)
+        _check_tensor("out", out, torch.bfloat16, q.shape, device)
+        self._check(self.lib.pkv_run_decode_weights(
+            self.h, q.data_ptr(), kv_layer.data_ptr(), out.data_ptr(), lse.data_ptr(), scores.data_ptr(), decay,
+            workspace.data_ptr(), _raw_stream(device) if stream is None else _stream(stream)))
 
     def run_weights(self, q, lse, kv_layer, scores, *, decay=1.0, workspace, stream=None):
         """The same scores from the queries and the lse of a prefill (MODE_WEIGHTS plans)."""
-        self._check_layer(kv_layer, scores)
-        self._check_q(q, lse)
-        self._check(self.lib.pkv_run_weights(self.h, _dptr(q), _dptr(lse), _dptr(kv_layer), _dptr(scores), float(decay),
-                                             _dptr(workspace), _stream(stream)))
+        torch, device = self._check_layer(kv_layer, scores)
+        self._check_q(q, lse, torch, device)
+        self._check(self.lib.pkv_run_weights(
+            self.h, q.data_ptr(), lse.data_ptr(), kv_layer.data_ptr(), scores.data_ptr(), decay, workspace.data_ptr(),
+            _raw_stream(device) if stream is None else _stream(stream)))
 
     def plan_evict(self, kv_indptr, kv_indices, last_page_len, keep, dst_indptr, dst_indices, *, num_sink=0,
                    num_recent=0, workspace, stream=None):
@@ -289,11 +306,11 @@ class Handle:
 
     def run_evict(self, kv_layer, scores, kept, *, workspace, stream=None):
         """Move the kept tokens of one layer; kept (int32) receives their positions, row after row."""
-        import torch
-        self._check_layer(kv_layer, scores)
-        _check_tensor("kept", kept, torch.int32, (self._kept,))
-        self._check(self.lib.pkv_run_evict(self.h, _dptr(kv_layer), _dptr(scores), _dptr(kept), _dptr(workspace),
-                                           _stream(stream)))
+        torch, device = self._check_layer(kv_layer, scores)
+        _check_tensor("kept", kept, torch.int32, (self._kept,), device)
+        self._check(self.lib.pkv_run_evict(
+            self.h, kv_layer.data_ptr(), scores.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
+            _raw_stream(device) if stream is None else _stream(stream)))
 
     def gather_kv(self, kv_layer, pages, num_tokens, k_out, v_out, stream=None):
         """pages: a device int32 tensor of page ids."""
@@ -351,6 +368,7 @@ class LatentHandle:
             raise PkvError(st, self.lib.pkv_latent_last_error(None).decode())
         self.h = h
         self._tokens = self._keys = 0
+        self._cache_shape = (num_cache_pages, page_size, self.LATENT + self.ROPE)
 
     def close(self):
         if getattr(self, "h", None):
@@ -383,37 +401,40 @@ class LatentHandle:
                                              workspace.numel() * workspace.element_size(), _stream(stream)))
         self._tokens = batch if arrs[0] is None else int(arrs[0][-1])
 
+    def _rows(self, name, t, width, torch, device):
+        """Pointer and row stride of a [tokens, width] tensor whose rows may be strided."""
+        _check_tensor(name, t, torch.bfloat16, (self._tokens, width), device, contiguous=False)
+        if t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit stride in its last dimension")
+        return t.data_ptr(), _stride(t, 0, width)
+
     def append_planned(self, c_new, rope_new, cache_layer, *, workspace, stream=None):
         """The step's new vectors into their slots: c_new [T, 512] and rope_new [T, 64], rows may be strided."""
-        import torch
-        _check_tensor("c_new", c_new, torch.bfloat16, (self._tokens, self.LATENT), contiguous=False)
-        _check_tensor("rope_new", rope_new, torch.bfloat16, (self._tokens, self.ROPE), contiguous=False)
-        self._check_cache(cache_layer)
-        if c_new.stride(1) != 1 or rope_new.stride(1) != 1:
-            raise ValueError("c_new and rope_new must have unit stride in their last dimension")
+        torch = _torch or _load_torch()
+        device = torch.cuda.current_device()
+        c, cs = self._rows("c_new", c_new, self.LATENT, torch, device)
+        r, rs = self._rows("rope_new", rope_new, self.ROPE, torch, device)
+        _check_tensor("cache_layer", cache_layer, torch.bfloat16, self._cache_shape, device)
         self._check(self.lib.pkv_latent_append_planned(
-            self.h, _dptr(c_new), _stride(c_new, 0, self.LATENT), _dptr(rope_new), _stride(rope_new, 0, self.ROPE),
-            _dptr(cache_layer), _dptr(workspace), _stream(stream)))
+            self.h, c, cs, r, rs, cache_layer.data_ptr(), workspace.data_ptr(),
+            _raw_stream(device) if stream is None else _stream(stream)))
 
-    def _check_cache(self, cache_layer):
-        import torch
-        _check_tensor("cache_layer", cache_layer, torch.bfloat16,
-                      (self.cfg.num_cache_pages, self.cfg.page_size, self.LATENT + self.ROPE))
-
-    def _check_out(self, out, lse, width):
-        import torch
-        _check_tensor("out", out, torch.bfloat16, (self._tokens, self.cfg.num_heads, width))
+    def _check_out(self, out, lse, width, torch, device):
+        tokens, heads = self._tokens, self.cfg.num_heads
+        _check_tensor("out", out, torch.bfloat16, (tokens, heads, width), device)
         if lse is not None:
-            _check_tensor("lse", lse, torch.float32, (self._tokens, self.cfg.num_heads))
+            _check_tensor("lse", lse, torch.float32, (tokens, heads), device)
 
     def run(self, q, cache_layer, out, lse=None, *, workspace, stream=None):
         """Absorbed form: q [T, heads, 576], out [T, heads, 512], lse [T, heads]."""
-        import torch
-        _check_tensor("q", q, torch.bfloat16, (self._tokens, self.cfg.num_heads, self.LATENT + self.ROPE))
-        self._check_cache(cache_layer)
-        self._check_out(out, lse, self.LATENT)
-        self._check(self.lib.pkv_latent_run(self.h, _dptr(q), _dptr(cache_layer), _dptr(out), _dptr(lse),
-                                            _dptr(workspace), _stream(stream)))
+        torch = _torch or _load_torch()
+        device = torch.cuda.current_device()
+        _check_tensor("q", q, torch.bfloat16, (self._tokens, self.cfg.num_heads, self.LATENT + self.ROPE), device)
+        _check_tensor("cache_layer", cache_layer, torch.bfloat16, self._cache_shape, device)
+        self._check_out(out, lse, self.LATENT, torch, device)
+        self._check(self.lib.pkv_latent_run(
+            self.h, q.data_ptr(), cache_layer.data_ptr(), out.data_ptr(), _dptr(lse), workspace.data_ptr(),
+            _raw_stream(device) if stream is None else _stream(stream)))
 
     def plan_dense(self, cu_q, cu_k, *, workspace, sm_scale, causal=True, window_left=-1, stream=None):
         cq, ck = _i32(cu_q), _i32(cu_k)
@@ -425,19 +446,20 @@ class LatentHandle:
     def run_dense(self, q, k_nope, k_rope, v, out, lse=None, *, workspace, stream=None):
         """Expanded form: q [T, heads, 192], k_nope and v [keys, heads, 128], k_rope [keys, 64] (these three
         with any token and head strides), out [T, heads, 128], lse [T, heads]."""
-        import torch
-        bf, H = torch.bfloat16, self.cfg.num_heads
-        _check_tensor("q", q, bf, (self._tokens, H, self.NOPE + self.ROPE))
-        _check_tensor("k_nope", k_nope, bf, (self._keys, H, self.NOPE), contiguous=False)
-        _check_tensor("k_rope", k_rope, bf, (self._keys, self.ROPE), contiguous=False)
-        _check_tensor("v", v, bf, (self._keys, H, self.V), contiguous=False)
+        torch = _torch or _load_torch()
+        device, bf, H = torch.cuda.current_device(), torch.bfloat16, self.cfg.num_heads
+        _check_tensor("q", q, bf, (self._tokens, H, self.NOPE + self.ROPE), device)
+        _check_tensor("k_nope", k_nope, bf, (self._keys, H, self.NOPE), device, contiguous=False)
+        _check_tensor("k_rope", k_rope, bf, (self._keys, self.ROPE), device, contiguous=False)
+        _check_tensor("v", v, bf, (self._keys, H, self.V), device, contiguous=False)
         if k_nope.stride(2) != 1 or k_rope.stride(1) != 1 or v.stride(2) != 1:
             raise ValueError("k_nope, k_rope and v must have unit stride in their last dimension")
-        self._check_out(out, lse, self.V)
+        self._check_out(out, lse, self.V, torch, device)
         self._check(self.lib.pkv_latent_run_dense(
-            self.h, _dptr(q), _dptr(k_nope), _stride(k_nope, 0, self.NOPE), _stride(k_nope, 1, self.NOPE), _dptr(k_rope),
-            _stride(k_rope, 0, self.ROPE), _dptr(v), _stride(v, 0, self.V), _stride(v, 1, self.V), _dptr(out), _dptr(lse),
-            _dptr(workspace), _stream(stream)))
+            self.h, q.data_ptr(), k_nope.data_ptr(), _stride(k_nope, 0, self.NOPE), _stride(k_nope, 1, self.NOPE),
+            k_rope.data_ptr(), _stride(k_rope, 0, self.ROPE), v.data_ptr(), _stride(v, 0, self.V), _stride(v, 1, self.V),
+            out.data_ptr(), _dptr(lse), workspace.data_ptr(),
+            _raw_stream(device) if stream is None else _stream(stream)))
 
     def check_device_error(self, workspace, stream=None) -> int:
         code = ctypes.c_int()
