@@ -4,13 +4,14 @@
 //
 // WEIGHTS plans: the product is taken transposed, S^T = K Q^T: 128 keys are the rows of the MMA and
 // tensor-memory lanes, so a thread owns a key and adds up its weights over a block's query rows (up to
-// 128: tokens x the group's heads) in registers, with no reduction across lanes.  Two groups of four
-// warps halve the columns of a block, so that each SM sub-partition has two warps to hide latencies.
-// One CTA per SM walks items (kv heads or query blocks of one tile, planned to an eighth of an SM's
-// share) with its rings running on across them; an item's sums go to its part, and the finishing
-// kernel adds a tile's parts in order.  K is read once from HBM, Q blocks come from L2.  Few query
-// rows: bounded by K's bytes.  Many: by the exponentials (16 a cycle and SM: 1,024 cycles a block,
-// against 512 of its MMAs at head_dim 128).
+// 128: tokens x the group's heads) in registers, with no reduction across lanes.  Two teams of four
+// warps take the blocks in turn, each with its own S buffer, so that one's loads and waits run under the
+// other's exponentials.  One CTA per SM walks items (kv heads or query blocks of one tile, planned to an
+// eighth of an SM's share) with its rings running on across them; a team's sums of an item go to a part
+// of their own, and the finishing kernel adds a tile's parts in order.  K is read once from HBM (four
+// warps issue its copies: a page and 64 columns each, some 50 cycles an instruction), Q blocks come
+// from L2.  Few query rows: bounded by K's bytes.  Many: by the exponentials (16 a cycle and SM: 1,024
+// cycles a block, against 512 of its MMAs at head_dim 128).
 //
 // DECODE_WEIGHTS plans: the decode kernel has left its logits; a thread per key adds the weights.
 #include <cuda.h>
@@ -26,7 +27,9 @@
 namespace pkv {
 namespace dev {
 
-constexpr int kWtThreads = 320;  // warps 0-7: a key a thread and half the columns; 8: copies; 9: MMAs
+// warps 0-3 and 4-7: the two teams, a key a thread; 8-11: copies of K; 12: copies of Q; 13: MMAs
+constexpr int kWtThreads = 448;
+constexpr int kWtProducers = 4;
 constexpr float kWtLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -38,10 +41,9 @@ struct WtSmem {
     static constexpr uint32_t K_OFF = 0;
     static constexpr uint32_t Q_OFF = KS * TILE;
     static constexpr uint32_t BAR_OFF = Q_OFF + QS * TILE;
-    // per buffer and block column: -lse (base 2), first and last key; then the halves' exchange
+    // per team and block column: -lse (base 2), first and last key
     static constexpr uint32_t COL_OFF = BAR_OFF + 256;
-    static constexpr uint32_t SUM_OFF = COL_OFF + 2 * 3 * 128 * 4;
-    static constexpr uint32_t BYTES = SUM_OFF + 2 * 128 * 4;
+    static constexpr uint32_t BYTES = COL_OFF + 2 * 3 * 128 * 4;
 };
 static_assert(1024 + WtSmem<256>::BYTES <= 227 * 1024, "the weights kernel fits shared memory");
 
@@ -51,7 +53,7 @@ struct WeightsArgs {
     const int32_t *pages;
     PlanHeader *hdr;
     const float *lse;
-    float *part;  // [item][128]
+    float *part;  // [item][team][128]
     int num_items, num_qo_heads, group;
     int page_size, page_shift, box_rows, box_tokens, oob_row;
 };
@@ -74,16 +76,16 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int P = a.page_size, G = a.group, bt = a.box_tokens;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&k_full[s], 1);
+            mbar_init(&k_full[s], kWtProducers);
             mbar_init(&k_empty[s], 1);
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1);
-            mbar_init(&s_empty[s], 8);
+            mbar_init(&s_empty[s], 4);
         }
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == 13) {
         tmem_alloc(tmem_holder, 256);
         tmem_relinquish();
     }
@@ -94,21 +96,24 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     griddep_launch();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp == 8) {
-        // ------------------------------------------------ copies
-        const int R = a.box_rows, jobs = kWeightKeys / R * L::CHUNKS;  // a box is one page run of one chunk
-        const uint32_t q_bytes = (uint32_t)(bt * G) * 128u * L::CHUNKS;
-        if (lane == 0) {
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_q);
-        }
-        uint32_t it = 0, kc = 0;
+    if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------ copies of K: a box is one page run of one chunk
+        const int R = a.box_rows, jobs = kWeightKeys / R * L::CHUNKS;      // 1 to 64
+        const int per = (jobs + kWtProducers - 1) / kWtProducers;           // at most 16 a warp, one a lane
+        const int job = (warp - 8) * per + lane;
+        const bool copies = lane < per && job < jobs;
+        const uint32_t bytes = (uint32_t)max(0, min(per, jobs - (warp - 8) * per)) * R * 128u;
+        if (warp == 8 && lane == 0) prefetch_tmap(&tm_k);
+        uint32_t kc = 0;
         bool ok = true;
         for (int n = blockIdx.x; n < a.num_items && ok; n += gridDim.x) {
             const WeightsItem w = a.items[n];
             const WeightsTile t = a.tiles[w.tile];
-            const int npages = (t.length + P - 1) >> a.page_shift;
-            for (int h = 0; h < w.nh && ok; ++h, ++kc) {
+            const int kb = t.key0 + job / L::CHUNKS * R, pg = kb >> a.page_shift;
+            const int row = copies && pg < ((t.length + P - 1) >> a.page_shift)
+                                ? a.pages[t.kv_base + pg] * 2 * P + (kb & (P - 1))
+                                : a.oob_row;
+            for (int h = 0; h < w.nh; ++h, ++kc) {
                 const int ks = kc % L::KS;
                 const uint32_t use = kc / L::KS;
                 ok = use == 0 || mbar_wait(&k_empty[ks], (use - 1) & 1, err, kErrWaitEmpty);
@@ -116,41 +121,43 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], L::TILE);
+                if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
                 __syncwarp();
-                for (int j = lane; j < jobs; j += 32) {
-                    const int b = j / L::CHUNKS, c = j % L::CHUNKS;
-                    const int kb = t.key0 + b * R, pg = kb >> a.page_shift;
-                    const int row = pg < npages ? a.pages[t.kv_base + pg] * 2 * P + (kb & (P - 1)) : a.oob_row;
-                    tma_load_3d(sm + L::K_OFF + ks * L::TILE + c * L::CHUNK + b * R * 128, &tm_k, &k_full[ks], c * 64,
-                                row, w.h0 + h);
-                }
-                for (int b = 0; b < w.blocks; ++b, ++it) {
-                    const int s = it & 1;
-                    ok = it < 2 || mbar_wait(&q_empty[s], ((it >> 1) - 1) & 1, err, kErrWaitEmpty);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&q_full[s], q_bytes);
-                        for (int c = 0; c < L::CHUNKS; ++c)
-                            tma_load_3d(sm + L::Q_OFF + s * L::TILE + c * L::CHUNK, &tm_q, &q_full[s], c * 64,
-                                        (w.h0 + h) * G, t.q_begin + w.i0 + b * bt);
-                    }
-                    __syncwarp();
-                }
+                if (copies)
+                    tma_load_3d(sm + L::K_OFF + ks * L::TILE + job % L::CHUNKS * L::CHUNK + job / L::CHUNKS * R * 128, &tm_k,
+                                &k_full[ks], job % L::CHUNKS * 64, row, w.h0 + h);
             }
         }
         // copies in flight land before the CTA may end (they have, unless a wait gave up)
         if (!ok)
-            for (int s = 0; s < 2; ++s) {
-                for (int p = 0; p < 2; ++p) {
-                    mbar_wait(&q_full[s], p, nullptr, 0, 1u << 16);
-                    if (s < L::KS) mbar_wait(&k_full[s], p, nullptr, 0, 1u << 16);
-                }
+            for (int s = 0; s < L::KS; ++s)
+                for (int p = 0; p < 2; ++p) mbar_wait(&k_full[s], p, nullptr, 0, 1u << 16);
+    } else if (warp == 12) {
+        // ------------------------------------------------ copies of Q blocks
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            const uint32_t bytes = (uint32_t)(bt * G) * 128u * L::CHUNKS;
+            uint32_t it = 0;
+            bool ok = true;
+            for (int n = blockIdx.x; n < a.num_items && ok; n += gridDim.x) {
+                const WeightsItem w = a.items[n];
+                const int q_begin = a.tiles[w.tile].q_begin + w.i0;
+                for (int h = 0; h < w.nh && ok; ++h)
+                    for (int b = 0; b < w.blocks; ++b, ++it) {
+                        const int s = it & 1;
+                        ok = it < 2 || mbar_wait(&q_empty[s], ((it >> 1) - 1) & 1, err, kErrWaitEmpty);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&q_full[s], bytes);
+                        for (int c = 0; c < L::CHUNKS; ++c)
+                            tma_load_3d(sm + L::Q_OFF + s * L::TILE + c * L::CHUNK, &tm_q, &q_full[s], c * 64,
+                                        (w.h0 + h) * G, q_begin + b * bt);
+                    }
             }
-    } else if (warp == 9) {
+            if (!ok)
+                for (int s = 0; s < 2; ++s)
+                    for (int p = 0; p < 2; ++p) mbar_wait(&q_full[s], p, nullptr, 0, 1u << 16);
+        }
+    } else if (warp == 13) {
         // ------------------------------------------------ S^T = K Q^T
         const uint32_t ncol = (uint32_t)(bt * G + 15) & ~15u;
         const uint32_t id = idesc_bf16_f32(128, 0, 0, 0) | ((ncol >> 3) << 17);
@@ -184,68 +191,59 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (!ok)  // a wait gave up: let the MMAs in flight finish before the tensor memory is released
             for (uint32_t i = 0; i < 1024; ++i) __nanosleep(1000);
     } else {
-        // ------------------------------------------------ a key a thread
-        const int half = warp >> 2, m = threadIdx.x & 127;  // the key; group 0 also fetches column m's lse
-        const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64u * half;
+        // ------------------------------------------------ the teams: a key a thread
+        const int team = warp >> 2, m = threadIdx.x & 127;  // the key, and the block column whose lse it fetches
+        const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * team;
         const float sl = a.hdr->scale_log2;
         const uint64_t sl2 = f2_make(sl, sl);
         const int causal = a.hdr->causal, window = a.hdr->window_left;
-        float *const sums = reinterpret_cast<float *>(sm + L::SUM_OFF);
-        uint32_t it = 0, seq = 0;
+        float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + team * 384;
+        int *const c_lo = reinterpret_cast<int *>(c_ls) + 128, *const c_hi = c_lo + 128;
+        uint32_t it0 = 0;  // blocks before this item
         // a wait that gives up clears ok; the warps still walk their blocks, without further waits, so
         // that they keep meeting at their barriers (which have no time limit)
         bool ok = true;
-        for (int n = blockIdx.x; n < a.num_items; n += gridDim.x, ++seq) {
+        for (int n = blockIdx.x; n < a.num_items; n += gridDim.x) {
             const WeightsItem w = a.items[n];
             const WeightsTile t = a.tiles[w.tile];
             const int key = t.key0 + m, total_blocks = w.nh * w.blocks;
             // column m of block g (of the item's heads x blocks)
             float nls = 0.f;
             int lo = 0, hi = -1;
-            auto fetch = [&](int h, int b) {
-                const int i = w.i0 + b * bt + m / G;
+            auto fetch = [&](int g) {
+                const int h = g / w.blocks, i = w.i0 + (g - h * w.blocks) * bt + m / G;
                 const bool valid = m < bt * G && i < w.i1;
                 const int pos = t.new_begin + i;
                 nls = valid ? -a.lse[(size_t)(t.q_begin + i) * a.num_qo_heads + (w.h0 + h) * G + m % G] * kWtLog2e : 0.f;
                 lo = window >= 0 ? max(0, pos - window) : 0;
                 hi = valid ? (causal ? pos : t.length - 1) : -1;
             };
-            if (half == 0) fetch(0, 0);
+            int g = (it0 & 1) == team ? 0 : 1;  // this team's blocks: every other one
+            if (g < total_blocks) fetch(g);
             float total = 0.f;
-            int h = 0, b = 0;
-            for (int g = 0; g < total_blocks; ++g, ++it) {
-                const int s = it & 1;
-                float *c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + s * 384;
-                int *c_lo = reinterpret_cast<int *>(c_ls) + 128, *c_hi = c_lo + 128;
-                const int ncols = min(bt, w.i1 - w.i0 - b * bt) * G;
-                // whether every column of the block sees every key of the tile: no masks then
-                unsigned mine = 1, all;
-                if (half == 0) {
-                    c_ls[m] = nls;
+            for (; g < total_blocks; g += 2) {
+                const uint32_t it = it0 + g;
+                const int i_first = w.i0 + g % w.blocks * bt, i_count = min(bt, w.i1 - i_first);
+                const int ncols = i_count * G, pos0 = t.new_begin + i_first;
+                // every column of the block sees every key of the tile: no masks then
+                const bool all = t.key0 + kWeightKeys <= t.length && (!causal || pos0 >= t.key0 + kWeightKeys - 1) &&
+                                 (window < 0 || pos0 + i_count - 1 - window <= t.key0);
+                named_barrier_sync(1 + team, 128);  // the block before has been read
+                c_ls[m] = nls;
+                if (!all || (ncols & 31)) {
                     c_lo[m] = lo;
                     c_hi[m] = hi;
-                    mine = m >= ncols || (lo <= t.key0 && hi >= t.key0 + kWeightKeys - 1);
                 }
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 256, p;\n\t"
-                             "selp.u32 %0, 1, 0, q;\n\t}"
-                             : "=r"(all)
-                             : "r"(mine)
-                             : "memory");
-                if (++b == w.blocks) {
-                    b = 0;
-                    ++h;
-                }
-                if (half == 0 && g + 1 < total_blocks) fetch(h, b);
-                ok = ok && mbar_wait(&s_full[s], (it >> 1) & 1, err, kErrWaitFull);
+                named_barrier_sync(1 + team, 128);
+                if (g + 2 < total_blocks) fetch(g + 2);
+                ok = ok && mbar_wait(&s_full[team], (it >> 1) & 1, err, kErrWaitFull);
                 __syncwarp();
                 tc_fence_after();
                 uint64_t acc[4] = {0, 0, 0, 0};
-                const int cols = max(0, min(64, ncols - 64 * half));
-                const int c_first = 64 * half;
                 auto take = [&](const uint32_t (&r)[32], int c0, bool masked) {
-                    const ulonglong2 *ls2 = reinterpret_cast<const ulonglong2 *>(c_ls + c_first + c0);
-                    const int4 *lo4 = reinterpret_cast<const int4 *>(c_lo + c_first + c0);
-                    const int4 *hi4 = reinterpret_cast<const int4 *>(c_hi + c_first + c0);
+                    const ulonglong2 *ls2 = reinterpret_cast<const ulonglong2 *>(c_ls + c0);
+                    const int4 *lo4 = reinterpret_cast<const int4 *>(c_lo + c0);
+                    const int4 *hi4 = reinterpret_cast<const int4 *>(c_hi + c0);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const ulonglong2 l = ls2[c];
@@ -264,38 +262,37 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         acc[(2 * c + 1) & 3] = fadd2(acc[(2 * c + 1) & 3], f2_make(ex2_ftz(x2), ex2_ftz(x3)));
                     }
                 };
-                if (cols > 0) {
+                const bool masked = !all || (ncols & 31);  // columns past the block's are masked too
+#pragma unroll 1
+                for (int c0 = 0; c0 < ncols; c0 += 64) {
                     uint32_t r0[32], r1[32];
-                    tmem_ld32(s_lane + 128u * s, r0);
-                    if (cols > 32) tmem_ld32(s_lane + 128u * s + 32, r1);
+                    const bool more = c0 + 32 < ncols;
+                    tmem_ld32(s_lane + c0, r0);
+                    if (more) tmem_ld32(s_lane + c0 + 32, r1);
                     tmem_wait_ld();
-                    const bool masked = !all || (cols & 31);  // columns past the block's are masked too
                     if (masked) {
-                        take(r0, 0, true);
-                        if (cols > 32) take(r1, 32, true);
+                        take(r0, c0, true);
+                        if (more) take(r1, c0 + 32, true);
                     } else {
-                        take(r0, 0, false);
-                        if (cols > 32) take(r1, 32, false);
+                        take(r0, c0, false);
+                        if (more) take(r1, c0 + 32, false);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[s]);
+                if (lane == 0) mbar_arrive(&s_empty[team]);
                 float u0, u1;
                 f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u0, u1);
                 total += u0 + u1;
             }
-            // the two halves' sums; two exchange buffers, so one barrier an item
-            float *x = sums + (seq & 1) * 128;
-            if (half == 1) x[m] = total;
-            named_barrier_sync(2, 256);
-            if (half == 0) a.part[(size_t)w.part * kWeightKeys + m] = total + x[m];
+            a.part[((size_t)w.part * 2 + team) * kWeightKeys + m] = total;
+            it0 += total_blocks;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 256);
+    if (warp == 13) tmem_dealloc(tmem, 256);
 }
 
 __device__ __forceinline__ void put_score(const WeightsTile &t, const int32_t *pages, int page_size, int page_shift, int key,
@@ -304,17 +301,33 @@ __device__ __forceinline__ void put_score(const WeightsTile &t, const int32_t *p
     scores[slot] = (decay != 0.f && key < t.new_begin ? decay * scores[slot] : 0.f) + w;
 }
 
-__global__ void __launch_bounds__(kWeightKeys) weights_finish_kernel(const WeightsTile *tiles, const int32_t *pages,
-                                                                     const float *part, int page_size, int page_shift,
-                                                                     float *scores, float decay) {
+// A tile's parts: a CTA of 128 keys x 8 slices, a thread adding every eighth part of its key, eight in
+// flight, the slices joined in order.
+constexpr int kWtSlices = 8;
+__global__ void __launch_bounds__(kWeightKeys * kWtSlices) weights_finish_kernel(const WeightsTile *tiles,
+                                                                                 const int32_t *pages, const float *part,
+                                                                                 int page_size, int page_shift,
+                                                                                 float *scores, float decay) {
+    __shared__ float sums[kWtSlices][kWeightKeys];
     const WeightsTile t = tiles[blockIdx.x];
-    const int key = t.key0 + threadIdx.x;
+    const int m = threadIdx.x % kWeightKeys, slice = threadIdx.x / kWeightKeys, key = t.key0 + m;
     griddep_wait();
     griddep_launch();
-    if (key >= t.length) return;
+    const float *p = part + (size_t)t.first * 2 * kWeightKeys + m;
+    const int n = 2 * t.base;
     float w = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < t.base; ++i) w += __ldcg(part + (size_t)(t.first + i) * kWeightKeys + threadIdx.x);
+    for (int i0 = slice; i0 < n; i0 += 8 * kWtSlices) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i0 + i * kWtSlices < n ? __ldcg(p + (size_t)(i0 + i * kWtSlices) * kWeightKeys) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w += x[i];
+    }
+    sums[slice][m] = w;
+    __syncthreads();
+    if (slice || key >= t.length) return;
+#pragma unroll
+    for (int i = 1; i < kWtSlices; ++i) w += sums[i][m];
     put_score(t, pages, page_size, page_shift, key, w, scores, decay);
 }
 
@@ -386,7 +399,7 @@ cudaError_t launch_weights(const Shape &s, const Plan &p, const WeightsPlan &wp,
                     : s.head_dim == 128 ? launch_weights_t<128>(tm_k, tm_q, a, grid, st)
                                         : launch_weights_t<256>(tm_k, tm_q, a, grid, st);
     if (e != cudaSuccess) return e;
-    return launch_pdl(dev::weights_finish_kernel, dim3(wp.tiles), dim3(kWeightKeys), 0, st, a.tiles, a.pages,
+    return launch_pdl(dev::weights_finish_kernel, dim3(wp.tiles), dim3(kWeightKeys * dev::kWtSlices), 0, st, a.tiles, a.pages,
                       static_cast<const float *>(a.part), s.page_size, s.page_shift(), scores, decay);
 }
 
