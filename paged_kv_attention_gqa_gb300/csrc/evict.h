@@ -31,11 +31,13 @@ struct WeightsTile {
 static_assert(sizeof(WeightsTile) == 32, "WeightsTile is 8 ints");
 
 // Work of one CTA at a time (WEIGHTS): kv heads [h0, h0 + nh) of a tile with the query tokens
-// [i0, i1) of its row, in `blocks` blocks.
-struct WeightsItem {
-    int32_t tile, h0, nh, i0, i1, blocks, part, pad;
+// [i0, i1) of its row, in `blocks` blocks; with the tile's own numbers, so that one load tells all.
+struct alignas(16) WeightsItem {
+    int32_t kv_base, length, key0, new_begin;
+    int32_t q_begin, h0, nh, blocks;
+    int32_t i0, i1, part, pad;
 };
-static_assert(sizeof(WeightsItem) == 32, "WeightsItem is 8 ints");
+static_assert(sizeof(WeightsItem) == 48, "WeightsItem is 12 ints");
 
 struct WeightsPlan {
     size_t off_pages = 0, off_tiles = 0, off_items = 0, off_part = 0;  // in the workspace

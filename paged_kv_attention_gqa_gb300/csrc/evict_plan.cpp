@@ -56,7 +56,9 @@ static void weight_items(const Shape &s, int causal, int window, int bt, std::ve
         const Range &r = ranges[t];
         tiles[t].first = (int)items.size();
         auto add = [&](int h0, int nh, int a, int b) {
-            items.push_back(WeightsItem{(int)t, h0, nh, a, b, (b - a + bt - 1) / bt, (int)items.size(), 0});
+            const WeightsTile &w = tiles[t];
+            items.push_back(WeightsItem{w.kv_base, w.length, w.key0, w.new_begin, w.q_begin, h0, nh, (b - a + bt - 1) / bt,
+                                        a, b, (int)items.size(), 0});
         };
         if (r.nb > 0 && r.nb <= cap) {
             const int nh = std::min(s.num_kv_heads, cap / r.nb);

@@ -8,7 +8,7 @@
 // warps take the blocks in turn, each with its own S buffer, so that one's loads and waits run under the
 // other's exponentials.  One CTA per SM walks items (kv heads or query blocks of one tile, planned to an
 // eighth of an SM's share) with its rings running on across them; a team's sums of an item go to a part
-// of their own, and the finishing kernel adds a tile's parts in order.  K is read once from HBM (four
+// of their own, and the finishing kernel adds a tile's parts in order.  K is read once from HBM (two
 // warps issue its copies: a page and 64 columns each, some 50 cycles an instruction), Q blocks come
 // from L2.  Few query rows: bounded by K's bytes.  Many: by the exponentials (16 a cycle and SM: 1,024
 // cycles a block, against 512 of its MMAs at head_dim 128).
@@ -27,9 +27,9 @@
 namespace pkv {
 namespace dev {
 
-// warps 0-3 and 4-7: the two teams, a key a thread; 8-11: copies of K; 12: copies of Q; 13: MMAs
-constexpr int kWtThreads = 448;
-constexpr int kWtProducers = 4;
+// warps 0-3 and 4-7: the two teams, a key a thread; 8, 9: copies of K; 10: copies of Q; 11: MMAs
+constexpr int kWtThreads = 384;
+constexpr int kWtProducers = 2;
 constexpr float kWtLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -37,18 +37,17 @@ struct WtSmem {
     static constexpr int CHUNKS = D / 64;
     static constexpr uint32_t CHUNK = 128 * 128;  // 128 rows x 64 columns
     static constexpr uint32_t TILE = CHUNKS * CHUNK;
-    static constexpr int KS = D == 256 ? 1 : 2, QS = 2;  // ring stages of K tiles and of Q blocks
+    static constexpr int KS = D == 256 ? 1 : 4, QS = 2;  // ring stages of K tiles and of Q blocks
     static constexpr uint32_t K_OFF = 0;
     static constexpr uint32_t Q_OFF = KS * TILE;
     static constexpr uint32_t BAR_OFF = Q_OFF + QS * TILE;
-    // per team and block column: -lse (base 2), first and last key
+    // per team, buffer and block column: -lse (base 2), first and last key
     static constexpr uint32_t COL_OFF = BAR_OFF + 256;
-    static constexpr uint32_t BYTES = COL_OFF + 2 * 3 * 128 * 4;
+    static constexpr uint32_t BYTES = COL_OFF + 2 * 2 * 3 * 128 * 4;
 };
 static_assert(1024 + WtSmem<256>::BYTES <= 227 * 1024, "the weights kernel fits shared memory");
 
 struct WeightsArgs {
-    const WeightsTile *tiles;
     const WeightsItem *items;
     const int32_t *pages;
     PlanHeader *hdr;
@@ -57,6 +56,46 @@ struct WeightsArgs {
     int num_items, num_qo_heads, group;
     int page_size, page_shift, box_rows, box_tokens, oob_row;
 };
+
+// Add the weights of 32 columns (below: `ncols`) of this thread's key to acc: 2^(s sl - lse), with MASKED
+// only where c_lo <= key <= c_hi.
+template <bool MASKED>
+__device__ __forceinline__ void take_columns(uint64_t (&acc)[4], const uint32_t (&r)[32], int key, uint64_t sl2,
+                                             const float *c_ls, const int *c_lo, const int *c_hi) {
+    const ulonglong2 *ls2 = reinterpret_cast<const ulonglong2 *>(c_ls);
+    const int4 *lo4 = reinterpret_cast<const int4 *>(c_lo), *hi4 = reinterpret_cast<const int4 *>(c_hi);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const ulonglong2 l = ls2[c];
+        float x0, x1, x2, x3;
+        f2_split(ffma2(f2_make(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])), sl2, l.x), x0, x1);
+        f2_split(ffma2(f2_make(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])), sl2, l.y), x2, x3);
+        if constexpr (MASKED) {  // selects, not products: a masked score may be NaN
+            const int4 a4 = lo4[c], b4 = hi4[c];
+            x0 = (key >= a4.x) & (key <= b4.x) ? x0 : -INFINITY;
+            x1 = (key >= a4.y) & (key <= b4.y) ? x1 : -INFINITY;
+            x2 = (key >= a4.z) & (key <= b4.z) ? x2 : -INFINITY;
+            x3 = (key >= a4.w) & (key <= b4.w) ? x3 : -INFINITY;
+        }
+        acc[(2 * c) & 3] = fadd2(acc[(2 * c) & 3], f2_make(ex2_ftz(x0), ex2_ftz(x1)));
+        acc[(2 * c + 1) & 3] = fadd2(acc[(2 * c + 1) & 3], f2_make(ex2_ftz(x2), ex2_ftz(x3)));
+    }
+}
+
+template <bool MASKED>
+__device__ __forceinline__ void add_columns(uint64_t (&acc)[4], uint32_t s_lane, int ncols, int key, uint64_t sl2,
+                                            const float *c_ls, const int *c_lo, const int *c_hi) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < ncols; c0 += 64) {
+        uint32_t r0[32], r1[32];
+        const bool more = c0 + 32 < ncols;
+        tmem_ld32(s_lane + c0, r0);
+        if (more) tmem_ld32(s_lane + c0 + 32, r1);
+        tmem_wait_ld();
+        take_columns<MASKED>(acc, r0, key, sl2, c_ls + c0, c_lo + c0, c_hi + c0);
+        if (more) take_columns<MASKED>(acc, r1, key, sl2, c_ls + c0 + 32, c_lo + c0 + 32, c_hi + c0 + 32);
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kWtThreads, 1)
@@ -67,17 +106,19 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR_OFF);
     // K tiles are counted over the CTA's items (kc: one per item and head), blocks too (it)
-    uint64_t *k_full = bars + 0, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 6;  // [2] each
-    uint64_t *s_full = bars + 8, *s_empty = bars + 10;                                          // [2] each
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 12);
+    uint64_t *k_full = bars + 0, *k_empty = bars + 4;                                              // [KS] each
+    uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *s_empty = bars + 14;  // [2] each
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 16);
 
     int *const err = &a.hdr->err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = a.page_size, G = a.group, bt = a.box_tokens;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < L::KS; ++s) {
             mbar_init(&k_full[s], kWtProducers);
             mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 1);
             mbar_init(&s_full[s], 1);
@@ -85,7 +126,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         fence_barrier_init();
     }
-    if (warp == 13) {
+    if (warp == 11) {
         tmem_alloc(tmem_holder, 256);
         tmem_relinquish();
     }
@@ -96,23 +137,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     griddep_launch();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp >= 8 && warp < 12) {
+    if (warp == 8 || warp == 9) {
         // ------------------------------------------------ copies of K: a box is one page run of one chunk
         const int R = a.box_rows, jobs = kWeightKeys / R * L::CHUNKS;      // 1 to 64
-        const int per = (jobs + kWtProducers - 1) / kWtProducers;           // at most 16 a warp, one a lane
+        const int per = (jobs + kWtProducers - 1) / kWtProducers;           // at most 32 a warp, one a lane
         const int job = (warp - 8) * per + lane;
         const bool copies = lane < per && job < jobs;
         const uint32_t bytes = (uint32_t)max(0, min(per, jobs - (warp - 8) * per)) * R * 128u;
         if (warp == 8 && lane == 0) prefetch_tmap(&tm_k);
         uint32_t kc = 0;
         bool ok = true;
+        WeightsItem w = a.items[blockIdx.x];
         for (int n = blockIdx.x; n < a.num_items && ok; n += gridDim.x) {
-            const WeightsItem w = a.items[n];
-            const WeightsTile t = a.tiles[w.tile];
-            const int kb = t.key0 + job / L::CHUNKS * R, pg = kb >> a.page_shift;
-            const int row = copies && pg < ((t.length + P - 1) >> a.page_shift)
-                                ? a.pages[t.kv_base + pg] * 2 * P + (kb & (P - 1))
+            const int kb = w.key0 + job / L::CHUNKS * R, pg = kb >> a.page_shift;
+            const int row = copies && pg < ((w.length + P - 1) >> a.page_shift)
+                                ? a.pages[w.kv_base + pg] * 2 * P + (kb & (P - 1))
                                 : a.oob_row;
+            const WeightsItem next = a.items[min(n + (int)gridDim.x, a.num_items - 1)];  // lands meanwhile
             for (int h = 0; h < w.nh; ++h, ++kc) {
                 const int ks = kc % L::KS;
                 const uint32_t use = kc / L::KS;
@@ -127,21 +168,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     tma_load_3d(sm + L::K_OFF + ks * L::TILE + job % L::CHUNKS * L::CHUNK + job / L::CHUNKS * R * 128, &tm_k,
                                 &k_full[ks], job % L::CHUNKS * 64, row, w.h0 + h);
             }
+            w = next;
         }
         // copies in flight land before the CTA may end (they have, unless a wait gave up)
         if (!ok)
             for (int s = 0; s < L::KS; ++s)
                 for (int p = 0; p < 2; ++p) mbar_wait(&k_full[s], p, nullptr, 0, 1u << 16);
-    } else if (warp == 12) {
+    } else if (warp == 10) {
         // ------------------------------------------------ copies of Q blocks
         if (lane == 0) {
             prefetch_tmap(&tm_q);
             const uint32_t bytes = (uint32_t)(bt * G) * 128u * L::CHUNKS;
             uint32_t it = 0;
             bool ok = true;
+            WeightsItem w = a.items[blockIdx.x];
             for (int n = blockIdx.x; n < a.num_items && ok; n += gridDim.x) {
-                const WeightsItem w = a.items[n];
-                const int q_begin = a.tiles[w.tile].q_begin + w.i0;
+                const WeightsItem next = a.items[min(n + (int)gridDim.x, a.num_items - 1)];
+                const int q_begin = w.q_begin + w.i0;
                 for (int h = 0; h < w.nh && ok; ++h)
                     for (int b = 0; b < w.blocks; ++b, ++it) {
                         const int s = it & 1;
@@ -152,12 +195,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                             tma_load_3d(sm + L::Q_OFF + s * L::TILE + c * L::CHUNK, &tm_q, &q_full[s], c * 64,
                                         (w.h0 + h) * G, q_begin + b * bt);
                     }
+                w = next;
             }
             if (!ok)
                 for (int s = 0; s < 2; ++s)
                     for (int p = 0; p < 2; ++p) mbar_wait(&q_full[s], p, nullptr, 0, 1u << 16);
         }
-    } else if (warp == 13) {
+    } else if (warp == 11) {
         // ------------------------------------------------ S^T = K Q^T
         const uint32_t ncol = (uint32_t)(bt * G + 15) & ~15u;
         const uint32_t id = idesc_bf16_f32(128, 0, 0, 0) | ((ncol >> 3) << 17);
@@ -166,8 +210,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         auto add = [](uint64_t d, uint32_t off) { return d + (off >> 4); };
         uint32_t it = 0, kc = 0;
         bool ok = true;
+        int nh = a.items[blockIdx.x].nh, blocks = a.items[blockIdx.x].blocks;
         for (int n = blockIdx.x; n < a.num_items && ok; n += gridDim.x) {
-            const int nh = a.items[n].nh, blocks = a.items[n].blocks;
+            const WeightsItem &next = a.items[min(n + (int)gridDim.x, a.num_items - 1)];
+            const int next_nh = next.nh, next_blocks = next.blocks;
             for (int h = 0; h < nh && ok; ++h, ++kc) {
                 const int ks = kc % L::KS;
                 ok = mbar_wait(&k_full[ks], (kc / L::KS) & 1, err, kErrWaitFull);
@@ -187,6 +233,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 }
                 if (ok) mma_commit_elect(&k_empty[ks]);
             }
+            nh = next_nh;
+            blocks = next_blocks;
         }
         if (!ok)  // a wait gave up: let the MMAs in flight finish before the tensor memory is released
             for (uint32_t i = 0; i < 1024; ++i) __nanosleep(1000);
@@ -197,87 +245,65 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const float sl = a.hdr->scale_log2;
         const uint64_t sl2 = f2_make(sl, sl);
         const int causal = a.hdr->causal, window = a.hdr->window_left;
-        float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + team * 384;
-        int *const c_lo = reinterpret_cast<int *>(c_ls) + 128, *const c_hi = c_lo + 128;
-        uint32_t it0 = 0;  // blocks before this item
+        const int m_tok = m / G, m_head = m % G;
+        uint32_t it0 = 0, seq = 0;  // blocks before this item; blocks this team has taken
         // a wait that gives up clears ok; the warps still walk their blocks, without further waits, so
         // that they keep meeting at their barriers (which have no time limit)
         bool ok = true;
+        // column m of a block (number g of an item's heads x blocks), fetched one block ahead; its lse is not
+        // touched before it is stored, so that the fetch does not wait for it
+        float ls = 0.f;
+        int lo = 0, hi = -1;
+        auto fetch = [&](const WeightsItem &w, int g) {
+            const int h = w.blocks == 1 ? g : g / w.blocks, i = w.i0 + (g - h * w.blocks) * bt + m_tok;
+            const bool valid = m < bt * G && i < w.i1;
+            const int pos = w.new_begin + i;
+            ls = 0.f;
+            if (valid) ls = a.lse[(size_t)(w.q_begin + i) * a.num_qo_heads + (w.h0 + h) * G + m_head];
+            lo = window >= 0 ? max(0, pos - window) : 0;
+            hi = valid ? (causal ? pos : w.length - 1) : -1;
+        };
+        WeightsItem w = a.items[blockIdx.x];
+        int g = team;  // this team's blocks: every other one
+        if (g < w.nh * w.blocks) fetch(w, g);
         for (int n = blockIdx.x; n < a.num_items; n += gridDim.x) {
-            const WeightsItem w = a.items[n];
-            const WeightsTile t = a.tiles[w.tile];
-            const int key = t.key0 + m, total_blocks = w.nh * w.blocks;
-            // column m of block g (of the item's heads x blocks)
-            float nls = 0.f;
-            int lo = 0, hi = -1;
-            auto fetch = [&](int g) {
-                const int h = g / w.blocks, i = w.i0 + (g - h * w.blocks) * bt + m / G;
-                const bool valid = m < bt * G && i < w.i1;
-                const int pos = t.new_begin + i;
-                nls = valid ? -a.lse[(size_t)(t.q_begin + i) * a.num_qo_heads + (w.h0 + h) * G + m % G] * kWtLog2e : 0.f;
-                lo = window >= 0 ? max(0, pos - window) : 0;
-                hi = valid ? (causal ? pos : t.length - 1) : -1;
-            };
-            int g = (it0 & 1) == team ? 0 : 1;  // this team's blocks: every other one
-            if (g < total_blocks) fetch(g);
+            const int key = w.key0 + m, total_blocks = w.nh * w.blocks;
+            const bool last = n + (int)gridDim.x >= a.num_items;
+            const WeightsItem next = a.items[last ? n : n + (int)gridDim.x];  // lands meanwhile
+            const int g_next = ((it0 + total_blocks) & 1) == (uint32_t)team ? 0 : 1;
+            bool fetched = false;
             float total = 0.f;
-            for (; g < total_blocks; g += 2) {
+            for (; g < total_blocks; g += 2, ++seq) {
                 const uint32_t it = it0 + g;
-                const int i_first = w.i0 + g % w.blocks * bt, i_count = min(bt, w.i1 - i_first);
-                const int ncols = i_count * G, pos0 = t.new_begin + i_first;
+                const int i_first = w.i0 + (w.blocks == 1 ? 0 : g % w.blocks) * bt, i_count = min(bt, w.i1 - i_first);
+                const int ncols = i_count * G, pos0 = w.new_begin + i_first;
                 // every column of the block sees every key of the tile: no masks then
-                const bool all = t.key0 + kWeightKeys <= t.length && (!causal || pos0 >= t.key0 + kWeightKeys - 1) &&
-                                 (window < 0 || pos0 + i_count - 1 - window <= t.key0);
-                named_barrier_sync(1 + team, 128);  // the block before has been read
-                c_ls[m] = nls;
+                const bool all = w.key0 + kWeightKeys <= w.length && (!causal || pos0 >= w.key0 + kWeightKeys - 1) &&
+                                 (window < 0 || pos0 + i_count - 1 - window <= w.key0);
+                // two buffers of columns, so one barrier a block: behind it the block before last has been read
+                float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + (team * 2 + (seq & 1)) * 384;
+                int *const c_lo = reinterpret_cast<int *>(c_ls) + 128, *const c_hi = c_lo + 128;
+                c_ls[m] = ls * -kWtLog2e;
                 if (!all || (ncols & 31)) {
                     c_lo[m] = lo;
                     c_hi[m] = hi;
                 }
                 named_barrier_sync(1 + team, 128);
-                if (g + 2 < total_blocks) fetch(g + 2);
+                if (g + 2 < total_blocks) {
+                    fetch(w, g + 2);
+                } else if (!last && g_next < next.nh * next.blocks) {
+                    fetch(next, g_next);
+                    fetched = true;
+                }
                 ok = ok && mbar_wait(&s_full[team], (it >> 1) & 1, err, kErrWaitFull);
                 __syncwarp();
                 tc_fence_after();
                 uint64_t acc[4] = {0, 0, 0, 0};
-                auto take = [&](const uint32_t (&r)[32], int c0, bool masked) {
-                    const ulonglong2 *ls2 = reinterpret_cast<const ulonglong2 *>(c_ls + c0);
-                    const int4 *lo4 = reinterpret_cast<const int4 *>(c_lo + c0);
-                    const int4 *hi4 = reinterpret_cast<const int4 *>(c_hi + c0);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const ulonglong2 l = ls2[c];
-                        float x0, x1, x2, x3;
-                        f2_split(ffma2(f2_make(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])), sl2, l.x), x0, x1);
-                        f2_split(ffma2(f2_make(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])), sl2, l.y), x2,
-                                 x3);
-                        if (masked) {  // selects, not products: a masked score may be NaN
-                            const int4 a4 = lo4[c], b4 = hi4[c];
-                            x0 = (key >= a4.x) & (key <= b4.x) ? x0 : -INFINITY;
-                            x1 = (key >= a4.y) & (key <= b4.y) ? x1 : -INFINITY;
-                            x2 = (key >= a4.z) & (key <= b4.z) ? x2 : -INFINITY;
-                            x3 = (key >= a4.w) & (key <= b4.w) ? x3 : -INFINITY;
-                        }
-                        acc[(2 * c) & 3] = fadd2(acc[(2 * c) & 3], f2_make(ex2_ftz(x0), ex2_ftz(x1)));
-                        acc[(2 * c + 1) & 3] = fadd2(acc[(2 * c + 1) & 3], f2_make(ex2_ftz(x2), ex2_ftz(x3)));
-                    }
-                };
-                const bool masked = !all || (ncols & 31);  // columns past the block's are masked too
-#pragma unroll 1
-                for (int c0 = 0; c0 < ncols; c0 += 64) {
-                    uint32_t r0[32], r1[32];
-                    const bool more = c0 + 32 < ncols;
-                    tmem_ld32(s_lane + c0, r0);
-                    if (more) tmem_ld32(s_lane + c0 + 32, r1);
-                    tmem_wait_ld();
-                    if (masked) {
-                        take(r0, c0, true);
-                        if (more) take(r1, c0 + 32, true);
-                    } else {
-                        take(r0, c0, false);
-                        if (more) take(r1, c0 + 32, false);
-                    }
-                }
+                // columns past the block's are masked too
+                if (all && !(ncols & 31))
+                    add_columns<false>(acc, s_lane, ncols, key, sl2, c_ls, c_lo, c_hi);
+                else
+                    add_columns<true>(acc, s_lane, ncols, key, sl2, c_ls, c_lo, c_hi);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[team]);
@@ -287,12 +313,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
             a.part[((size_t)w.part * 2 + team) * kWeightKeys + m] = total;
             it0 += total_blocks;
+            g = g_next;
+            w = next;
+            if (!fetched && !last && g < w.nh * w.blocks) fetch(w, g);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 13) tmem_dealloc(tmem, 256);
+    if (warp == 11) tmem_dealloc(tmem, 256);
 }
 
 __device__ __forceinline__ void put_score(const WeightsTile &t, const int32_t *pages, int page_size, int page_shift, int key,
@@ -379,7 +408,7 @@ cudaError_t launch_weights(const Shape &s, const Plan &p, const WeightsPlan &wp,
     (void)p;
     uint8_t *w = static_cast<uint8_t *>(ws);
     dev::WeightsArgs a;
-    a.tiles = reinterpret_cast<const WeightsTile *>(w + wp.off_tiles);
+    const WeightsTile *tiles = reinterpret_cast<const WeightsTile *>(w + wp.off_tiles);
     a.pages = reinterpret_cast<const int32_t *>(w + wp.off_pages);
     a.hdr = reinterpret_cast<PlanHeader *>(w);
     a.lse = lse;
@@ -399,7 +428,7 @@ cudaError_t launch_weights(const Shape &s, const Plan &p, const WeightsPlan &wp,
                     : s.head_dim == 128 ? launch_weights_t<128>(tm_k, tm_q, a, grid, st)
                                         : launch_weights_t<256>(tm_k, tm_q, a, grid, st);
     if (e != cudaSuccess) return e;
-    return launch_pdl(dev::weights_finish_kernel, dim3(wp.tiles), dim3(kWeightKeys * dev::kWtSlices), 0, st, a.tiles, a.pages,
+    return launch_pdl(dev::weights_finish_kernel, dim3(wp.tiles), dim3(kWeightKeys * dev::kWtSlices), 0, st, tiles, a.pages,
                       static_cast<const float *>(a.part), s.page_size, s.page_shift(), scores, decay);
 }
 
