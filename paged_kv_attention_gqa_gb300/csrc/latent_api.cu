@@ -258,9 +258,9 @@ extern "C" pkv_status pkv_latent_run_dense(pkv_latent_t h, const void *q, const 
         const long long rd[2] = {pkv::kLatentRope, K}, rs[1] = {kr_token_stride};
         const long long vd[3] = {pkv::kLatentV, K, H}, vs[2] = {v_token_stride, v_head_stride};
         if ((st = encode(h, q, 3, qd, qs, 128, &tq)) != PKV_OK) return st;
-        if ((st = encode(h, k_nope, 3, kd, ks, 128, &tk)) != PKV_OK) return st;
-        if ((st = encode(h, k_rope, 2, rd, rs, 128, &tr)) != PKV_OK) return st;
-        if ((st = encode(h, v, 3, vd, vs, 128, &tv)) != PKV_OK) return st;
+        if ((st = encode(h, k_nope, 3, kd, ks, 64, &tk)) != PKV_OK) return st;
+        if ((st = encode(h, k_rope, 2, rd, rs, 64, &tr)) != PKV_OK) return st;
+        if ((st = encode(h, v, 3, vd, vs, 64, &tv)) != PKV_OK) return st;
         const cudaError_t e = pkv::launch_latent_dense(h->shape, h->plan, tq, tk, tr, tv, workspace, out, lse,
                                                        static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? PKV_OK : cuda_fail(h, e, "expanded latent launch");
