@@ -8,19 +8,18 @@
 //  * warp 8 copies Q0 and Q1 once, then streams the K tiles ([k_nope | k_rope], 24 KB) and the V tiles
 //    (16 KB) through three stages each; a stage is refilled as soon as the MMAs of both query tiles
 //    that read it are done;
-//  * warps 9 and 10 issue the MMAs of Q0 and Q1: S(j+1) = Q K^T (12 k-steps, N = 64) before
-//    O += P(j) V (4 k-steps, N = 128, P from tensor memory over its S), so that the next scores are
-//    there when the softmax of a tile ends;
+//  * warps 9 and 10 issue S = Q K^T of Q0 and Q1 (12 k-steps, N = 64), up to two tiles ahead of the
+//    softmax, warps 11 and 12 O += P V (4 k-steps, N = 128, P from tensor memory over its S);
 //  * warps 0-3 and 4-7 run the softmax of Q0 and Q1, a thread a query.  The running maximum moves, and
 //    O is rescaled, only when it grows by more than 2^8.
 // Tensor memory: two S buffers of 64 columns and an O of 128 for each query tile, all 512 columns.
 // Tiles of 128 keys leave room for one S each; then a query tile's S, softmax and PV wait for one
 // another, two chains of 4,600 cycles per 128 keys against 2,560 of MMAs: 305 us (32 heads, prompts of
 // 801 to 4,093 tokens, 9,788 in all, causal).  N = 64 costs 48 cycles a k-step of S (the A operand's
-// reads) in place of 32, 3,328 cycles per 128 keys: 271 us, 160 us being the operations at the measured
-// rate.  What is left is the MMA warps' own instructions: 33 cycles an MMA, 100 to 200 a commit or a
-// wait, even of a completed phase.  (Both query tiles from one warp: 412 us.  PV as two N = 64 halves:
-// 281 us.)
+// reads) in place of 32, 3,328 cycles per 128 keys.  A warp's MMA takes it 33 cycles to issue, a commit
+// or a wait, even for a completed phase, 100 to 200; so S and PV of both query tiles have a warp each:
+// 234 us, the operations at the measured rate being 160.  (One warp for S and PV of a query tile: 265
+// us, one for both query tiles: 412 us; PV as two N = 64 halves: + 10 us.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,11 +32,11 @@ namespace pkv {
 namespace dev {
 
 constexpr int kLdKeys = 64, kLdQueries = 128;
-constexpr int kLdThreads = 384;
-// Registers: 384 x 168 at launch = 64,512; the softmax groups take most of warp group 2's share
-// (128 x 96 + 256 x 200 = 63,488).
-constexpr int kLdLaunchRegs = 168, kLdSoftmaxRegs = 200, kLdOtherRegs = 96;
-static_assert(128 * kLdOtherRegs + 256 * kLdSoftmaxRegs <= kLdThreads * kLdLaunchRegs, "setmaxnreg split fits the launch");
+constexpr int kLdThreads = 512;
+// Registers: 512 x 128 at launch = 65,536; the softmax groups take most of the other warps' share
+// (256 x 64 + 256 x 184 = 63,488).
+constexpr int kLdLaunchRegs = 128, kLdSoftmaxRegs = 184, kLdOtherRegs = 64;
+static_assert(256 * kLdOtherRegs + 256 * kLdSoftmaxRegs <= kLdThreads * kLdLaunchRegs, "setmaxnreg split fits the launch");
 constexpr float kLdRescale = 8.f;  // log2
 constexpr float kLdLn2 = 0.6931471805599453f;
 
@@ -75,10 +74,10 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     uint64_t *v_full = bars + 8;     // [3] V stage landed
     uint64_t *v_empty = bars + 11;   // [3] the PV MMAs that read it completed
     uint64_t *s_full = bars + 14;    // [2][2] S_X(j) in buffer j & 1
-    uint64_t *p_full = bars + 18;    // [2] P_X(j) written (and O_X rescaled if it had to be)
-    uint64_t *pv_done = bars + 20;   // [2] PV_X(j) completed
-    uint64_t *v_tail = bars + 22;    // the value rows past the segment are zero (at most one tile)
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 23);
+    uint64_t *p_full = bars + 18;    // [2][2] P_X(j) written over S_X(j) (and O_X rescaled if it had to be)
+    uint64_t *pv_done = bars + 22;   // [2][2] PV_X(j) completed, of buffer j & 1
+    uint64_t *v_tail = bars + 26;    // the value rows past the segment are zero (at most one tile)
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 27);
 
     const PrefillTile t = a.tiles[blockIdx.x];
     int *const err = &a.hdr->err;
@@ -97,8 +96,10 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             mbar_init(&q_full[x], 1);
             mbar_init(&s_full[2 * x], 1);
             mbar_init(&s_full[2 * x + 1], 1);
-            mbar_init(&p_full[x], 4);
-            mbar_init(&pv_done[x], 1);
+            mbar_init(&p_full[2 * x], 4);
+            mbar_init(&p_full[2 * x + 1], 4);
+            mbar_init(&pv_done[2 * x], 1);
+            mbar_init(&pv_done[2 * x + 1], 1);
         }
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(&k_full[s], 1);
@@ -164,74 +165,85 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 }
             }
         } else if (warp == 9 || (warp == 10 && two)) {
-            // ------------------------------------------------ MMAs: warp 9 for Q0, warp 10 for Q1
-            const int x = warp - 9;
-            const int ntx = x == 0 ? nt0 : nt;
+            // ------------------------------------------------ S = Q K^T: warp 9 for Q0, warp 10 for Q1
+            const int x = warp - 9, ntx = x == 0 ? nt0 : nt;
             constexpr uint32_t ID_S = idesc_bf16_f32(128, kLdKeys, 0, 0);
-            constexpr uint32_t ID_O = idesc_bf16_f32(128, kLatentV, 0, 1);
             const uint64_t dQ = smem_desc(smem_u32(sm + L::Q_OFF + x * L::QC * L::QCHUNK), 16, 1024, kSwizzle128B);
             const uint64_t dK = smem_desc(smem_u32(sm + L::K_OFF), 16, 1024, kSwizzle128B);
-            // the leading offset steps from the first 64 value columns to the second
-            const uint64_t dV = smem_desc(smem_u32(sm + L::V_OFF), L::CHUNK, 1024, kSwizzle128B);
-            auto add = [](uint64_t d, uint32_t off) { return d + (off >> 4); };
-            const uint32_t Sx = S_col(x), Ox = O_col(x);
-            // S_X(j) into buffer j & 1, which held P_X(j-2): PV_X(j-2) has completed
-            auto issue_s = [&](int j) -> bool {
-                const int s = j % L::STAGES;
-                if (j > 1 && !mbar_wait(&pv_done[x], (j - 2) & 1, err, kErrWaitFull)) return false;
-                if (!mbar_wait(&k_full[s], (j / L::STAGES) & 1, err, kErrWaitFull)) return false;
-                tc_fence_after();
+            const uint32_t hi = (uint32_t)(dQ >> 32);  // dK's too
+            auto desc = [hi](uint32_t lo, uint32_t off) { return ((uint64_t)hi << 32) | (lo + (off >> 4)); };
+            const uint32_t Sx = S_col(x);
+            bool ok = mbar_wait(&q_full[x], 0, err, kErrWaitFull);
+            int s = 0, ph = 0;  // stage and its phase
+            for (int j = 0; j < nt && ok; ++j) {
+                ok = mbar_wait(&k_full[s], ph, err, kErrWaitFull);
+                if (j < ntx) {
+                    // S_X(j) into buffer j & 1, which held P_X(j-2): PV_X(j-2) has completed
+                    if (ok && j > 1) ok = mbar_wait(&pv_done[2 * x + (j & 1)], ((j >> 1) - 1) & 1, err, kErrWaitFull);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t lK = (uint32_t)dK + ((s * L::KC * L::CHUNK) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4 * L::KC; ++kk)
-                    mma_ss_elect(Sx + 64u * (j & 1), add(dQ, (kk >> 2) * L::QCHUNK + (kk & 3) * 32),
-                                 add(dK, (s * L::KC + (kk >> 2)) * L::CHUNK + (kk & 3) * 32), ID_S, kk > 0 ? 1u : 0u);
-                mma_commit_elect(&k_empty[s]);
-                mma_commit_elect(&s_full[2 * x + (j & 1)]);
-                return true;
-            };
-            bool ok = mbar_wait(&q_full[x], 0, err, kErrWaitFull) && issue_s(0);
-            for (int j = 0; j < ntx && ok; ++j) {
-                if (j + 1 < ntx && !(ok = issue_s(j + 1))) break;
-                const int s = j % L::STAGES;
-                ok = mbar_wait(&v_full[s], (j / L::STAGES) & 1, err, kErrWaitFull);
-                // Value rows past the segment's end belong to the next segment (or are zero past the
-                // tensor): their P is 0, but 0 * NaN would reach O.  The last query tile's warp zeroes
-                // them; the other waits for that on the one tile that has them.
-                const int key0 = (kt0 + j) * kLdKeys;
-                if (ok && key0 + kLdKeys > t.length) {
-                    if (x == (two ? 1 : 0)) {
-                        const int zb = t.length - key0;  // >= 1: the tile holds a visible key
-                        for (int e = lane; e < (kLdKeys - zb) * 16; e += 32) {
-                            const int k = zb + (e >> 4), ch = e & 15;
-                            *reinterpret_cast<uint4 *>(sm + L::V_OFF + (s * L::VC + (ch >> 3)) * L::CHUNK +
-                                                       swz128(k, ch & 7)) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(v_tail);
-                    } else {
-                        ok = mbar_wait(v_tail, 0, err, kErrWaitFull);
-                    }
+                    for (int kk = 0; kk < 4 * L::KC; ++kk)
+                        mma_ss_elect(Sx + 64u * (j & 1), desc((uint32_t)dQ, (kk >> 2) * L::QCHUNK + (kk & 3) * 32),
+                                     desc(lK, (kk >> 2) * L::CHUNK + (kk & 3) * 32), ID_S, kk > 0 ? 1u : 0u);
+                    mma_commit_elect(&s_full[2 * x + (j & 1)]);
+                    mma_commit_elect(&k_empty[s]);
+                } else if (ok && lane == 0) {
+                    mbar_arrive(&k_empty[s]);  // a tile of the pair's that Q0 does not see
                 }
-                if (ok) ok = mbar_wait(&p_full[x], j & 1, err, kErrWaitFull);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kLdKeys / 16; ++kk)
-                    mma_ts_elect(Ox, Sx + 64u * (j & 1) + kk * 8, add(dV, s * L::VC * L::CHUNK + kk * 2048), ID_O,
-                                 (j > 0 || kk > 0) ? 1u : 0u);
-                mma_commit_elect(&pv_done[x]);
-                mma_commit_elect(&v_empty[s]);
-            }
-            // the pair's tiles past Q0's last: Q0 has no use of them
-            for (int j = ntx; j < nt && ok; ++j) {
-                const int s = j % L::STAGES;
-                ok = mbar_wait(&k_full[s], (j / L::STAGES) & 1, err, kErrWaitFull);
-                if (ok && lane == 0) mbar_arrive(&k_empty[s]);
-                if (ok) ok = mbar_wait(&v_full[s], (j / L::STAGES) & 1, err, kErrWaitFull);
-                if (ok && lane == 0) mbar_arrive(&v_empty[s]);
+                if (++s == L::STAGES) s = 0, ph ^= 1;
             }
             if (!ok)  // a wait gave up: let the MMAs in flight finish before the tensor memory is released
+                for (uint32_t k = 0; k < 1024; ++k) __nanosleep(1000);
+        } else if (warp == 11 || (warp == 12 && two)) {
+            // ------------------------------------------------ O += P V: warp 11 for Q0, warp 12 for Q1
+            const int x = warp - 11, ntx = x == 0 ? nt0 : nt;
+            constexpr uint32_t ID_O = idesc_bf16_f32(128, kLatentV, 0, 1);
+            // the leading offset steps from the first 64 value columns to the second
+            const uint64_t dV = smem_desc(smem_u32(sm + L::V_OFF), L::CHUNK, 1024, kSwizzle128B);
+            const uint32_t hi = (uint32_t)(dV >> 32);
+            const uint32_t Sx = S_col(x), Ox = O_col(x);
+            bool ok = true;
+            int s = 0, ph = 0;
+            for (int j = 0; j < nt && ok; ++j) {
+                ok = mbar_wait(&v_full[s], ph, err, kErrWaitFull);
+                if (!ok) break;
+                if (j < ntx) {
+                    // Value rows past the segment's end belong to the next segment (or are zero past the
+                    // tensor): their P is 0, but 0 * NaN would reach O.  The last query tile's warp zeroes
+                    // them; the other waits for that on the one tile that has them.
+                    const int zb = t.length - (kt0 + j) * kLdKeys;  // >= 1: the tile holds a visible key
+                    if (zb < kLdKeys) {
+                        if (x == (two ? 1 : 0)) {
+                            for (int e = lane; e < (kLdKeys - zb) * 16; e += 32) {
+                                const int k = zb + (e >> 4), ch = e & 15;
+                                *reinterpret_cast<uint4 *>(sm + L::V_OFF + (s * L::VC + (ch >> 3)) * L::CHUNK +
+                                                           swz128(k, ch & 7)) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(v_tail);
+                        } else {
+                            ok = mbar_wait(v_tail, 0, err, kErrWaitFull);
+                        }
+                    }
+                    if (ok) ok = mbar_wait(&p_full[2 * x + (j & 1)], (j >> 1) & 1, err, kErrWaitFull);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t lV = (uint32_t)dV + ((s * L::VC * L::CHUNK) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kLdKeys / 16; ++kk)
+                        mma_ts_elect(Ox, Sx + 64u * (j & 1) + kk * 8, ((uint64_t)hi << 32) | (lV + kk * (2048 >> 4)),
+                                     ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit_elect(&pv_done[2 * x + (j & 1)]);
+                    mma_commit_elect(&v_empty[s]);
+                } else if (lane == 0) {
+                    mbar_arrive(&v_empty[s]);
+                }
+                if (++s == L::STAGES) s = 0, ph ^= 1;
+            }
+            if (!ok)
                 for (uint32_t k = 0; k < 1024; ++k) __nanosleep(1000);
         }
     } else {
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 tmem_wait_st();
                 if (warp_grow) {
                     // O holds P_0..P_{j-1} V: wait for the last of those MMAs, then scale O's rows
-                    if (!mbar_wait(&pv_done[x], (j - 1) & 1, err, kErrWaitFull)) {
+                    if (!mbar_wait(&pv_done[2 * x + ((j - 1) & 1)], ((j - 1) >> 1) & 1, err, kErrWaitFull)) {
                         ok = false;
                         break;
                     }
@@ -334,11 +346,9 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
+                if (lane == 0) mbar_arrive(&p_full[2 * x + (j & 1)]);
             }
-            // S(ntx-1) says that PV(ntx-3) completed: two phases of the barrier are left
-            if (ok && (ntx < 2 || mbar_wait(&pv_done[x], (ntx - 2) & 1, err, kErrWaitFull)) &&
-                mbar_wait(&pv_done[x], (ntx - 1) & 1, err, kErrWaitFull)) {
+            if (ok && mbar_wait(&pv_done[2 * x + ((ntx - 1) & 1)], ((ntx - 1) >> 1) & 1, err, kErrWaitFull)) {
                 tc_fence_after();
                 const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
                 const size_t row = (size_t)(t.q_begin + tok) * a.num_heads + t.kv_head;
