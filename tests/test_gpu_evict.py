@@ -153,6 +153,42 @@ def test_weights_of_another_sequence_do_not_leak():
     assert torch.equal(a[mine], b[mine]) and torch.isfinite(a[mine]).all()
 
 
+def test_graphs_of_two_handles_on_two_streams():
+    """A decode step and a prompt's weights, each captured with its own handle and workspace, replayed at
+    the same time on streams other than the capturing one: the bits of the eager calls."""
+    d = Step([700, 40, 129], [1, 1, 1], 8, 2, 128, 16, 21, mode=B.MODE_DECODE_WEIGHTS)
+    w = Step([400, 129], [90, 129], 8, 2, 128, 16, 22, mode=B.MODE_WEIGHTS)
+    _, l, _, _ = E.attention(w.q, w.cache, *w.idx(), w.scale)
+    wl, wq, wc = l.float().cuda(), w.q.cuda(), w.cache.cuda()
+    dq, dc = d.q.cuda(), d.cache.cuda()
+    out, dl = torch.empty_like(dq), torch.empty(3, 8, device="cuda")
+    ds, wsc = d.scores.cuda(), w.scores.cuda()
+    dec = lambda t: d.h.run_decode_weights(dq, dc, out, dl, t, decay=0.5, workspace=d.ws)
+    wei = lambda t: w.h.run_weights(wq, wl, wc, t, decay=0.5, workspace=w.ws)
+    want_d, want_w = d.scores.cuda(), w.scores.cuda()
+    for _ in range(3):
+        dec(want_d), wei(want_w)
+    want_o, want_l = out.clone(), dl.clone()
+    graphs = []
+    for f, t in ((dec, ds), (wei, wsc)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f(t)
+        graphs.append(g)
+    out.zero_(), dl.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert d.h.check_device_error(d.ws) == 0 and w.h.check_device_error(w.ws) == 0
+    assert torch.equal(bits(out), bits(want_o)) and torch.equal(dl, want_l)
+    for got, want, s in ((ds, want_d, d), (wsc, want_w, w)):
+        assert torch.equal(got[s.used.cuda()], want[s.used.cuda()])
+
+
 # ---------------------------------------------------------------- eviction
 
 class Cut:
