@@ -5,13 +5,19 @@
 // WEIGHTS plans: the product is taken transposed, S^T = K Q^T: 128 keys are the rows of the MMA and
 // tensor-memory lanes, so a thread owns a key and adds up its weights over a block's query rows (up to
 // 128: tokens x the group's heads) in registers, with no reduction across lanes.  Two teams of four
-// warps take the blocks in turn, each with its own S buffer, so that one's loads and waits run under the
-// other's exponentials.  One CTA per SM walks items (kv heads or query blocks of one tile, planned to an
+// warps take the blocks in turn; four S buffers (all of tensor memory) let the MMAs run two blocks
+// ahead of each.  One CTA per SM walks items (kv heads or query blocks of one tile, planned to an
 // eighth of an SM's share) with its rings running on across them; a team's sums of an item go to a part
 // of their own, and the finishing kernel adds a tile's parts in order.  K is read once from HBM (two
 // warps issue its copies: a page and 64 columns each, some 50 cycles an instruction), Q blocks come
-// from L2.  Few query rows: bounded by K's bytes.  Many: by the exponentials (16 a cycle and SM: 1,024
-// cycles a block, against 512 of its MMAs at head_dim 128).
+// from L2.
+//
+// Measured (32 query heads on 8, head_dim 128): last 32 tokens of 8 rows of 1,999 to 16,381, 36 us,
+// 23 of them K's bytes at the copy rate; two whole prompts of 2,003 tokens 62 us, 17 of operations.  The
+// bound is the teams' work, some 1,700 cycles a block of 128 x 128 (1,024 of them the exponentials at
+// 16 a cycle and SM): without Q's copies 65 of then 67 us, with an eighth of the MMAs 66, with a
+// quarter of the columns 37.  Steps of 64 columns (spilling registers): 40 / 67 us; one S buffer a
+// team 40 / 67; an MMA warp a team 48 / 81; four teams 42 / 65; the lse as a k-step of the MMA 44 / 70.
 //
 // DECODE_WEIGHTS plans: the decode kernel has left its logits; a thread per key adds the weights.
 #include <cuda.h>
@@ -86,14 +92,11 @@ template <bool MASKED>
 __device__ __forceinline__ void add_columns(uint64_t (&acc)[4], uint32_t s_lane, int ncols, int key, uint64_t sl2,
                                             const float *c_ls, const int *c_lo, const int *c_hi) {
 #pragma unroll 1
-    for (int c0 = 0; c0 < ncols; c0 += 64) {
-        uint32_t r0[32], r1[32];
-        const bool more = c0 + 32 < ncols;
-        tmem_ld32(s_lane + c0, r0);
-        if (more) tmem_ld32(s_lane + c0 + 32, r1);
+    for (int c0 = 0; c0 < ncols; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(s_lane + c0, r);
         tmem_wait_ld();
-        take_columns<MASKED>(acc, r0, key, sl2, c_ls + c0, c_lo + c0, c_hi + c0);
-        if (more) take_columns<MASKED>(acc, r1, key, sl2, c_ls + c0 + 32, c_lo + c0 + 32, c_hi + c0 + 32);
+        take_columns<MASKED>(acc, r, key, sl2, c_ls + c0, c_lo + c0, c_hi + c0);
     }
 }
 
@@ -107,8 +110,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR_OFF);
     // K tiles are counted over the CTA's items (kc: one per item and head), blocks too (it)
     uint64_t *k_full = bars + 0, *k_empty = bars + 4;                                              // [KS] each
-    uint64_t *q_full = bars + 8, *q_empty = bars + 10, *s_full = bars + 12, *s_empty = bars + 14;  // [2] each
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 16);
+    uint64_t *q_full = bars + 8, *q_empty = bars + 10;  // [2] each
+    uint64_t *s_full = bars + 12, *s_empty = bars + 16;  // [4] each: block it in S buffer it % 4
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 20);
 
     int *const err = &a.hdr->err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -121,13 +125,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&s_empty[s], 4);
         }
         fence_barrier_init();
     }
     if (warp == 11) {
-        tmem_alloc(tmem_holder, 256);
+        tmem_alloc(tmem_holder, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -218,18 +224,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int ks = kc % L::KS;
                 ok = mbar_wait(&k_full[ks], (kc / L::KS) & 1, err, kErrWaitFull);
                 for (int b = 0; b < blocks && ok; ++b, ++it) {
-                    const int s = it & 1;
+                    const int s = it & 1, sb = it & 3;
                     ok = mbar_wait(&q_full[s], (it >> 1) & 1, err, kErrWaitFull) &&
-                         (it < 2 || mbar_wait(&s_empty[s], ((it >> 1) - 1) & 1, err, kErrWaitEmpty));
+                         (it < 4 || mbar_wait(&s_empty[sb], ((it >> 2) - 1) & 1, err, kErrWaitEmpty));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk / 4) * L::CHUNK + (kk % 4) * 32;
-                        mma_ss_elect(tmem + 128u * s, add(dK, ks * L::TILE + off), add(dQ, s * L::TILE + off), id, kk > 0);
+                        mma_ss_elect(tmem + 128u * sb, add(dK, ks * L::TILE + off), add(dQ, s * L::TILE + off), id, kk > 0);
                     }
                     mma_commit_elect(&q_empty[s]);
-                    mma_commit_elect(&s_full[s]);
+                    mma_commit_elect(&s_full[sb]);
                 }
                 if (ok) mma_commit_elect(&k_empty[ks]);
             }
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     } else {
         // ------------------------------------------------ the teams: a key a thread
         const int team = warp >> 2, m = threadIdx.x & 127;  // the key, and the block column whose lse it fetches
-        const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * team;
+        const uint32_t s_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl = a.hdr->scale_log2;
         const uint64_t sl2 = f2_make(sl, sl);
         const int causal = a.hdr->causal, window = a.hdr->window_left;
@@ -295,18 +301,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     fetch(next, g_next);
                     fetched = true;
                 }
-                ok = ok && mbar_wait(&s_full[team], (it >> 1) & 1, err, kErrWaitFull);
+                ok = ok && mbar_wait(&s_full[it & 3], (it >> 2) & 1, err, kErrWaitFull);
                 __syncwarp();
                 tc_fence_after();
                 uint64_t acc[4] = {0, 0, 0, 0};
                 // columns past the block's are masked too
                 if (all && !(ncols & 31))
-                    add_columns<false>(acc, s_lane, ncols, key, sl2, c_ls, c_lo, c_hi);
+                    add_columns<false>(acc, s_lane + 128u * (it & 3), ncols, key, sl2, c_ls, c_lo, c_hi);
                 else
-                    add_columns<true>(acc, s_lane, ncols, key, sl2, c_ls, c_lo, c_hi);
+                    add_columns<true>(acc, s_lane + 128u * (it & 3), ncols, key, sl2, c_ls, c_lo, c_hi);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[team]);
+                if (lane == 0) mbar_arrive(&s_empty[it & 3]);
                 float u0, u1;
                 f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u0, u1);
                 total += u0 + u1;
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 11) tmem_dealloc(tmem, 256);
+    if (warp == 11) tmem_dealloc(tmem, 512);
 }
 
 __device__ __forceinline__ void put_score(const WeightsTile &t, const int32_t *pages, int page_size, int page_shift, int key,
