@@ -47,9 +47,8 @@ struct WtSmem {
     static constexpr uint32_t K_OFF = 0;
     static constexpr uint32_t Q_OFF = KS * TILE;
     static constexpr uint32_t BAR_OFF = Q_OFF + QS * TILE;
-    // per team, buffer and block column: -lse (base 2), first and last key
-    static constexpr uint32_t COL_OFF = BAR_OFF + 256;
-    static constexpr uint32_t BYTES = COL_OFF + 2 * 2 * 3 * 128 * 4;
+    static constexpr uint32_t COL_OFF = BAR_OFF + 256;  // -lse (base 2) of a block's columns: [team][buffer][128]
+    static constexpr uint32_t BYTES = COL_OFF + 2 * 2 * 128 * 4;
 };
 static_assert(1024 + WtSmem<256>::BYTES <= 227 * 1024, "the weights kernel fits shared memory");
 
@@ -63,40 +62,31 @@ struct WeightsArgs {
     int page_size, page_shift, box_rows, box_tokens, oob_row;
 };
 
-// Add the weights of 32 columns (below: `ncols`) of this thread's key to acc: 2^(s sl - lse), with MASKED
-// only where c_lo <= key <= c_hi.
+// Add the weights of the block's `ncols` columns of this thread's key to acc: 2^(s sl - lse), with MASKED
+// only of the columns [c_begin, c_end).  (Columns come 32 at a time; without MASKED ncols is a multiple.)
 template <bool MASKED>
-__device__ __forceinline__ void take_columns(uint64_t (&acc)[4], const uint32_t (&r)[32], int key, uint64_t sl2,
-                                             const float *c_ls, const int *c_lo, const int *c_hi) {
-    const ulonglong2 *ls2 = reinterpret_cast<const ulonglong2 *>(c_ls);
-    const int4 *lo4 = reinterpret_cast<const int4 *>(c_lo), *hi4 = reinterpret_cast<const int4 *>(c_hi);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const ulonglong2 l = ls2[c];
-        float x0, x1, x2, x3;
-        f2_split(ffma2(f2_make(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])), sl2, l.x), x0, x1);
-        f2_split(ffma2(f2_make(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])), sl2, l.y), x2, x3);
-        if constexpr (MASKED) {  // selects, not products: a masked score may be NaN
-            const int4 a4 = lo4[c], b4 = hi4[c];
-            x0 = (key >= a4.x) & (key <= b4.x) ? x0 : -INFINITY;
-            x1 = (key >= a4.y) & (key <= b4.y) ? x1 : -INFINITY;
-            x2 = (key >= a4.z) & (key <= b4.z) ? x2 : -INFINITY;
-            x3 = (key >= a4.w) & (key <= b4.w) ? x3 : -INFINITY;
-        }
-        acc[(2 * c) & 3] = fadd2(acc[(2 * c) & 3], f2_make(ex2_ftz(x0), ex2_ftz(x1)));
-        acc[(2 * c + 1) & 3] = fadd2(acc[(2 * c + 1) & 3], f2_make(ex2_ftz(x2), ex2_ftz(x3)));
-    }
-}
-
-template <bool MASKED>
-__device__ __forceinline__ void add_columns(uint64_t (&acc)[4], uint32_t s_lane, int ncols, int key, uint64_t sl2,
-                                            const float *c_ls, const int *c_lo, const int *c_hi) {
+__device__ __forceinline__ void add_columns(uint64_t (&acc)[4], uint32_t s_lane, int ncols, uint64_t sl2, const float *c_ls,
+                                            int c_begin, int c_end) {
 #pragma unroll 1
     for (int c0 = 0; c0 < ncols; c0 += 32) {
         uint32_t r[32];
         tmem_ld32(s_lane + c0, r);
         tmem_wait_ld();
-        take_columns<MASKED>(acc, r, key, sl2, c_ls + c0, c_lo + c0, c_hi + c0);
+        const ulonglong2 *ls2 = reinterpret_cast<const ulonglong2 *>(c_ls + c0);
+        const int begin = c_begin - c0, end = c_end - c0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const ulonglong2 l = ls2[c];
+            float x[4];
+            f2_split(ffma2(f2_make(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])), sl2, l.x), x[0], x[1]);
+            f2_split(ffma2(f2_make(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])), sl2, l.y), x[2], x[3]);
+            if constexpr (MASKED) {  // selects, not products: a masked score may be NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = (4 * c + i >= begin) & (4 * c + i < end) ? x[i] : -INFINITY;
+            }
+            acc[(2 * c) & 3] = fadd2(acc[(2 * c) & 3], f2_make(ex2_ftz(x[0]), ex2_ftz(x[1])));
+            acc[(2 * c + 1) & 3] = fadd2(acc[(2 * c + 1) & 3], f2_make(ex2_ftz(x[2]), ex2_ftz(x[3])));
+        }
     }
 }
 
@@ -252,76 +242,89 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const uint64_t sl2 = f2_make(sl, sl);
         const int causal = a.hdr->causal, window = a.hdr->window_left;
         const int m_tok = m / G, m_head = m % G;
-        uint32_t it0 = 0, seq = 0;  // blocks before this item; blocks this team has taken
         // a wait that gives up clears ok; the warps still walk their blocks, without further waits, so
         // that they keep meeting at their barriers (which have no time limit)
         bool ok = true;
-        // column m of a block (number g of an item's heads x blocks), fetched one block ahead; its lse is not
-        // touched before it is stored, so that the fetch does not wait for it
+        // The lse of column m of a block, fetched one block ahead and not touched before it is stored, so
+        // that the fetch does not wait for it.
         float ls = 0.f;
-        int lo = 0, hi = -1;
-        auto fetch = [&](const WeightsItem &w, int g) {
-            const int h = w.blocks == 1 ? g : g / w.blocks, i = w.i0 + (g - h * w.blocks) * bt + m_tok;
-            const bool valid = m < bt * G && i < w.i1;
-            const int pos = w.new_begin + i;
+        auto fetch = [&](const WeightsItem &w, int h, int b) {
+            const int i = w.i0 + b * bt + m_tok;
             ls = 0.f;
-            if (valid) ls = a.lse[(size_t)(w.q_begin + i) * a.num_qo_heads + (w.h0 + h) * G + m_head];
-            lo = window >= 0 ? max(0, pos - window) : 0;
-            hi = valid ? (causal ? pos : w.length - 1) : -1;
+            if (m < bt * G && i < w.i1) ls = a.lse[(size_t)(w.q_begin + i) * a.num_qo_heads + (w.h0 + h) * G + m_head];
+        };
+        // This team's blocks are every other one: (h, b) steps by two, past the item's end into the next
+        // one.  (Counted, not divided: the divisions cost 500 cycles a block.)
+        auto settle = [](const WeightsItem &w, int &h, int &b) {
+            while (b >= w.blocks) {
+                b -= w.blocks;
+                ++h;
+            }
         };
         WeightsItem w = a.items[blockIdx.x];
-        int g = team;  // this team's blocks: every other one
-        if (g < w.nh * w.blocks) fetch(w, g);
+        uint32_t it = team;  // block of the CTA's whole run
+        int h = 0, b = team;
+        settle(w, h, b);
+        if (h < w.nh) fetch(w, h, b);
         for (int n = blockIdx.x; n < a.num_items; n += gridDim.x) {
-            const int key = w.key0 + m, total_blocks = w.nh * w.blocks;
+            const int key = w.key0 + m;
             const bool last = n + (int)gridDim.x >= a.num_items;
             const WeightsItem next = a.items[last ? n : n + (int)gridDim.x];  // lands meanwhile
-            const int g_next = ((it0 + total_blocks) & 1) == (uint32_t)team ? 0 : 1;
             bool fetched = false;
             float total = 0.f;
-            for (; g < total_blocks; g += 2, ++seq) {
-                const uint32_t it = it0 + g;
-                const int i_first = w.i0 + (w.blocks == 1 ? 0 : g % w.blocks) * bt, i_count = min(bt, w.i1 - i_first);
+            while (h < w.nh) {
+                const int i_first = w.i0 + b * bt, i_count = min(bt, w.i1 - i_first);
                 const int ncols = i_count * G, pos0 = w.new_begin + i_first;
                 // every column of the block sees every key of the tile: no masks then
                 const bool all = w.key0 + kWeightKeys <= w.length && (!causal || pos0 >= w.key0 + kWeightKeys - 1) &&
-                                 (window < 0 || pos0 + i_count - 1 - window <= w.key0);
+                                 (window < 0 || pos0 + i_count - 1 - window <= w.key0) && !(ncols & 31);
                 // two buffers of columns, so one barrier a block: behind it the block before last has been read
-                float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + (team * 2 + (seq & 1)) * 384;
-                int *const c_lo = reinterpret_cast<int *>(c_ls) + 128, *const c_hi = c_lo + 128;
+                float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + (team * 2 + ((it >> 1) & 1)) * 128;
                 c_ls[m] = ls * -kWtLog2e;
-                if (!all || (ncols & 31)) {
-                    c_lo[m] = lo;
-                    c_hi[m] = hi;
-                }
                 named_barrier_sync(1 + team, 128);
-                if (g + 2 < total_blocks) {
-                    fetch(w, g + 2);
-                } else if (!last && g_next < next.nh * next.blocks) {
-                    fetch(next, g_next);
-                    fetched = true;
+                int h2 = h, b2 = b + 2;
+                settle(w, h2, b2);
+                if (h2 < w.nh) {
+                    fetch(w, h2, b2);
+                } else if (!last) {
+                    int hn = 0, bn = (h2 - w.nh) * w.blocks + b2;
+                    settle(next, hn, bn);
+                    if (hn < next.nh) {
+                        fetch(next, hn, bn);
+                        fetched = true;
+                    }
                 }
                 ok = ok && mbar_wait(&s_full[it & 3], (it >> 2) & 1, err, kErrWaitFull);
                 __syncwarp();
                 tc_fence_after();
                 uint64_t acc[4] = {0, 0, 0, 0};
-                // columns past the block's are masked too
-                if (all && !(ncols & 31))
-                    add_columns<false>(acc, s_lane + 128u * (it & 3), ncols, key, sl2, c_ls, c_lo, c_hi);
-                else
-                    add_columns<true>(acc, s_lane + 128u * (it & 3), ncols, key, sl2, c_ls, c_lo, c_hi);
+                if (all) {
+                    add_columns<false>(acc, s_lane + 128u * (it & 3), ncols, sl2, c_ls, 0, 0);
+                } else {
+                    // token t of the block, at pos0 + t, sees the key from t = key - pos0 (causal) to
+                    // key - pos0 + window; a key past the row is seen by none
+                    const int t_begin = causal ? max(0, key - pos0) : 0;
+                    const int t_end = key >= w.length ? 0
+                                      : window < 0 ? i_count
+                                                   : (int)max(0ll, min((long long)i_count, (long long)key - pos0 + window + 1));
+                    add_columns<true>(acc, s_lane + 128u * (it & 3), ncols, sl2, c_ls, min(t_begin, bt) * G, t_end * G);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[it & 3]);
                 float u0, u1;
                 f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u0, u1);
                 total += u0 + u1;
+                h = h2;
+                b = b2;
+                it += 2;
             }
             a.part[((size_t)w.part * 2 + team) * kWeightKeys + m] = total;
-            it0 += total_blocks;
-            g = g_next;
+            b += (h - w.nh) * w.blocks;
+            h = 0;
             w = next;
-            if (!fetched && !last && g < w.nh * w.blocks) fetch(w, g);
+            settle(w, h, b);
+            if (!fetched && !last && h < w.nh) fetch(w, h, b);
         }
     }
     tc_fence_before();
