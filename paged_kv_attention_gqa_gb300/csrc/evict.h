@@ -13,6 +13,7 @@
 namespace pkv {
 
 constexpr int kWeightKeys = 128;       // keys of one work tile of the score kernels
+constexpr int kWeightTeams = 3;        // thread groups of the weights kernel that take query blocks in turn
 constexpr int kWeightsMinPage = 8;     // the K boxes of a WEIGHTS plan fill whole 8-row swizzle atoms
 constexpr int kEvictTaskTokens = 32;   // kept tokens copied by one CTA of the gather
 constexpr int kEvictMaxCluster = 8;    // CTAs that select one row's tokens

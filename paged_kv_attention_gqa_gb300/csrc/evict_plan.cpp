@@ -148,7 +148,7 @@ int make_weights_plan(const Shape &s, int mode, const int32_t *qo, const int32_t
     w.off_tiles = put(at, tiles.size() * sizeof(WeightsTile));
     w.off_items = put(at, items.size() * sizeof(WeightsItem));
     plan.lay.int_bytes = at;
-    w.off_part = put(at, items.size() * 2 * kWeightKeys * 4);  // one per item and team
+    w.off_part = put(at, items.size() * kWeightTeams * kWeightKeys * 4);  // one per item and team
     plan.lay.total = at;
     image.assign(plan.lay.int_bytes, 0);
     PlanHeader hdr{};
@@ -281,7 +281,7 @@ size_t evict_workspace_bound(const Shape &s, int mode) {
     // block of one head where the share is less)
     const size_t items = 16 * (size_t)std::max(1, s.sm_count) + 2 * tiles;
     put(at, items * sizeof(WeightsItem));
-    put(at, items * 2 * kWeightKeys * 4);
+    put(at, items * kWeightTeams * kWeightKeys * 4);
     return at;
 }
 

@@ -4,20 +4,20 @@
 //
 // WEIGHTS plans: the product is taken transposed, S^T = K Q^T: 128 keys are the rows of the MMA and
 // tensor-memory lanes, so a thread owns a key and adds up its weights over a block's query rows (up to
-// 128: tokens x the group's heads) in registers, with no reduction across lanes.  Two teams of four
-// warps take the blocks in turn; four S buffers (all of tensor memory) let the MMAs run two blocks
-// ahead of each.  One CTA per SM walks items (kv heads or query blocks of one tile, planned to an
-// eighth of an SM's share) with its rings running on across them; a team's sums of an item go to a part
-// of their own, and the finishing kernel adds a tile's parts in order.  K is read once from HBM (two
-// warps issue its copies: a page and 64 columns each, some 50 cycles an instruction), Q blocks come
-// from L2.
+// 128: tokens x the group's heads) in registers, with no reduction across lanes.  Three teams of four
+// warps take the blocks in turn; four S buffers (all of tensor memory) let the MMAs run ahead of them.
+// One CTA per SM walks items (kv heads or query blocks of one tile, planned to an eighth of an SM's
+// share) with its rings running on across them; a team's sums of an item go to a part of their own, and
+// the finishing kernel adds a tile's parts in order.  K is read once from HBM (two warps issue its
+// copies: a page and 64 columns each, some 50 cycles an instruction), Q blocks come from L2.
 //
-// Measured (32 query heads on 8, head_dim 128): last 32 tokens of 8 rows of 1,999 to 16,381, 36 us,
-// 23 of them K's bytes at the copy rate; two whole prompts of 2,003 tokens 62 us, 17 of operations.  The
-// bound is the teams' work, some 1,700 cycles a block of 128 x 128 (1,024 of them the exponentials at
-// 16 a cycle and SM): without Q's copies 65 of then 67 us, with an eighth of the MMAs 66, with a
-// quarter of the columns 37.  Steps of 64 columns (spilling registers): 40 / 67 us; one S buffer a
-// team 40 / 67; an MMA warp a team 48 / 81; four teams 42 / 65; the lse as a k-step of the MMA 44 / 70.
+// Measured (32 query heads on 8, head_dim 128): last 32 tokens of 8 rows of 1,999 to 16,381, 34 us, 23 of
+// them K's bytes at the copy rate; two whole prompts of 2,003 tokens 49 us, 17 of operations.  The bound
+// is the teams' work: some 900 cycles a block of 128 x 128 with all warps busy (512 of them the
+// exponentials at 32 a cycle and SM), half as much again between two blocks of a team (its columns' lse,
+// the barrier, the next fetch), which the other teams cover in part.  Before: two teams 35 / 52; with a
+// block's head and number found by division and first and last key read per column 36 / 62; steps of 64
+// columns (spilling registers) 40 / 67; an MMA warp a team 48 / 81; the lse as a k-step of the MMA 44 / 70.
 //
 // DECODE_WEIGHTS plans: the decode kernel has left its logits; a thread per key adds the weights.
 #include <cuda.h>
@@ -33,8 +33,8 @@
 namespace pkv {
 namespace dev {
 
-// warps 0-3 and 4-7: the two teams, a key a thread; 8, 9: copies of K; 10: copies of Q; 11: MMAs
-constexpr int kWtThreads = 384;
+// warps 0-11: the three teams, a key a thread; 12, 13: copies of K; 14: copies of Q; 15: MMAs
+constexpr int kWtThreads = 128 * kWeightTeams + 128, kWtK = 4 * kWeightTeams, kWtQ = kWtK + 2, kWtMma = kWtK + 3;
 constexpr int kWtProducers = 2;
 constexpr float kWtLog2e = 1.4426950408889634f;
 
@@ -48,7 +48,7 @@ struct WtSmem {
     static constexpr uint32_t Q_OFF = KS * TILE;
     static constexpr uint32_t BAR_OFF = Q_OFF + QS * TILE;
     static constexpr uint32_t COL_OFF = BAR_OFF + 256;  // -lse (base 2) of a block's columns: [team][buffer][128]
-    static constexpr uint32_t BYTES = COL_OFF + 2 * 2 * 128 * 4;
+    static constexpr uint32_t BYTES = COL_OFF + kWeightTeams * 2 * 128 * 4;
 };
 static_assert(1024 + WtSmem<256>::BYTES <= 227 * 1024, "the weights kernel fits shared memory");
 
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
         fence_barrier_init();
     }
-    if (warp == 11) {
+    if (warp == kWtMma) {
         tmem_alloc(tmem_holder, 512);
         tmem_relinquish();
     }
@@ -133,14 +133,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     griddep_launch();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp == 8 || warp == 9) {
+    if (warp == kWtK || warp == kWtK + 1) {
         // ------------------------------------------------ copies of K: a box is one page run of one chunk
         const int R = a.box_rows, jobs = kWeightKeys / R * L::CHUNKS;      // 1 to 64
         const int per = (jobs + kWtProducers - 1) / kWtProducers;           // at most 32 a warp, one a lane
-        const int job = (warp - 8) * per + lane;
+        const int job = (warp - kWtK) * per + lane;
         const bool copies = lane < per && job < jobs;
-        const uint32_t bytes = (uint32_t)max(0, min(per, jobs - (warp - 8) * per)) * R * 128u;
-        if (warp == 8 && lane == 0) prefetch_tmap(&tm_k);
+        const uint32_t bytes = (uint32_t)max(0, min(per, jobs - (warp - kWtK) * per)) * R * 128u;
+        if (warp == kWtK && lane == 0) prefetch_tmap(&tm_k);
         uint32_t kc = 0;
         bool ok = true;
         WeightsItem w = a.items[blockIdx.x];
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (!ok)
             for (int s = 0; s < L::KS; ++s)
                 for (int p = 0; p < 2; ++p) mbar_wait(&k_full[s], p, nullptr, 0, 1u << 16);
-    } else if (warp == 10) {
+    } else if (warp == kWtQ) {
         // ------------------------------------------------ copies of Q blocks
         if (lane == 0) {
             prefetch_tmap(&tm_q);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 for (int s = 0; s < 2; ++s)
                     for (int p = 0; p < 2; ++p) mbar_wait(&q_full[s], p, nullptr, 0, 1u << 16);
         }
-    } else if (warp == 11) {
+    } else if (warp == kWtMma) {
         // ------------------------------------------------ S^T = K Q^T
         const uint32_t ncol = (uint32_t)(bt * G + 15) & ~15u;
         const uint32_t id = idesc_bf16_f32(128, 0, 0, 0) | ((ncol >> 3) << 17);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             ls = 0.f;
             if (m < bt * G && i < w.i1) ls = a.lse[(size_t)(w.q_begin + i) * a.num_qo_heads + (w.h0 + h) * G + m_head];
         };
-        // This team's blocks are every other one: (h, b) steps by two, past the item's end into the next
+        // This team's blocks are every third one: (h, b) steps by three, past the item's end into the next
         // one.  (Counted, not divided: the divisions cost 500 cycles a block.)
         auto settle = [](const WeightsItem &w, int &h, int &b) {
             while (b >= w.blocks) {
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
         };
         WeightsItem w = a.items[blockIdx.x];
-        uint32_t it = team;  // block of the CTA's whole run
+        uint32_t seq = 0, it = team;  // block of the CTA's whole run
         int h = 0, b = team;
         settle(w, h, b);
         if (h < w.nh) fetch(w, h, b);
@@ -279,10 +279,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const bool all = w.key0 + kWeightKeys <= w.length && (!causal || pos0 >= w.key0 + kWeightKeys - 1) &&
                                  (window < 0 || pos0 + i_count - 1 - window <= w.key0) && !(ncols & 31);
                 // two buffers of columns, so one barrier a block: behind it the block before last has been read
-                float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + (team * 2 + ((it >> 1) & 1)) * 128;
+                float *const c_ls = reinterpret_cast<float *>(sm + L::COL_OFF) + (team * 2 + (seq & 1)) * 128;
                 c_ls[m] = ls * -kWtLog2e;
                 named_barrier_sync(1 + team, 128);
-                int h2 = h, b2 = b + 2;
+                int h2 = h, b2 = b + kWeightTeams;
                 settle(w, h2, b2);
                 if (h2 < w.nh) {
                     fetch(w, h2, b2);
@@ -317,9 +317,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 total += u0 + u1;
                 h = h2;
                 b = b2;
-                it += 2;
+                it += kWeightTeams;
+                ++seq;
             }
-            a.part[((size_t)w.part * 2 + team) * kWeightKeys + m] = total;
+            a.part[((size_t)w.part * kWeightTeams + team) * kWeightKeys + m] = total;
             b += (h - w.nh) * w.blocks;
             h = 0;
             w = next;
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 11) tmem_dealloc(tmem, 512);
+    if (warp == kWtMma) tmem_dealloc(tmem, 512);
 }
 
 __device__ __forceinline__ void put_score(const WeightsTile &t, const int32_t *pages, int page_size, int page_shift, int key,
@@ -351,8 +352,8 @@ __global__ void __launch_bounds__(kWeightKeys * kWtSlices) weights_finish_kernel
     const int m = threadIdx.x % kWeightKeys, slice = threadIdx.x / kWeightKeys, key = t.key0 + m;
     griddep_wait();
     griddep_launch();
-    const float *p = part + (size_t)t.first * 2 * kWeightKeys + m;
-    const int n = 2 * t.base;
+    const float *p = part + (size_t)t.first * kWeightTeams * kWeightKeys + m;
+    const int n = kWeightTeams * t.base;
     float w = 0.f;
     for (int i0 = slice; i0 < n; i0 += 8 * kWtSlices) {
         float x[8];
