@@ -131,6 +131,39 @@ def test_weights(name, decay):
     s.check_scores(scores, lse, decay, name)
 
 
+WEIGHTS_BLOCKS = {
+    "one head, many blocks": dict(lens=[900], news=[900], Hq=1, Hkv=1, D=128, P=16),
+    "one head, one block": dict(lens=[3000, 77], news=[5, 2], Hq=4, Hkv=1, D=128, P=32),
+    "two SMs, heads of several tiles": dict(lens=[600, 333], news=[90, 333], Hq=12, Hkv=3, D=64, P=8, sm_count=2),
+    "a window inside a block": dict(lens=[500], news=[300], Hq=5, Hkv=1, D=128, P=16, window_left=5),
+    "window 0": dict(lens=[260, 3], news=[130, 3], Hq=4, Hkv=2, D=128, P=16, window_left=0),
+    "the longest window": dict(lens=[260, 3], news=[130, 3], Hq=4, Hkv=2, D=128, P=16, window_left=2 ** 31 - 1),
+    "not causal, a window": dict(lens=[300], news=[140], Hq=6, Hkv=2, D=128, P=16, causal=False, window_left=40),
+    "columns that are no multiple of 32": dict(lens=[400], news=[43], Hq=6, Hkv=2, D=128, P=16),
+}
+
+
+@pytest.mark.parametrize("name", WEIGHTS_BLOCKS)
+def test_weights_blocks(name):
+    """Blocks and masks as the teams meet them: items without a block for some team, partial blocks, masks
+    that cut through a block from either side."""
+    s = Step(seed=61 + len(name), mode=B.MODE_WEIGHTS, **WEIGHTS_BLOCKS[name])
+    _, l, _, _ = E.attention(s.q, s.cache, *s.idx(), s.scale, **s.kw)
+    scores = s.scores.cuda()
+    s.h.run_weights(s.q.cuda(), l.float().cuda(), s.cache.cuda(), scores, decay=0.5, workspace=s.ws)
+    torch.cuda.synchronize()
+    assert s.h.check_device_error(s.ws) == 0
+    s.check_scores(scores, l.float(), 0.5, name)
+
+
+def test_weights_without_any_query_decay_the_scores():
+    s = Step([70, 33], [0, 0], 8, 2, 64, 16, 5, mode=B.MODE_WEIGHTS)
+    scores = s.scores.cuda()
+    s.h.run_weights(s.q.cuda(), torch.empty(0, 8, device="cuda"), s.cache.cuda(), scores, decay=0.25, workspace=s.ws)
+    want = torch.where(s.used, s.scores * 0.25, s.scores)
+    assert torch.equal(scores.cpu(), want)
+
+
 def test_weights_sum_to_the_queries():
     """Without a window every query's weights sum to 1 per head."""
     s = Step([333, 64], [50, 64], 8, 2, 128, 16, 9, mode=B.MODE_WEIGHTS)

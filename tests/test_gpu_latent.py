@@ -293,6 +293,64 @@ def test_expanded(name, packed):
     check(out, lse, R.dense(q, kn, kr, v, cu_q, cu_k, SCALE, **mask), name)
 
 
+DENSE_TILES = {
+    "64-key edges": dict(nq=[129, 190, 193, 1], nk=[191, 192, 193, 64], H=2),
+    "a window across tiles": dict(nq=[260, 130, 64], nk=[260, 330, 65], H=2, window_left=65),
+    "a window shorter than a tile": dict(nq=[300], nk=[700], H=1, window_left=3),
+    "not causal, two query tiles": dict(nq=[129, 256], nk=[129, 1000], H=2, causal=False),
+    "not causal, a window": dict(nq=[300], nk=[450], H=2, causal=False, window_left=90),
+    "1024 heads": dict(nq=[2, 1], nk=[70, 1], H=1024),
+    "many tiles": dict(nq=[257], nk=[6001], H=1),
+    "many tiles, growing maxima": dict(nq=[200], nk=[3001], H=2, q_scale=12.0),
+}
+
+
+@pytest.mark.parametrize("name", DENSE_TILES)
+def test_expanded_tiles(name):
+    c = dict(DENSE_TILES[name])
+    mask = dict(causal=c.get("causal", True), window_left=c.get("window_left", -1))
+    q, kn, kr, v, cu_q, cu_k, out, lse = dense_step(seed=37, **c)
+    check(out, lse, R.dense(q, kn, kr, v, cu_q, cu_k, SCALE, **mask), name)
+
+
+def test_expanded_head_major_and_captured():
+    """Keys and values stored head by head, and the call captured and replayed on another stream: the bits
+    of the token-major call."""
+    q, kn, kr, v, cu_q, cu_k, out, lse = dense_step([300, 70], [333, 70], 3, 43)
+    h = B.LatentHandle(num_heads=3, page_size=64, max_batch=2, max_total_tokens=370, max_num_pages=1, num_cache_pages=1)
+    ws = torch.empty(h.workspace_size(B.MODE_DENSE), dtype=torch.uint8, device="cuda")
+    h.plan_dense(cu_q, cu_k, workspace=ws, sm_scale=SCALE)
+    head_major = lambda t: t.permute(1, 0, 2).contiguous().cuda().permute(1, 0, 2)
+    args = (q.cuda(), head_major(kn), kr.cuda(), head_major(v))
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        h.run_dense(*args, o2, l2, workspace=ws)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        g.replay()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(o2), bits(out)) and torch.equal(l2, lse)
+
+
+def test_expanded_refuses_strides_it_cannot_step():
+    q, kn, kr, v, cu_q, cu_k, out, lse = dense_step([40], [40], 2, 47)
+    h = B.LatentHandle(num_heads=2, page_size=64, max_batch=1, max_total_tokens=40, max_num_pages=1, num_cache_pages=1)
+    ws = torch.empty(h.workspace_size(B.MODE_DENSE), dtype=torch.uint8, device="cuda")
+    h.plan_dense(cu_q, cu_k, workspace=ws, sm_scale=SCALE)
+    q, kn, kr, v = q.cuda(), kn.cuda(), kr.cuda(), v.cuda()
+    wide = torch.zeros(40, 2, 132, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(k_nope=kn[:, :1].expand(-1, 2, -1)),    # every head the same row: a stride of nothing
+                dict(v=wide[..., :128]),                      # rows 264 bytes apart
+                dict(k_rope=kr[:1].expand(40, -1))):
+        a = dict(q=q, k_nope=kn.contiguous(), k_rope=kr, v=v.contiguous(), out=out)
+        a.update(bad)
+        with pytest.raises(B.PkvError) as e:
+            h.run_dense(**a, workspace=ws)
+        assert e.value.status == B.ERR_INVALID
+
+
 def test_expanded_next_segment_does_not_leak():
     """Keys and values of the next segment hold infinities and NaN: the first one's result is the same."""
     q, kn, kr, v, cu_q, cu_k, out, lse = dense_step([50, 30], [50, 30], 2, 41)
