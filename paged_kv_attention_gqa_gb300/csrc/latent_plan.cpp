@@ -23,8 +23,10 @@ static Shape as_shape(const LatentShape &s) {
     return b;
 }
 
-// Key tiles a CTA is given at least (fewer would only add pieces to join).
-static constexpr int kMinTiles = 1;
+// What a piece of a unit costs beside its tiles, in tiles: its Q, the first S, and writing O, which the
+// next piece's first PV waits for.  (48 rows of 128 heads: 82.8 us with 0, 78.7 with 2, 85.4 with 4, where
+// CTAs that take no further piece leave too much to the others; a batch of 32 rows 41.2, 40.7, 41.0.)
+static constexpr long long kPieceCost = 2;
 
 namespace {
 struct Unit {
@@ -34,7 +36,7 @@ struct Unit {
 
 // A sequence's query rows f = token * H + head are cut into blocks of 64; (sequence, block) is a
 // unit over the key tiles any of its rows sees.  The blocks of one index over all sequences form a
-// lane; each lane gets CTAs in proportion to its tiles and is cut into equal runs of tiles.  With
+// lane; each lane gets CTAs in proportion to its tiles and is cut into equal runs of tiles and pieces.  With
 // equal blocks per sequence (a step of one token each) the lanes are cut alike, so the CTAs that
 // read the same keys for different heads do it at the same time and share them in L2.
 static void split_units(const LatentShape &s, const std::vector<std::vector<Unit>> &lanes, std::vector<LatentTile> &tiles,
@@ -53,20 +55,37 @@ static void split_units(const LatentShape &s, const std::vector<std::vector<Unit
     const long long cmax = std::max(1, s.sm_count);
     const bool flat = (long long)lanes.size() * 2 > cmax;  // more blocks than CTAs to give them: one lane
     auto cut = [&](const std::vector<const Unit *> &us, long long total, long long ctas) {
-        const long long per = std::max<long long>((total + ctas - 1) / ctas, kMinTiles);
+        // the least budget per CTA with which the run takes no more than `ctas` of them.  A CTA that has
+        // a piece takes no other one that its budget leaves no tile for
+        auto count = [&](long long per) {
+            long long n = 1, budget = per;
+            for (const Unit *u : us)
+                for (int used = 0; used < u->ntiles;) {
+                    if (budget <= kPieceCost) {
+                        ++n;
+                        budget = per;
+                    }
+                    const int take = (int)std::min<long long>(budget - kPieceCost, u->ntiles - used);
+                    used += take;
+                    budget -= take + kPieceCost;
+                }
+            return n;
+        };
+        long long per = kPieceCost + std::max<long long>((total + ctas - 1) / ctas, 1);
+        for (long long n; (n = count(per)) > ctas;) per += std::max<long long>(1, per * (n - ctas) / (4 * n));
         long long budget = per;
         for (const Unit *u : us) {
             int used = 0;
             const int first_tile = (int)tiles.size();
             while (used < u->ntiles) {
-                if (budget == 0) {
+                if (budget <= kPieceCost) {
                     cta_ptr.push_back((int32_t)tiles.size());
                     budget = per;
                 }
-                const int take = (int)std::min<long long>(budget, u->ntiles - used);
+                const int take = (int)std::min<long long>(budget - kPieceCost, u->ntiles - used);
                 tiles.push_back(LatentTile{u->q_row, u->n_rows, u->pos0, u->length, u->kv_base, u->tile0 + used, take, -1});
                 used += take;
-                budget -= take;
+                budget -= take + kPieceCost;
             }
             const int pieces = (int)tiles.size() - first_tile;
             if (pieces > 1) {

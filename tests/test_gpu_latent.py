@@ -138,6 +138,26 @@ CASES = {
 }
 
 
+# several blocks of 64 rows over the same keys
+BLOCKS = {
+    "128 heads, one row": dict(lens=[1], news=[1], H=128, P=64),
+    "128 heads, pages of 8": dict(lens=[200, 9, 1000], news=[1, 1, 1], H=128, P=8),
+    "128 heads, pages of 32, a row longer than the others": dict(lens=[70, 9000, 65], news=[1, 1, 1], H=128, P=32),
+    "100 heads": dict(lens=[300, 64, 65, 3000], news=[1, 1, 1, 1], H=100, P=64),
+    "256 heads": dict(lens=[300, 700], news=[1, 1], H=256, P=16),
+    "1024 heads": dict(lens=[130, 1], news=[1, 1], H=1024, P=64),
+    "64 heads, two tokens, not causal": dict(lens=[500, 64], news=[2, 2], H=64, P=16, causal=False),
+    "32 heads, four tokens": dict(lens=[500, 1000], news=[4, 4], H=32, P=64),
+    "128 heads, a window": dict(lens=[500, 90], news=[1, 1], H=128, P=16, window_left=70),
+    "128 heads, empty rows": dict(lens=[0, 33, 0, 5], news=[0, 1, 0, 1], H=128, P=8),
+    "128 heads, three CTAs": dict(lens=[400, 900, 64, 1, 700], news=[1] * 5, H=128, P=16, sm_count=3),
+    "128 heads, five CTAs": dict(lens=[400, 900, 64, 1, 700], news=[1] * 5, H=128, P=64, sm_count=5),
+    "128 heads, peaked scores": dict(lens=[900, 222], news=[1, 1], H=128, P=64, q_scale=8.0),
+    "some rows with one block": dict(lens=[400, 90], news=[2, 1], H=64, P=64),
+}
+CASES.update(BLOCKS)
+
+
 @pytest.mark.parametrize("name", CASES)
 def test_absorbed_step(name):
     c = CASES[name]
