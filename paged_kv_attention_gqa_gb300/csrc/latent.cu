@@ -29,6 +29,10 @@
 //  * A row's running maximum moves (and O is rescaled in tensor memory) only when it grows by more
 //    than 2^8.  Sums and maxima are 32-bit; P is rounded to bf16 for the MMA (relative 2^-8 a weight at
 //    most, as the output's own rounding), the sum adds the unrounded weights.
+// Measured, append and join included: 32 rows of 203 to 8,190 tokens, 16 heads, 156 MB: 41 us (23 at the
+// copy rate); 48 rows of 611 to 6,151, 128 heads: 79 us (2,580 cycles a tile, the rest pieces and their
+// join); one row of 517: 10 us.  Two CTAs sharing a sequence's tiles by multicast changed nothing at 128
+// heads: the copies are not what bounds it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

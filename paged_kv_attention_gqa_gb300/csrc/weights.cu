@@ -19,7 +19,9 @@
 // block's head and number found by division and first and last key read per column 36 / 62; steps of 64
 // columns (spilling registers) 40 / 67; an MMA warp a team 48 / 81; the lse as a k-step of the MMA 44 / 70.
 //
-// DECODE_WEIGHTS plans: the decode kernel has left its logits; a thread per key adds the weights.
+// DECODE_WEIGHTS plans: the decode kernel has left its logits; a thread per key adds the weights.  64 rows
+// of 517 to 8,190 tokens, 32 heads: 11 us for 36 MB of logits, most of them in L2 still, after 185 us of
+// decode and join.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
