@@ -90,7 +90,7 @@ int make_weights_plan(const Shape &s, int mode, const int32_t *qo, const int32_t
         err = "weights plans are causal (1) or non-causal (0)";
         return PKV_ERR_INVALID;
     }
-    int rc = decode ? make_plan(s, PKV_MODE_DECODE, nullptr, kvp, kvi, lpl, batch, 1, window_left, sm_scale, plan, err)
+    int rc = decode ? make_plan(s, PKV_MODE_DECODE, qo, kvp, kvi, lpl, batch, 1, window_left, sm_scale, plan, err)
                     : validate_rows(s, PKV_MODE_PREFILL, qo, kvp, kvi, lpl, batch, window_left, err, causal);
     if (rc) return rc;
     std::vector<uint8_t> seen;
