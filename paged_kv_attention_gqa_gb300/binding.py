@@ -115,23 +115,29 @@ def _i32(a):
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
-def _lists(**lists):
-    """The host index arrays of a plan as int32, in order, with the number of rows.  The library takes their
-    lengths on trust: kv_indptr (or cu_q) gives the rows, the others have an entry a row (indptr arrays
-    one more) and the ids that their indptr counts.  Longer arrays are fine; qo_indptr may be None."""
-    a = {name: _i32(x) for name, x in lists.items()}
-    rows = a["cu_q" if "cu_q" in a else "kv_indptr"]
-    batch = -1 if rows is None else rows.size - 1
-    counted = {"kv_indices": "kv_indptr", "dst_indices": "dst_indptr"}
-    for name, x in a.items():
-        if name in counted:
-            need = int(a[counted[name]][batch])
-        else:
-            need = batch if name in ("last_page_len", "keep") else max(batch, 0) + 1
-        have = 0 if x is None else x.size
-        if have < need and not (x is None and name == "qo_indptr"):
-            raise ValueError(f"{name} needs {need} entries, has {have}")
-    return list(a.values()), batch
+def _need(name, a, entries):
+    """The library takes the lengths of its host lists on trust: they are checked here (longer is fine)."""
+    if entries > 0 and (a is None or a.size < entries):
+        raise ValueError(f"{name} needs {entries} entries, has {0 if a is None else a.size}")
+
+
+def _paged_lists(qo_indptr, kv_indptr, kv_indices, last_page_len):
+    """The index arrays of a paged plan as int32 and its number of rows."""
+    qo, kvp, kvi, lpl = _i32(qo_indptr), _i32(kv_indptr), _i32(kv_indices), _i32(last_page_len)
+    _need("kv_indptr", kvp, 1)
+    batch = kvp.size - 1
+    if qo is not None:
+        _need("qo_indptr", qo, batch + 1)
+    _need("kv_indices", kvi, kvp.item(batch))
+    _need("last_page_len", lpl, batch)
+    return [qo, kvp, kvi, lpl], batch
+
+
+def _dense_lists(cu_q, cu_k):
+    cq, ck = _i32(cu_q), _i32(cu_k)
+    _need("cu_q", cq, 1)
+    _need("cu_k", ck, cq.size)
+    return cq, ck, cq.size - 1
 
 
 def _p(a):
@@ -225,14 +231,14 @@ class Handle:
 
     def plan(self, mode, qo_indptr, kv_indptr, kv_indices, last_page_len, *, workspace, causal=True,
              window_left=-1, sm_scale=0.0, stream=None):
-        arrs, batch = _lists(qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices, last_page_len=last_page_len)
+        arrs, batch = _paged_lists(qo_indptr, kv_indptr, kv_indices, last_page_len)
         self._keep = arrs  # host arrays are read synchronously; kept only for symmetry
         st = self.lib.pkv_plan(self.h, mode, *(_p(a) for a in arrs), batch,
                                int(causal) if causal == CONTEXT_ONLY else int(bool(causal)), int(window_left),
                                float(sm_scale), _dptr(workspace), workspace.numel() * workspace.element_size(),
                                _stream(stream))
         self._check(st)
-        self._planned_tokens = batch if arrs[0] is None else int(arrs[0][batch])
+        self._planned_tokens = batch if arrs[0] is None else arrs[0].item(batch)
 
     def kv_append(self, k, v, num_new_tokens, kv_layer, qo_indptr, kv_indptr, kv_indices, last_page_len, batch,
                   stream=None):
@@ -265,7 +271,7 @@ class Handle:
         self._run(self.lib.pkv_run_mixed, q, kv_layer, out, lse, workspace, stream)
 
     def plan_dense(self, cu_q, cu_k, *, workspace, causal=True, window_left=-1, sm_scale=0.0, stream=None):
-        (cq, ck), batch = _lists(cu_q=cu_q, cu_k=cu_k)
+        cq, ck, batch = _dense_lists(cu_q, cu_k)
         self._check(self.lib.pkv_plan_dense(self.h, _p(cq), _p(ck), batch, int(bool(causal)), int(window_left),
                                             float(sm_scale), _dptr(workspace),
                                             workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -311,8 +317,11 @@ class Handle:
                    num_recent=0, workspace, stream=None):
         """Row r keeps keep[r] tokens if it has more: the first num_sink, the last num_recent and the
         best-scored between; they move to the new pages dst_indices[dst_indptr[r]:dst_indptr[r + 1]]."""
-        a, batch = _lists(kv_indptr=kv_indptr, kv_indices=kv_indices, last_page_len=last_page_len, keep=keep,
-                          dst_indptr=dst_indptr, dst_indices=dst_indices)
+        lists, batch = _paged_lists(None, kv_indptr, kv_indices, last_page_len)
+        a = lists[1:] + [_i32(x) for x in (keep, dst_indptr, dst_indices)]
+        _need("keep", a[3], batch)
+        _need("dst_indptr", a[4], batch + 1)
+        _need("dst_indices", a[5], a[4].item(batch))
         if len(a[3]) != batch or len(a[4]) != batch + 1:
             raise ValueError("keep has one entry per row, dst_indptr one more")
         self._check(self.lib.pkv_plan_evict(self.h, _p(a[0]), _p(a[1]), _p(a[2]), batch, _p(a[3]), int(num_sink),
@@ -412,11 +421,11 @@ class LatentHandle:
     def plan(self, qo_indptr, kv_indptr, kv_indices, last_page_len, *, workspace, sm_scale, causal=True,
              window_left=-1, stream=None):
         """qo_indptr None: one new token per row."""
-        arrs, batch = _lists(qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices, last_page_len=last_page_len)
+        arrs, batch = _paged_lists(qo_indptr, kv_indptr, kv_indices, last_page_len)
         self._check(self.lib.pkv_latent_plan(self.h, *(_p(a) for a in arrs), batch, int(bool(causal)), int(window_left),
                                              float(sm_scale), _dptr(workspace),
                                              workspace.numel() * workspace.element_size(), _stream(stream)))
-        self._tokens = batch if arrs[0] is None else int(arrs[0][batch])
+        self._tokens = batch if arrs[0] is None else arrs[0].item(batch)
 
     def _rows(self, name, t, width, torch, device):
         """Pointer and row stride of a [tokens, width] tensor whose rows may be strided."""
@@ -454,11 +463,11 @@ class LatentHandle:
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def plan_dense(self, cu_q, cu_k, *, workspace, sm_scale, causal=True, window_left=-1, stream=None):
-        (cq, ck), batch = _lists(cu_q=cu_q, cu_k=cu_k)
+        cq, ck, batch = _dense_lists(cu_q, cu_k)
         self._check(self.lib.pkv_latent_plan_dense(self.h, _p(cq), _p(ck), batch, int(bool(causal)),
                                                    int(window_left), float(sm_scale), _dptr(workspace),
                                                    workspace.numel() * workspace.element_size(), _stream(stream)))
-        self._tokens, self._keys = int(cq[batch]), int(ck[batch])
+        self._tokens, self._keys = cq.item(batch), ck.item(batch)
 
     def run_dense(self, q, k_nope, k_rope, v, out, lse=None, *, workspace, stream=None):
         """Expanded form: q [T, heads, 192], k_nope and v [keys, heads, 128], k_rope [keys, 64] (these three
