@@ -125,11 +125,12 @@ def _paged_lists(qo_indptr, kv_indptr, kv_indices, last_page_len):
     """The index arrays of a paged plan as int32 and its number of rows."""
     qo, kvp, kvi, lpl = _i32(qo_indptr), _i32(kv_indptr), _i32(kv_indices), _i32(last_page_len)
     _need("kv_indptr", kvp, 1)
-    batch = kvp.size - 1
+    batch = len(kvp) - 1
+    if kvi is None or lpl is None or len(kvi) < kvp[-1] or len(lpl) < batch:
+        _need("kv_indices", kvi, kvp[-1])
+        _need("last_page_len", lpl, batch)
     if qo is not None:
         _need("qo_indptr", qo, batch + 1)
-    _need("kv_indices", kvi, kvp.item(batch))
-    _need("last_page_len", lpl, batch)
     return [qo, kvp, kvi, lpl], batch
 
 
