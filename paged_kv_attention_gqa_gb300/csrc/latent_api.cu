@@ -32,13 +32,20 @@ static pkv_status cuda_fail(pkv_latent_t h, cudaError_t e, const char *what) {
     return fail(h, PKV_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-// No C++ exception crosses the C boundary: the planners' host buffers may fail to grow.
+// No C++ exception crosses the C boundary: the planners' host buffers may fail to grow.  The text of the
+// exception becomes the handle's; if there is no memory for that either, the last one is cleared.
 template <typename F>
 static pkv_status guarded(pkv_latent_t h, F &&f) {
     try {
         return f();
-    } catch (const std::exception &) {
+    } catch (const std::exception &ex) {
         if (h) h->planned_ws = nullptr;
+        std::string &err = h ? h->err : g_latent_create_err;
+        err.clear();
+        try {
+            err = ex.what();
+        } catch (const std::exception &) {
+        }
         return PKV_ERR_INVALID;
     }
 }

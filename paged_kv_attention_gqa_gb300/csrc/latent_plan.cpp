@@ -146,7 +146,7 @@ int make_latent_plan(const LatentShape &s, const int32_t *qo, const int32_t *kvp
     const Shape b = as_shape(s);
     std::vector<int32_t> iota;
     if (!qo && batch >= 0 && batch <= s.max_batch) {
-        iota.resize(batch + 1);
+        iota.resize((size_t)batch + 1);
         for (int r = 0; r <= batch; ++r) iota[r] = r;
         qo = iota.data();
     }
