@@ -383,7 +383,9 @@ pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t 
  * head's query is [q W_uk^T | q_rope] (latent_dim + rope_dim values), its keys are the cached
  * vectors, its values their first latent_dim columns; the caller multiplies the output by W_uv.
  * Rows, new tokens, causal, window_left and lse mean what they mean for pkv_plan in prefill
- * mode; every row may have any number of new tokens, one (a decode step) included.
+ * mode; every row may have any number of new tokens, one (a decode step) included.  Vectors that a
+ * query does not see (later tokens of its row, tokens before its window) never reach it, NaN and
+ * infinities in them included.
  *
  * Expanded form (prompts): contiguous per-head keys [k_nope | k_rope], k_rope shared by all
  * heads, and per-head values, both made from the latent vectors by the caller; segments as in

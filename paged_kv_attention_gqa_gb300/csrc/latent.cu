@@ -26,6 +26,10 @@
 //    for S (3,940 cycles per 64 keys).
 //  * Warps 0-3 softmax (16 rows each, a quad per row pair), 4 and 7-9 copy tiles, 5 issues S, 10 issues
 //    PV (a warp each, so that neither's wait holds up the other), 6 copies Q.
+//  * A key that a row does not see has weight 0, but 0 * NaN would reach O.  Those that no row of the unit
+//    sees are zeroed in shared memory; a tile with keys that some rows see and others do not (several
+//    tokens of a step, causal or windowed) is looked over by warp 10 before its PV, and one that holds NaN or
+//    infinities there is left to the softmax warps, each row adding the keys it sees.
 //  * A row's running maximum moves (and O is rescaled in tensor memory) only when it grows by more
 //    than 2^8.  Sums and maxima are 32-bit; P is rounded to bf16 for the MMA (relative 2^-8 a weight at
 //    most, as the output's own rounding), the sum adds the unrounded weights.
@@ -77,6 +81,79 @@ struct LatentArgs {
     int oob_row;      // a row past the cache: TMA fills zeros
 };
 
+// The positions that the rows of a unit see.  Their keys range over [lo_min, hi_max]; all rows see
+// [lo_max, hi_min] of them, and of the rest some rows see one and others do not (causal or windowed units
+// of several tokens).
+struct LatentSeen {
+    int lo_min, lo_max, hi_min, hi_max;
+};
+__device__ __forceinline__ LatentSeen latent_seen(const LatentTile &t, int heads, int causal, int window_left) {
+    const int first = t.pos0 + t.q_row / heads, last = t.pos0 + (t.q_row + t.n_rows - 1) / heads;
+    LatentSeen u;
+    u.lo_min = window_left >= 0 ? max(0, first - window_left) : 0;
+    u.lo_max = window_left >= 0 ? max(0, last - window_left) : 0;
+    u.hi_min = causal ? first : t.length - 1;
+    u.hi_max = causal ? last : t.length - 1;
+    return u;
+}
+// The piece's tiles that hold keys which some rows see and others do not: those below `low` and from `high`.
+struct LatentMixed {
+    int low, high;
+    __device__ __forceinline__ bool operator()(int j) const { return j < low || j >= high; }
+};
+__device__ __forceinline__ LatentMixed latent_mixed(const LatentSeen &u, int tile0) {
+    LatentMixed m;
+    m.low = u.lo_min < u.lo_max ? (u.lo_max + kLatentKeys - 1) / kLatentKeys - tile0 : 0;
+    m.high = u.hi_min < u.hi_max ? (u.hi_min + 1) / kLatentKeys - tile0 : INT_MAX;
+    return m;
+}
+
+// O += P C of one tile without the tensor cores, for tiles that hold NaN or infinities in a key that
+// some rows see and others do not: each row adds the keys it sees alone.  A thread holds the two rows and
+// the columns of tmem_ld16x64; P is read back from shared memory.
+__device__ __noinline__ void latent_pv_rows(uint32_t o_addr, const uint8_t *tile, const uint8_t *p_sm, int row_a,
+                                            int quad, int key0, int lo_a, int hi_a, int lo_b, int hi_b, float al_a, float al_b,
+                                            bool first) {
+    const int row_b = row_a + 8;
+#pragma unroll 1
+    for (int n = 0; n < kLatentDim / 64; ++n) {
+        uint32_t r[32];
+        float o[32];
+        __syncwarp();
+        tmem_ld16x64(o_addr + 64 * n, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = first ? 0.f : __uint_as_float(r[i]) * ((i & 2) ? al_b : al_a);
+        const uint8_t *chunk = tile + n * LtSmem::CHUNK + quad * 4;
+#pragma unroll 1
+        for (int k = 0; k < kLatentKeys; ++k) {
+            const bool sees_a = key0 + k >= lo_a && key0 + k <= hi_a, sees_b = key0 + k >= lo_b && key0 + k <= hi_b;
+            if (!sees_a && !sees_b) continue;
+            auto weight = [&](int row) {
+                return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p_sm + swz128(row, k >> 3) + (k & 7) * 2));
+            };
+            const float p_a = weight(row_a), p_b = weight(row_b);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(chunk + swz128(k, c)));
+                if (sees_a) {
+                    o[4 * c] = fmaf(p_a, v.x, o[4 * c]);
+                    o[4 * c + 1] = fmaf(p_a, v.y, o[4 * c + 1]);
+                }
+                if (sees_b) {
+                    o[4 * c + 2] = fmaf(p_b, v.x, o[4 * c + 2]);
+                    o[4 * c + 3] = fmaf(p_b, v.y, o[4 * c + 3]);
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i]);
+        tmem_st16x64(o_addr + 64 * n, r);
+    }
+    tmem_wait_st();
+}
+
 __global__ void __launch_bounds__(kLtThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_q,
                   const LatentArgs a) {
@@ -95,7 +172,9 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     uint64_t *q_full = bars + 8;   // the piece's Q landed
     uint64_t *q_empty = bars + 9;  // the piece's last S completed
     uint64_t *o_free = bars + 10;  // the piece's O has been read
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 11);
+    uint64_t *checked = bars + 11;  // a tile with keys that not all rows see has been looked over
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 12);
+    uint32_t *by_rows = tmem_holder + 1;  // it holds NaN or infinities there: its PV goes by rows
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -133,6 +212,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(o_free, 4);
+        mbar_init(checked, 1);
         fence_barrier_init();
         prefetch_tmap(&tm_cache);
         prefetch_tmap(&tm_q);
@@ -234,35 +314,74 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         bool ok = true;
         for (int ti = t_begin; ti < t_end && ok; ++ti, ++pc) {
             const LatentTile t = ti == t_begin ? first_tile : a.tiles[ti];
+            const LatentSeen u = latent_seen(t, a.num_heads, a.hdr->causal, a.hdr->window_left);
+            const LatentMixed mixed = latent_mixed(u, t.tile0);
+            // the piece's tiles below edge_low and from edge_high hold keys that not all rows see
+            const int page_end = (t.length + P - 1) & ~(P - 1);
+            const int edge_low = (u.lo_max + kLatentKeys - 1) / kLatentKeys - t.tile0;
+            const int edge_high = u.hi_min + 1 < page_end ? (u.hi_min + 1) / kLatentKeys - t.tile0 : INT_MAX;
             // O may be overwritten once the last piece's has been read
             if (pc > 0) ok = mbar_wait(o_free, (pc - 1) & 1, err, kErrWaitEmpty);
             for (int j = 0; j < t.ntiles && ok; ++j, ++it) {
                 const uint32_t b = it & 1;
-                // Cache rows of the sequence's last page past its end hold anything; their P is 0, but
-                // 0 * NaN would reach O: zero them (S of these columns is masked whatever it reads)
-                const int key0 = (t.tile0 + j) * kLatentKeys;
-                const int zb = max(t.length, key0), ze = min((t.length + P - 1) & ~(P - 1), key0 + kLatentKeys);
-                if (zb < ze) {
+                bool rows = false;
+                if (j < edge_low || j >= edge_high) {
                     ok = mbar_wait(&full[b], (it >> 1) & 1, err, kErrWaitFull);
                     if (!ok) break;
-                    for (int e = lane; e < (ze - zb) * kLtValueChunks * 8; e += 32) {
-                        const int k = zb - key0 + e / (kLtValueChunks * 8), c = e % (kLtValueChunks * 8);
-                        *reinterpret_cast<uint4 *>(k_sm + b * L::TILE + (c >> 3) * L::CHUNK + swz128(k, c & 7)) =
-                            make_uint4(0, 0, 0, 0);
+                    uint8_t *const tile = k_sm + b * L::TILE;
+                    // Keys that no row of the unit sees hold anything (past the sequence's end to the end of its
+                    // last page, behind the last row's position, before the window); their P is 0, but 0 * NaN
+                    // would reach O: zero them (S of these columns is masked whatever it reads)
+                    const int key0 = (t.tile0 + j) * kLatentKeys, ze = min(page_end, key0 + kLatentKeys);
+                    const int n_low = max(0, min(u.lo_min, ze) - key0), high = max(u.hi_max + 1, key0);
+                    const int n_zero = n_low + max(0, ze - high);
+                    for (int e = lane; e < n_zero * kLtValueChunks * 8; e += 32) {
+                        const int i = e / (kLtValueChunks * 8), c = e % (kLtValueChunks * 8);
+                        const int k = i < n_low ? i : high - key0 + i - n_low;
+                        *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::CHUNK + swz128(k, c & 7)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
+                    // Keys that some rows see and others do not stay; a NaN or an infinity among them goes to
+                    // the rows that see it, one by one
+                    if (mixed(j)) {
+                        const int begin = max(key0, u.lo_min), end = min(key0 + kLatentKeys, u.hi_max + 1);
+                        const int first = (begin < u.lo_max ? begin : max(begin, u.hi_min + 1)) - key0;
+                        const int n = ((u.hi_min + 1 < end ? end : min(end, u.lo_max)) - key0 - first) * kLtValueChunks * 8;
+                        uint32_t f0 = 0, f1 = 0;
+                        for (int e0 = lane; e0 < n; e0 += 4 * 32) {  // four vectors in flight
+                            uint4 x[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = min(e0 + 32 * i, n - 1), c = e % (kLtValueChunks * 8);
+                                x[i] = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * L::CHUNK +
+                                                                        swz128(first + e / (kLtValueChunks * 8), c & 7));
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                f0 = keep_nonfinite(x[i].x, keep_nonfinite(x[i].y, f0));
+                                f1 = keep_nonfinite(x[i].z, keep_nonfinite(x[i].w, f1));
+                            }
+                        }
+                        rows = __any_sync(0xffffffffu, has_nan(f0) || has_nan(f1));
+                        if (lane == 0) {
+                            *by_rows = rows;
+                            mbar_arrive(checked);
+                        }
+                    }
                     __syncwarp();
                 }
                 ok = mbar_wait(p_full, it & 1, err, kErrWaitFull);
                 if (!ok) break;
                 tc_fence_after();
+                if (!rows) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int kk = 0; kk < kLatentKeys / 16; ++kk)
-                        mma_ss_elect(tmem + 256u * h, add(dP, kk * 32),
-                                     add(dV, b * L::TILE + h * 4 * L::CHUNK + kk * 2048), ID_O,
-                                     (j > 0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < kLatentKeys / 16; ++kk)
+                            mma_ss_elect(tmem + 256u * h, add(dP, kk * 32),
+                                         add(dV, b * L::TILE + h * 4 * L::CHUNK + kk * 2048), ID_O,
+                                         (j > 0 || kk > 0) ? 1u : 0u);
+                }
                 mma_commit_elect(&empty[b]);
                 mma_commit_elect(pv_done);
             }
@@ -276,7 +395,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         const float sl = a.hdr->scale_log2;
         const int causal = a.hdr->causal, window_left = a.hdr->window_left;
         uint8_t *const pa = p_sm + quad * 4;
-        uint32_t it = 0, pc = 0;
+        uint32_t it = 0, pc = 0, checks = 0;  // tiles of `checked` so far
         bool ok = true;
         for (int ti = t_begin; ti < t_end && ok; ++ti, ++pc) {
             const LatentTile t = ti == t_begin ? first_tile : a.tiles[ti];
@@ -294,6 +413,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
             range(row_a, lo_a, hi_a);
             range(row_b, lo_b, hi_b);
             const int lo_max = max(lo_a, lo_b), hi_min = min(hi_a, hi_b);
+            const LatentMixed mixed = latent_mixed(latent_seen(t, a.num_heads, causal, window_left), t.tile0);
             float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
             for (int j = 0; j < t.ntiles; ++j, ++it) {
                 const uint32_t b = it & 1;
@@ -302,6 +422,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
                     break;
                 }
                 if (idle) {  // P's rows of this warp stay as they are: O's are never read
+                    checks += mixed(j);
                     if (it > 0 && !mbar_wait(pv_done, (it - 1) & 1, err, kErrWaitFull)) {
                         ok = false;
                         break;
@@ -376,18 +497,32 @@ __global__ void __launch_bounds__(kLtThreads, 1)
                     *reinterpret_cast<uint32_t *>(pa + swz128(row_b, c)) = pk[2 * c + 1];
                 }
                 fence_proxy_async_smem();
-                if (any && j > 0) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < kLatentDim; c0 += 64) {
-                        uint32_t o[32];
-                        tmem_ld16x64(tmem + lane_off + c0, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * ((i & 2) ? al_b : al_a));
-                        tmem_st16x64(tmem + lane_off + c0, o);
+                if ((any && j > 0) || mixed(j)) {
+                    bool rows = false;
+                    if (mixed(j)) {
+                        if (!mbar_wait(checked, checks++ & 1, err, kErrWaitFull) ||
+                            !mbar_wait(&full[b], (it >> 1) & 1, err, kErrWaitFull)) {  // (has: S(it) has read the tile)
+                            ok = false;
+                            break;
+                        }
+                        rows = *by_rows != 0;
                     }
-                    tmem_wait_st();
+                    if (rows) {
+                        latent_pv_rows(tmem + lane_off, k_sm + b * L::TILE, p_sm, row_a, quad, key0, lo_a, hi_a, lo_b, hi_b,
+                                       al_a, al_b, j == 0);
+                    } else if (any && j > 0) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kLatentDim; c0 += 64) {
+                            uint32_t o[32];
+                            tmem_ld16x64(tmem + lane_off + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * ((i & 2) ? al_b : al_a));
+                            tmem_st16x64(tmem + lane_off + c0, o);
+                        }
+                        tmem_wait_st();
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();

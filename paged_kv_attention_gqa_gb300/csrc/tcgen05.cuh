@@ -172,6 +172,18 @@ __device__ __forceinline__ void tmem_st16x64(uint32_t taddr, const uint32_t (&r)
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// ---- values that a product with a weight of 0 does not cancel ----------------------------
+
+// 0 * x + t in each half of a word of two bf16: NaN once x is NaN or infinite, else t.
+__device__ __forceinline__ uint32_t keep_nonfinite(uint32_t x, uint32_t t) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(t));
+    return d;
+}
+__device__ __forceinline__ bool has_nan(uint32_t t) {  // of two bf16
+    return (t & 0x7fffu) > 0x7f80u || (t & 0x7fff0000u) > 0x7f800000u;
+}
+
 // ---- packed / fused FP32 forms of sm_100-class cores (softmax arithmetic) -----------
 
 __device__ __forceinline__ float ex2_ftz(float x) {
