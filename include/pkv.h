@@ -389,7 +389,7 @@ pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t 
  *
  * Expanded form (prompts): contiguous per-head keys [k_nope | k_rope], k_rope shared by all
  * heads, and per-head values, both made from the latent vectors by the caller; segments as in
- * pkv_plan_dense.
+ * pkv_plan_dense.  Masked keys and values as above.
  *
  * Widths: latent_dim 512, rope_dim 64, nope_dim 128, v_dim 128 (0 selects these); others are
  * PKV_ERR_UNSUPPORTED.  page_size: a power of two from 8 to 1024.  num_heads: 1 to 1024.

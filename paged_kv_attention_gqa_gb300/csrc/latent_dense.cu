@@ -11,7 +11,12 @@
 //  * warps 9 and 10 issue S = Q K^T of Q0 and Q1 (12 k-steps, N = 64), up to two tiles ahead of the
 //    softmax, warps 11 and 12 O += P V (4 k-steps, N = 128, P from tensor memory over its S);
 //  * warps 0-3 and 4-7 run the softmax of Q0 and Q1, a thread a query.  The running maximum moves, and
-//    O is rescaled, only when it grows by more than 2^8.
+//    O is rescaled, only when it grows by more than 2^8;
+//  * warps 13 and 14 look over the value tiles that some queries of Q0 or Q1 see and others do not
+//    (causal diagonal, window edges) as they land: the weight of a value that a query does not see is 0,
+//    but 0 * NaN would reach it.  A tile that holds NaN or infinities there is left to the softmax
+//    warps, each query adding the values it sees.  (In the PV warps, between two tiles, the look cost 14 us of
+//    the 234 below; in warps of its own 2 %.)
 // Tensor memory: two S buffers of 64 columns and an O of 128 for each query tile, all 512 columns.
 // Tiles of 128 keys leave room for one S each; then a query tile's S, softmax and PV wait for one
 // another, two chains of 4,600 cycles per 128 keys against 2,560 of MMAs: 305 us (32 heads, prompts of
@@ -23,6 +28,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <climits>
 
 #include "latent.h"
 #include "launch.h"
@@ -48,7 +55,7 @@ struct LdSmem {
     static constexpr uint32_t K_OFF = 2 * QC * QCHUNK;
     static constexpr uint32_t V_OFF = K_OFF + STAGES * KC * CHUNK;
     static constexpr uint32_t BAR_OFF = V_OFF + STAGES * VC * CHUNK;
-    static constexpr uint32_t BYTES = BAR_OFF + 256;
+    static constexpr uint32_t BYTES = BAR_OFF + 320;
 };
 static_assert(1024 + LdSmem::BYTES <= 227 * 1024, "the expanded latent kernel fits shared memory");
 
@@ -59,6 +66,63 @@ struct LatentDenseArgs {
     PlanHeader *hdr;
     int num_heads;
 };
+
+// The tiles (counted from kt0) with keys that some queries of a query tile see and others do not: those below
+// `low`, whose keys start before `lo_max`, and those from `high`, that hold key `hi_min` + 1 or later ones.
+struct LdMixed {
+    int lo_max, hi_min, low, high;
+    __device__ __forceinline__ bool operator()(int j) const { return j < low || j >= high; }
+};
+__device__ __forceinline__ LdMixed ld_mixed(const PrefillTile &t, int x, int kt0, int causal, int window_left) {
+    const int first = t.pos0 + x * kLdQueries, last = t.pos0 + min(t.n_q, (x + 1) * kLdQueries) - 1;
+    LdMixed m;
+    m.lo_max = window_left >= 0 ? max(0, last - window_left) : 0;
+    m.hi_min = causal == 1 ? first : t.length - 1;
+    m.low = (m.lo_max + kLdKeys - 1) / kLdKeys - kt0;
+    m.high = m.hi_min + 1 < t.length ? (m.hi_min + 1) / kLdKeys - kt0 : INT_MAX;
+    return m;
+}
+
+// O += P V of one tile without the tensor cores, for tiles that hold NaN or infinities in a key that
+// some queries see and others do not: each query adds the keys [lo, hi] that it sees alone.  P is read back
+// from tensor memory.
+__device__ __noinline__ void ld_pv_rows(uint32_t o_addr, uint32_t p_addr, const uint8_t *v, int key0, int lo, int hi,
+                                        float alpha, bool first) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < kLatentV; c0 += 32) {
+        uint32_t r[32];
+        float o[32];
+        tmem_ld32(o_addr + c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = first ? 0.f : __uint_as_float(r[c]) * alpha;
+        const uint8_t *chunk = v + (c0 >> 6) * LdSmem::CHUNK;
+#pragma unroll 1
+        for (int k = 0; k < kLdKeys; ++k) {
+            __syncwarp();
+            const uint32_t pair = tmem_ld1(p_addr + (k >> 1));
+            tmem_wait_ld();
+            const float p = __uint_as_float((k & 1) ? pair & 0xffff0000u : pair << 16);
+            if (key0 + k >= lo && key0 + k <= hi) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(chunk + swz128(k, ((c0 & 63) >> 3) + i));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        o[8 * i + 2 * c] = fmaf(p, __uint_as_float(w[c] << 16), o[8 * i + 2 * c]);
+                        o[8 * i + 2 * c + 1] = fmaf(p, __uint_as_float(w[c] & 0xffff0000u), o[8 * i + 2 * c + 1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(o[c]);
+        tmem_st32(o_addr + c0, r);
+    }
+    tmem_wait_st();
+}
 
 __global__ void __launch_bounds__(kLdThreads, 1)
     latent_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -72,12 +136,14 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     uint64_t *k_full = bars + 2;     // [3] K stage landed
     uint64_t *k_empty = bars + 5;    // [3] the S MMAs that read it completed (one arrival per query tile)
     uint64_t *v_full = bars + 8;     // [3] V stage landed
-    uint64_t *v_empty = bars + 11;   // [3] the PV MMAs that read it completed
+    uint64_t *v_empty = bars + 11;   // [3] the PV MMAs that read it completed, and it has been looked over
     uint64_t *s_full = bars + 14;    // [2][2] S_X(j) in buffer j & 1
     uint64_t *p_full = bars + 18;    // [2][2] P_X(j) written over S_X(j) (and O_X rescaled if it had to be)
     uint64_t *pv_done = bars + 22;   // [2][2] PV_X(j) completed, of buffer j & 1
     uint64_t *v_tail = bars + 26;    // the value rows past the segment are zero (at most one tile)
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 27);
+    uint64_t *checked = bars + 27;   // [2][3] the V stage has been looked over for X
+    uint32_t *by_rows = reinterpret_cast<uint32_t *>(bars + 33);  // [2][3] its PV goes by rows
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 36);
 
     const PrefillTile t = a.tiles[blockIdx.x];
     int *const err = &a.hdr->err;
@@ -105,7 +171,9 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             mbar_init(&k_full[s], 1);
             mbar_init(&v_full[s], 1);
             mbar_init(&k_empty[s], two ? 2 : 1);
-            mbar_init(&v_empty[s], two ? 2 : 1);
+            mbar_init(&v_empty[s], two ? 4 : 2);
+            mbar_init(&checked[s], 1);
+            mbar_init(&checked[3 + s], 1);
         }
         mbar_init(v_tail, 1);
         fence_barrier_init();
@@ -204,6 +272,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             const uint64_t dV = smem_desc(smem_u32(sm + L::V_OFF), L::CHUNK, 1024, kSwizzle128B);
             const uint32_t hi = (uint32_t)(dV >> 32);
             const uint32_t Sx = S_col(x), Ox = O_col(x);
+            const LdMixed mixed = ld_mixed(t, x, kt0, causal, a.hdr->window_left);
             bool ok = true;
             int s = 0, ph = 0;
             for (int j = 0; j < nt && ok; ++j) {
@@ -232,10 +301,12 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t lV = (uint32_t)dV + ((s * L::VC * L::CHUNK) >> 4);
+                    if (!(mixed(j) && by_rows[3 * x + s])) {  // (written before the softmax warps arrived)
 #pragma unroll
-                    for (int kk = 0; kk < kLdKeys / 16; ++kk)
-                        mma_ts_elect(Ox, Sx + 64u * (j & 1) + kk * 8, ((uint64_t)hi << 32) | (lV + kk * (2048 >> 4)),
-                                     ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < kLdKeys / 16; ++kk)
+                            mma_ts_elect(Ox, Sx + 64u * (j & 1) + kk * 8, ((uint64_t)hi << 32) | (lV + kk * (2048 >> 4)),
+                                         ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                    }
                     mma_commit_elect(&pv_done[2 * x + (j & 1)]);
                     mma_commit_elect(&v_empty[s]);
                 } else if (lane == 0) {
@@ -245,6 +316,45 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             }
             if (!ok)
                 for (uint32_t k = 0; k < 1024; ++k) __nanosleep(1000);
+        } else if (warp == 13 || (warp == 14 && two)) {
+            // ------------------------------------------------ values that not all queries see
+            // A NaN or an infinity among the values that some queries of X see and others do not would reach
+            // all of them, as 0 * NaN: such tiles are left to the softmax warps, which add to each query the
+            // keys it sees.  The stages are looked over as they land, ahead of their use; those that every
+            // query sees are passed on at once.
+            const int x = warp - 13, ntx = x == 0 ? nt0 : nt;
+            const LdMixed mixed = ld_mixed(t, x, kt0, causal, a.hdr->window_left);
+            int s = 0, ph = 0;
+            for (int j = 0; j < nt; ++j) {
+                if (!mbar_wait(&v_full[s], ph, err, kErrWaitFull)) break;
+                if (j < ntx && mixed(j)) {
+                    const int key0 = (kt0 + j) * kLdKeys, end = min(key0 + kLdKeys, t.length);
+                    const int k_begin = (j < mixed.low ? key0 : max(key0, mixed.hi_min + 1)) - key0;
+                    const int k_end = (j >= mixed.high ? end : min(end, mixed.lo_max)) - key0;
+                    // a lane reads 16 bytes of every second key, four of them in flight
+                    const uint8_t *const v = sm + L::V_OFF + (s * L::VC + ((lane >> 3) & 1)) * L::CHUNK;
+                    uint32_t f0 = 0, f1 = 0;
+                    for (int k0 = k_begin + (lane >> 4); k0 < k_end; k0 += 8) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = *reinterpret_cast<const uint4 *>(v + swz128(min(k0 + 2 * i, k_end - 1), lane & 7));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f0 = keep_nonfinite(w[i].x, keep_nonfinite(w[i].y, f0));
+                            f1 = keep_nonfinite(w[i].z, keep_nonfinite(w[i].w, f1));
+                        }
+                    }
+                    const bool rows = __any_sync(0xffffffffu, has_nan(f0) || has_nan(f1));
+                    if (lane == 0) by_rows[3 * x + s] = rows;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&checked[3 * x + s]);
+                    mbar_arrive(&v_empty[s]);
+                }
+                if (++s == L::STAGES) s = 0, ph ^= 1;
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLdSoftmaxRegs));
@@ -261,6 +371,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             const int lo = window_left >= 0 ? max(0, pos - window_left) : 0;
             const float sl = a.hdr->scale_log2;
             const uint32_t Sx = S_col(x) + lane_off, Ox = O_col(x) + lane_off;
+            const LdMixed mixed = ld_mixed(t, x, kt0, causal, window_left);
             float m_run = -INFINITY, l_run = 0.f;
             bool ok = true;
             for (int j = 0; j < ntx; ++j) {
@@ -326,23 +437,43 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u0, u1);
                 l_run = l_run * alpha + (u0 + u1);
                 tmem_wait_st();
-                if (warp_grow) {
-                    // O holds P_0..P_{j-1} V: wait for the last of those MMAs, then scale O's rows
-                    if (!mbar_wait(&pv_done[2 * x + ((j - 1) & 1)], ((j - 1) >> 1) & 1, err, kErrWaitFull)) {
-                        ok = false;
-                        break;
+                if (warp_grow || mixed(j)) {
+                    bool rows = false;
+                    if (mixed(j)) {
+                        const int s = j % L::STAGES;
+                        if (!mbar_wait(&checked[3 * x + s], (j / L::STAGES) & 1, err, kErrWaitFull) ||
+                            !mbar_wait(&v_full[s], (j / L::STAGES) & 1, err, kErrWaitFull)) {  // (has: it was looked over)
+                            ok = false;
+                            break;
+                        }
+                        rows = by_rows[3 * x + s] != 0;
+                        if (rows) {
+                            if (j > 0 && !mbar_wait(&pv_done[2 * x + ((j - 1) & 1)], ((j - 1) >> 1) & 1, err, kErrWaitFull)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            ld_pv_rows(Ox, Sj, sm + L::V_OFF + s * L::VC * L::CHUNK, key0, lo, hi, alpha, j == 0);
+                        }
                     }
-                    tc_fence_after();
+                    if (warp_grow && !rows) {
+                        // O holds P_0..P_{j-1} V: wait for the last of those MMAs, then scale O's rows
+                        if (!mbar_wait(&pv_done[2 * x + ((j - 1) & 1)], ((j - 1) >> 1) & 1, err, kErrWaitFull)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kLatentV; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(Ox + c0, o);
-                        tmem_wait_ld();
+                        for (int c0 = 0; c0 < kLatentV; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(Ox + c0, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                        tmem_st32(Ox + c0, o);
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            tmem_st32(Ox + c0, o);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();

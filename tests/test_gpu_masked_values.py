@@ -126,6 +126,60 @@ def test_absorbed(name):
             check(out[a:b], lse[a:b], ref, name)
 
 
+EXPANDED = {
+    "a short prompt": dict(nq=[40], nk=[40], H=2, bad={10: NAN, 35: INF}),
+    "every query alone": dict(nq=[128], nk=[128], H=1, bad={0: -INF, 64: NAN, 127: INF}),
+    "both query tiles": dict(nq=[256, 200], nk=[256, 300], H=2, bad={63: INF, 64: NAN, 130: INF, 199: NAN, 255: -INF}),
+    "odd lengths": dict(nq=[129, 190, 3], nk=[191, 193, 64], H=2, bad={63: NAN, 120: INF, 190: NAN}),
+    "a window": dict(nq=[300, 20], nk=[300, 400], H=2, window_left=100, bad={5: NAN, 150: INF, 295: NAN}),
+    "a window shorter than a tile": dict(nq=[300], nk=[700], H=1, window_left=3, bad={401: NAN, 500: INF, 640: -INF}),
+    "not causal, a window": dict(nq=[300], nk=[450], H=2, causal=False, window_left=90, bad={70: NAN, 200: INF}),
+    "many tiles": dict(nq=[257], nk=[2001], H=1, bad={1800: NAN, 1999: INF}),
+    "growing maxima": dict(nq=[200], nk=[1001], H=2, q_scale=12.0, bad={900: NAN, 990: NAN}),
+}
+
+
+@pytest.mark.parametrize("columns", [[5], [0, 31, 32, 127], None])
+@pytest.mark.parametrize("name", EXPANDED)
+def test_expanded(name, columns):
+    c = dict(causal=True, window_left=-1, q_scale=1.0)
+    c.update(EXPANDED[name])
+    nq, nk, H = c["nq"], c["nk"], c["H"]
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (nq, nk))
+    T, K = int(cu_q[-1]), int(cu_k[-1])
+    q = (randn(1, T, H, 192).float() * c["q_scale"]).to(torch.bfloat16)
+    kn, kr, v = randn(2, K, H, 128), randn(3, K, 64), randn(4, K, H, 128)
+    for s, L in enumerate(nk):
+        for at, value in c["bad"].items():
+            if at < L:
+                v[cu_k[s] + at, H - 1, columns or slice(0, 128)] = value  # the first head of two stays clean
+    h = B.LatentHandle(num_heads=H, page_size=64, max_batch=len(nq), max_total_tokens=T, max_num_pages=1, num_cache_pages=1)
+    ws = torch.empty(h.workspace_size(B.MODE_DENSE), dtype=torch.uint8, device="cuda")
+    h.plan_dense(cu_q, cu_k, workspace=ws, sm_scale=SCALE, causal=c["causal"], window_left=c["window_left"])
+    out, lse = torch.zeros(T, H, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H, device="cuda")
+    h.run_dense(q.cuda(), kn.cuda(), kr.cuda(), v.cuda(), out, lse, workspace=ws)
+    assert h.check_device_error(ws) == 0
+    for s in range(len(nq)):
+        a, b, x, y = int(cu_q[s]), int(cu_q[s + 1]), int(cu_k[s]), int(cu_k[s + 1])
+        k = torch.cat([kn[x:y], kr[x:y, None].expand(-1, H, -1)], -1)
+        check(out[a:b], lse[a:b], by_query(q[a:b], k, v[x:y], b - a, y - x, c["causal"], c["window_left"]), name)
+
+
+def test_expanded_keys_that_are_not_seen():
+    """NaN and infinite keys behind a query leave it alone; the queries that see them are NaN."""
+    L, H = 200, 2
+    q, kn, kr, v = randn(1, L, H, 192), randn(2, L, H, 128), randn(3, L, 64), randn(4, L, H, 128)
+    kn[150, 1], kr[180] = NAN, NAN
+    h = B.LatentHandle(num_heads=H, page_size=64, max_batch=1, max_total_tokens=L, max_num_pages=1, num_cache_pages=1)
+    ws = torch.empty(h.workspace_size(B.MODE_DENSE), dtype=torch.uint8, device="cuda")
+    h.plan_dense([0, L], [0, L], workspace=ws, sm_scale=SCALE)
+    out, lse = torch.zeros(L, H, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(L, H, device="cuda")
+    h.run_dense(q.cuda(), kn.cuda(), kr.cuda(), v.cuda(), out, lse, workspace=ws)
+    k = torch.cat([kn, kr[:, None].expand(-1, H, -1)], -1)
+    check(out, lse, by_query(q, k, v, L, L, True, -1), "keys")
+    assert torch.isfinite(out[:180, 0]).all() and torch.isfinite(out[:150, 1]).all()
+
+
 @pytest.mark.parametrize("value", [NAN, INF])
 def test_absorbed_result_is_that_of_finite_keys(value):
     """The tokens that do not see the bad one: within rounding of the same step without it, and the same
