@@ -53,6 +53,9 @@ struct WtSmem {
     static constexpr uint32_t BYTES = COL_OFF + kWeightTeams * 2 * 128 * 4;
 };
 static_assert(1024 + WtSmem<256>::BYTES <= 227 * 1024, "the weights kernel fits shared memory");
+// A team's wait for its next block tells the two phases of that block's buffer apart because its last block
+// used another of the four buffers, less than a turn before.
+static_assert(kWeightTeams < 4, "a team's step is shorter than the ring of score buffers");
 
 struct WeightsArgs {
     const WeightsItem *items;
