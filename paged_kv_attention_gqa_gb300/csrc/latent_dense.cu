@@ -441,8 +441,10 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                     bool rows = false;
                     if (mixed(j)) {
                         const int s = j % L::STAGES;
-                        if (!mbar_wait(&checked[3 * x + s], (j / L::STAGES) & 1, err, kErrWaitFull) ||
-                            !mbar_wait(&v_full[s], (j / L::STAGES) & 1, err, kErrWaitFull)) {  // (has: it was looked over)
+                        // the tile first: it lands once the stage's last one has been looked over, so that
+                        // the wait for the look is never two phases early
+                        if (!mbar_wait(&v_full[s], (j / L::STAGES) & 1, err, kErrWaitFull) ||
+                            !mbar_wait(&checked[3 * x + s], (j / L::STAGES) & 1, err, kErrWaitFull)) {
                             ok = false;
                             break;
                         }

@@ -300,9 +300,12 @@ class Expanded(Model):
             yield self.delay(50, 900)
             rescale = self.rng.random() < 0.2 and j > 0
             if self.partial[x][j]:
-                if self.plant != "no wait for the look":
-                    yield ("wait", self.checked[x][j % 3], j // 3)
-                yield ("wait", self.v_full[j % 3], j // 3)
+                waits = [("wait", self.v_full[j % 3], j // 3), ("wait", self.checked[x][j % 3], j // 3)]
+                if self.plant == "the look before the tile":
+                    waits.reverse()
+                if self.plant == "no wait for the look":
+                    waits.pop()
+                yield from waits
                 assert self.flag[x][j % 3] == (j, self.bad[x][j]), "the flag of another tile"
                 rescale = rescale or (self.bad[x][j] and j > 0)
             if rescale:
@@ -434,7 +437,8 @@ def test_expanded_protocol_is_sound():
         Expanded(seed).run()
 
 
-@pytest.mark.parametrize("plant", ["one P barrier", "no wait for the tail", "S over P", "not counted", "no wait for the look"])
+@pytest.mark.parametrize("plant", ["one P barrier", "no wait for the tail", "S over P", "not counted", "no wait for the look",
+                                   "the look before the tile"])
 def test_expanded_model_catches(plant):
     assert caught(lambda seed: Expanded(seed, plant)) > 0
 
