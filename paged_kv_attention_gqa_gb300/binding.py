@@ -187,6 +187,13 @@ def _check_tensor(name, t, dtype, shape, device, contiguous=True):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace(ws, device):
+    """Pointer of the workspace of a call whose kernels run on `device`."""
+    if ws.get_device() != device:
+        raise ValueError(f"workspace must be on the current CUDA device, is on {ws.device}")
+    return ws.data_ptr()
+
+
 def _stride(t, dim, least):
     """Stride of one dimension in elements; of a dimension of one entry, which is never stepped, the least."""
     return t.stride(dim) if t.shape[dim] > 1 else least
@@ -304,14 +311,14 @@ class Handle:
         _check_tensor("out", out, torch.bfloat16, q.shape, device)
         self._check(self.lib.pkv_run_decode_weights(
             self.h, q.data_ptr(), kv_layer.data_ptr(), out.data_ptr(), lse.data_ptr(), scores.data_ptr(), decay,
-            workspace.data_ptr(), _raw_stream(device) if stream is None else _stream(stream)))
+            _workspace(workspace, device), _raw_stream(device) if stream is None else _stream(stream)))
 
     def run_weights(self, q, lse, kv_layer, scores, *, decay=1.0, workspace, stream=None):
         """The same scores from the queries and the lse of a prefill (MODE_WEIGHTS plans)."""
         torch, device = self._check_layer(kv_layer, scores)
         self._check_q(q, lse, torch, device)
         self._check(self.lib.pkv_run_weights(
-            self.h, q.data_ptr(), lse.data_ptr(), kv_layer.data_ptr(), scores.data_ptr(), decay, workspace.data_ptr(),
+            self.h, q.data_ptr(), lse.data_ptr(), kv_layer.data_ptr(), scores.data_ptr(), decay, _workspace(workspace, device),
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def plan_evict(self, kv_indptr, kv_indices, last_page_len, keep, dst_indptr, dst_indices, *, num_sink=0,
@@ -337,7 +344,7 @@ class Handle:
         torch, device = self._check_layer(kv_layer, scores)
         _check_tensor("kept", kept, torch.int32, (self._kept,), device)
         self._check(self.lib.pkv_run_evict(
-            self.h, kv_layer.data_ptr(), scores.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
+            self.h, kv_layer.data_ptr(), scores.data_ptr(), kept.data_ptr(), _workspace(workspace, device),
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def gather_kv(self, kv_layer, pages, num_tokens, k_out, v_out, stream=None):
@@ -443,7 +450,7 @@ class LatentHandle:
         r, rs = self._rows("rope_new", rope_new, self.ROPE, torch, device)
         _check_tensor("cache_layer", cache_layer, torch.bfloat16, self._cache_shape, device)
         self._check(self.lib.pkv_latent_append_planned(
-            self.h, c, cs, r, rs, cache_layer.data_ptr(), workspace.data_ptr(),
+            self.h, c, cs, r, rs, cache_layer.data_ptr(), _workspace(workspace, device),
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def _check_out(self, out, lse, width, torch, device):
@@ -460,7 +467,7 @@ class LatentHandle:
         _check_tensor("cache_layer", cache_layer, torch.bfloat16, self._cache_shape, device)
         self._check_out(out, lse, self.LATENT, torch, device)
         self._check(self.lib.pkv_latent_run(
-            self.h, q.data_ptr(), cache_layer.data_ptr(), out.data_ptr(), _dptr(lse), workspace.data_ptr(),
+            self.h, q.data_ptr(), cache_layer.data_ptr(), out.data_ptr(), _dptr(lse), _workspace(workspace, device),
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def plan_dense(self, cu_q, cu_k, *, workspace, sm_scale, causal=True, window_left=-1, stream=None):
@@ -485,7 +492,7 @@ class LatentHandle:
         self._check(self.lib.pkv_latent_run_dense(
             self.h, q.data_ptr(), k_nope.data_ptr(), _stride(k_nope, 0, self.NOPE), _stride(k_nope, 1, self.NOPE),
             k_rope.data_ptr(), _stride(k_rope, 0, self.ROPE), v.data_ptr(), _stride(v, 0, self.V), _stride(v, 1, self.V),
-            out.data_ptr(), _dptr(lse), workspace.data_ptr(),
+            out.data_ptr(), _dptr(lse), _workspace(workspace, device),
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def check_device_error(self, workspace, stream=None) -> int:
