@@ -536,8 +536,14 @@ __global__ void __launch_bounds__(kLtThreads, 1)
             l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
             if (!mbar_wait(pv_done, (it - 1) & 1, err, kErrWaitFull)) break;
             tc_fence_after();
-            // a piece may hold no visible key of a row (causal, several tokens): weight 0, lse -inf
-            const float inv_a = l_a == 0.f ? 0.f : 1.f / l_a, inv_b = l_b == 0.f ? 0.f : 1.f / l_b;
+            // a piece may hold no visible key of a row (causal, several tokens): weight 0, lse -inf.  Keys whose
+            // scores are all -inf weigh nothing against other pieces, but 0 * inf of their values stays; a
+            // row that has no others is NaN (0 / 0).
+            const int first_key = t.tile0 * kLatentKeys, last_key = first_key + t.ntiles * kLatentKeys - 1;
+            auto inverse = [&](float l, int lo, int hi) {
+                return max(lo, first_key) > min(hi, last_key) ? 0.f : l == 0.f && t.partial >= 0 ? 1.f : 1.f / l;
+            };
+            const float inv_a = inverse(l_a, lo_a, hi_a), inv_b = inverse(l_b, lo_b, hi_b);
             const float lse_a = l_a == 0.f ? -INFINITY : m_a + log2f(l_a);
             const float lse_b = l_b == 0.f ? -INFINITY : m_b + log2f(l_b);
             const size_t g_a = (size_t)t.q_row + row_a, g_b = (size_t)t.q_row + row_b;

@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             }
             if (ok && mbar_wait(&pv_done[2 * x + ((ntx - 1) & 1)], ((ntx - 1) >> 1) & 1, err, kErrWaitFull)) {
                 tc_fence_after();
-                const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+                const float inv = 1.f / l_run;  // every query sees a key; one whose scores are all -inf is NaN (0 / 0)
                 const size_t row = (size_t)(t.q_begin + tok) * a.num_heads + t.kv_head;
                 __nv_bfloat16 *orow = a.out + row * kLatentV;
 #pragma unroll 1

@@ -80,6 +80,9 @@ ABSORBED = {
     "one CTA": dict(lens=[200, 130, 64], news=[3, 2, 2], H=20, P=64, sm_count=1, bad={1: INF}),
     "two CTAs, both ends": dict(lens=[700, 260], news=[6, 70], H=16, P=32, sm_count=2, window_left=100, bad={1: NAN, 104: INF, 60: NAN},
                                 columns=[2, 300]),
+    # scores of -inf: rows that see nothing else, and pieces of a row that hold nothing else
+    "an infinite key alone": dict(lens=[1, 70], news=[1, 1], H=64, P=16, window_left=0, bad={1: INF}, columns=[9]),
+    "an infinite key alone in its piece": dict(lens=[65, 129], news=[1, 3], H=16, P=16, bad={1: INF}, columns=[9]),
 }
 
 
@@ -178,6 +181,23 @@ def test_expanded_keys_that_are_not_seen():
     k = torch.cat([kn, kr[:, None].expand(-1, H, -1)], -1)
     check(out, lse, by_query(q, k, v, L, L, True, -1), "keys")
     assert torch.isfinite(out[:180, 0]).all() and torch.isfinite(out[:150, 1]).all()
+
+
+def test_expanded_scores_of_minus_infinity():
+    """A query whose keys all score -inf is NaN, one that sees others is not."""
+    L, H = 70, 1
+    q, kn, kr, v = randn(1, L, H, 192), randn(2, L, H, 128), randn(3, L, 64), randn(4, L, H, 128)
+    q[..., 5] = 1.0
+    kn[0, :, 5], kn[20, :, 5] = -INF, -INF
+    h = B.LatentHandle(num_heads=H, page_size=64, max_batch=1, max_total_tokens=L, max_num_pages=1, num_cache_pages=1)
+    ws = torch.empty(h.workspace_size(B.MODE_DENSE), dtype=torch.uint8, device="cuda")
+    for window in (-1, 0):
+        h.plan_dense([0, L], [0, L], workspace=ws, sm_scale=SCALE, window_left=window)
+        out, lse = torch.zeros(L, H, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(L, H, device="cuda")
+        h.run_dense(q.cuda(), kn.cuda(), kr.cuda(), v.cuda(), out, lse, workspace=ws)
+        k = torch.cat([kn, kr[:, None]], -1)
+        check(out, lse, by_query(q, k, v, L, L, True, window), f"window {window}")
+        assert torch.isnan(out[[0] if window else [0, 20]]).all() and lse[0, 0] == -INF
 
 
 @pytest.mark.parametrize("value", [NAN, INF])
