@@ -1,5 +1,6 @@
 #pragma once
-// Batched paged decode with split-KV, the split-KV merge, and the last-page append.
+// The decode kernel: batched paged decode with split-KV (the merge of its partials and the last-page
+// append are in decode.cu; decode_weights.cu instantiates it with stored logits).
 //
 // Decode (FlashInferDecodeWrapper.run; mstar.engine.resources.attn.wrappers): every row
 // has one query token; q head h attends, through kv head h / g, to the row's visible

@@ -5,8 +5,8 @@
 // and 10 bits from the top: up to three histograms, fewer once a bin is taken whole), then the tokens
 // above it and, from the lowest position up, as many equal to it as are still wanted are written out in
 // position order.  Each thread owns a run of consecutive tokens, so that one scan over the threads
-// orders the output.  A CTA takes a row of up to 8,192 tokens, a cluster of up to eight CTAs a longer
-// one (histograms and counts joined through distributed shared memory); the scores are read once,
+// orders the output.  Every row of a plan gets the CTAs that its longest cut row needs at 8,192 tokens
+// each, one or a cluster of up to eight (histograms and counts joined through distributed shared memory); the scores are read once,
 // through the page list, into shared memory.  Counters are integers, so the result does not depend on
 // the order of the atomics.  Latency-bound: a row of 16,000 tokens is 64 KB.
 //

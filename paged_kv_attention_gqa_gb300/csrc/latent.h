@@ -82,11 +82,12 @@ int make_latent_dense_plan(const LatentShape &s, const int32_t *cu_q, const int3
 size_t latent_workspace_bound(const LatentShape &s, bool dense);
 
 // Launchers.  `tm_cache`: boxes of (64 columns, box_rows() rows, box_chunks() chunks) of the layer slice
-// viewed as [9 chunks][pages * page_size][64] (chunks outermost, so that one chunk's rows land together); `tm_q`: boxes of (64 columns, box_q rows) of q viewed as [T * H][576].
+// viewed as [9 chunks][pages * page_size][64] (chunks outermost, so that one chunk's rows land together);
+// `tm_q`: boxes of (64 columns, box_q rows) of q viewed as [T * H][576].
 cudaError_t launch_latent(const LatentShape &s, const LatentPlan &p, const CUtensorMap &tm_cache,
                           const CUtensorMap &tm_q, void *ws, void *out, float *lse, cudaStream_t st);
-// Expanded form: boxes of 64 columns x 128 rows of q [H][T][192], k_nope [H][keys][128], k_rope
-// [keys][64] and v [H][keys][128].
+// Expanded form: boxes of 64 columns x 128 rows of q [H][T][192], and of 64 columns x 64 rows of
+// k_nope [H][keys][128], k_rope [keys][64] and v [H][keys][128].
 cudaError_t launch_latent_dense(const LatentShape &s, const LatentPlan &p, const CUtensorMap &tm_q,
                                 const CUtensorMap &tm_k, const CUtensorMap &tm_r, const CUtensorMap &tm_v, void *ws,
                                 void *out, float *lse, cudaStream_t st);

@@ -15,16 +15,18 @@
 //  * warps 13 and 14 look over the value tiles that some queries of Q0 or Q1 see and others do not
 //    (causal diagonal, window edges) as they land: the weight of a value that a query does not see is 0,
 //    but 0 * NaN would reach it.  A tile that holds NaN or infinities there is left to the softmax
-//    warps, each query adding the values it sees.  (In the PV warps, between two tiles, the look cost 14 us of
-//    the 234 below; in warps of its own 2 %.)
+//    warps, each query adding the values it sees.  (In the PV warps, between two tiles, the look cost 14 us; in
+//    warps of its own 6.)
 // Tensor memory: two S buffers of 64 columns and an O of 128 for each query tile, all 512 columns.
 // Tiles of 128 keys leave room for one S each; then a query tile's S, softmax and PV wait for one
 // another, two chains of 4,600 cycles per 128 keys against 2,560 of MMAs: 305 us (32 heads, prompts of
-// 801 to 4,093 tokens, 9,788 in all, causal).  N = 64 costs 48 cycles a k-step of S (the A operand's
+// 801 to 4,093 tokens, 9,788 in all, causal) when this kernel had one issuing warp a query tile and waits that
+// looped from the start; that form has not been timed with what came later.  N = 64 costs 48 cycles a k-step of S (the A operand's
 // reads) in place of 32, 3,328 cycles per 128 keys.  A warp's MMA takes it 33 cycles to issue, a commit
 // or a wait, even for a completed phase, 100 to 200; so S and PV of both query tiles have a warp each:
-// 234 us, the operations at the measured rate being 160.  (One warp for S and PV of a query tile: 265
-// us, one for both query tiles: 412 us; PV as two N = 64 halves: + 10 us.)
+// 241 us in short runs of calls and 251 in long ones (234 and 245 without the look at the values), the
+// operations at the measured rate being 160.  (One warp for S and PV of a query tile: 265 us, one for both
+// query tiles: 412 us; PV as two N = 64 halves: + 10 us; all in short runs, without the look.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

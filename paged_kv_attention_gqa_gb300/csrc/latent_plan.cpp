@@ -55,8 +55,9 @@ static void split_units(const LatentShape &s, const std::vector<std::vector<Unit
     const long long cmax = std::max(1, s.sm_count);
     const bool flat = (long long)lanes.size() * 2 > cmax;  // more blocks than CTAs to give them: one lane
     auto cut = [&](const std::vector<const Unit *> &us, long long total, long long ctas) {
-        // the least budget per CTA with which the run takes no more than `ctas` of them.  A CTA that has
-        // a piece takes no other one that its budget leaves no tile for
+        // a budget per CTA with which the run takes no more than `ctas` of them, found by growing the even
+        // share step by step (by a quarter of what is missing: near the least one, not always at it).  A CTA
+        // that has a piece takes no other one that its budget leaves no tile for
         auto count = [&](long long per) {
             long long n = 1, budget = per;
             for (const Unit *u : us)

@@ -68,6 +68,10 @@ struct PpSmem {
 // address here is below 256 KB).
 __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t off_bytes) { return d + (off_bytes >> 4); }
 
+// The form of the barrier waits (mbar_wait says what each measured).
+template <int D>
+constexpr bool kWaitFirst = D != 64;
+
 template <int D, int G>
 __global__ void __launch_bounds__(kPpThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_v,
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
             const int s = i % NS;
             const uint32_t use = i / NS;
             // the MMAs that read this stage use-1 rounds ago must have completed
-            if (use > 0 && !mbar_wait(&kv_empty[s], (use - 1) & 1, err, kErrWaitEmpty)) break;
+            if (use > 0 && !mbar_wait<kWaitFirst<D>>(&kv_empty[s], (use - 1) & 1, err, kErrWaitEmpty)) break;
             if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], L::KV_TILE);
             __syncwarp();
             uint8_t *dst = sm + L::RING_OFF + s * L::KV_TILE;
@@ -229,14 +233,14 @@ __global__ void __launch_bounds__(kPpThreads, 1)
         const uint32_t Sx = S_col(x), Ox = O_col(x);
         const int tail_begin = t.length;
         const int tail_end = (t.length + P - 1) & ~(P - 1);
-        bool ok = mbar_wait(&q_full[x], 0, err, kErrWaitFull);
+        bool ok = mbar_wait<kWaitFirst<D>>(&q_full[x], 0, err, kErrWaitFull);
         uint32_t i = 0;  // ring slot sequence, as the producer counts it
-        if (ok && nt > 0) ok = mbar_wait(&kv_full[0], 0, err, kErrWaitFull);
+        if (ok && nt > 0) ok = mbar_wait<kWaitFirst<D>>(&kv_full[0], 0, err, kErrWaitFull);
         for (int j = 0; j < nt && ok; ++j, i += 2) {
             const int sk = i % NS, sv = (i + 1) % NS;
             // S_X(j) overwrites P_X(j-1), which PV_X(j-1) reads: wait until it completed (PV_X(j)
             // cannot complete before this warp issues it, so the parity is exact)
-            if (j > 0) ok = mbar_wait(&pv_done[x], (j - 1) & 1, err, kErrWaitFull);
+            if (j > 0) ok = mbar_wait<kWaitFirst<D>>(&pv_done[x], (j - 1) & 1, err, kErrWaitFull);
             if (!ok) break;
             tc_fence_after();
             {
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 mma_commit_elect(&s_full[x]);
                 mma_commit_elect(&kv_empty[sk]);  // K_j's stage frees once both tiles' S MMAs completed
             }
-            ok = mbar_wait(&kv_full[sv], ((i + 1) / NS) & 1, err, kErrWaitFull);
+            ok = mbar_wait<kWaitFirst<D>>(&kv_full[sv], ((i + 1) / NS) & 1, err, kErrWaitFull);
             if (!ok) break;
             // V rows of the row's last page past its end (poisoned or stale slots: their P is 0,
             // but 0 * NaN would poison O) are zeroed by warp 9; warp 10 waits for that on the
@@ -269,14 +273,14 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                     __syncwarp();
                     if (lane == 0 && two) mbar_arrive(v_tail);
                 } else {
-                    ok = mbar_wait(v_tail, 0, err, kErrWaitFull);
+                    ok = mbar_wait<kWaitFirst<D>>(v_tail, 0, err, kErrWaitFull);
                     if (!ok) break;
                 }
             }
             // K_{j+1} is awaited here, while the softmax still runs, so that after PV_X(j) only
             // its own completion stands between it and S_X(j+1)
-            if (j + 1 < nt) ok = mbar_wait(&kv_full[(i + 2) % NS], ((i + 2) / NS) & 1, err, kErrWaitFull);
-            if (ok) ok = mbar_wait(&p_full[x], j & 1, err, kErrWaitFull);
+            if (j + 1 < nt) ok = mbar_wait<kWaitFirst<D>>(&kv_full[(i + 2) % NS], ((i + 2) / NS) & 1, err, kErrWaitFull);
+            if (ok) ok = mbar_wait<kWaitFirst<D>>(&p_full[x], j & 1, err, kErrWaitFull);
             if (!ok) break;
             tc_fence_after();
             {
@@ -312,12 +316,12 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 const int key0 = (kt0 + j) * kPpKeys;
                 // take turns with the other group: group 1 starts tile j after group 0 finished
                 // it, group 0 starts tile j + 1 after group 1 finished tile j
-                if (two && (x == 1 || j > 0) && !mbar_wait(&turn[x], (x ? j : j - 1) & 1, err, kErrWaitFull)) {
+                if (two && (x == 1 || j > 0) && !mbar_wait<kWaitFirst<D>>(&turn[x], (x ? j : j - 1) & 1, err, kErrWaitFull)) {
                     ok = false;
                     break;
                 }
                 // S_X(j+1) needs P_X(j) (through PV_X(j)), so this phase is the next one
-                if (!mbar_wait(&s_full[x], j & 1, err, kErrWaitFull)) {
+                if (!mbar_wait<kWaitFirst<D>>(&s_full[x], j & 1, err, kErrWaitFull)) {
                     ok = false;
                     break;
                 }
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (warp_grow) {
                     // O holds P_0..P_{j-1} V: wait for the last of those MMAs, then scale O rows
                     // (PV_X(j) waits for this group's p_full, so nothing else touches O now)
-                    if (!mbar_wait(&pv_done[x], (j - 1) & 1, err, kErrWaitFull)) {
+                    if (!mbar_wait<kWaitFirst<D>>(&pv_done[x], (j - 1) & 1, err, kErrWaitFull)) {
                         ok = false;
                         break;
                     }
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(kPpThreads, 1)
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
             // epilogue
-            if (ok && mbar_wait(&o_final[x], 0, err, kErrWaitFull)) {
+            if (ok && mbar_wait<kWaitFirst<D>>(&o_final[x], 0, err, kErrWaitFull)) {
                 tc_fence_after();
                 const bool none = l_run == 0.f;  // no visible key (empty context): o = 0, lse = -inf
                 const float inv = none ? 0.f : 1.f / l_run;
