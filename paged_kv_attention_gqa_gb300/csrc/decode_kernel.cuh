@@ -191,7 +191,7 @@ __global__ void __launch_bounds__((D > 128 ? 4 + (SMALL ? 2 : 1) : 8 + (SMALL ? 
                 }
                 // every lane waits on the barrier itself (they wake together); the vote keeps
                 // the warp on one path if a wait gives up
-                const bool w = use == 0 || mbar_wait(&empty[s], (use - 1) & 1, err, kErrWaitEmpty);
+                const bool w = use == 0 || mbar_wait<kWaitFirst<D>>(&empty[s], (use - 1) & 1, err, kErrWaitEmpty);
                 if (!__all_sync(0xffffffffu, w)) {
                     ok = false;
                     break;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__((D > 128 ? 4 + (SMALL ? 2 : 1) : 8 + (SMALL ? 
             const uint32_t issued = it;
             for (uint32_t d = issued > (uint32_t)a.stages ? issued - a.stages : 0; d < issued; ++d) {
                 const int s = d % a.stages;
-                if (!mbar_wait(&empty[s], (d / a.stages) & 1, err, kErrWaitDrain)) break;
+                if (!mbar_wait<kWaitFirst<D>>(&empty[s], (d / a.stages) & 1, err, kErrWaitDrain)) break;
             }
         }
         return;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__((D > 128 ? 4 + (SMALL ? 2 : 1) : 8 + (SMALL ? 
                         if (it < (uint32_t)nhead) continue;  // issued above
                         const int s = it % a.stages;
                         const uint32_t use = it / a.stages;
-                        if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, err, kErrWaitEmpty)) {
+                        if (use > 0 && !mbar_wait<kWaitFirst<D>>(&empty[s], (use - 1) & 1, err, kErrWaitEmpty)) {
                             ok = false;
                             break;
                         }
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__((D > 128 ? 4 + (SMALL ? 2 : 1) : 8 + (SMALL ? 
                     for (int k = cr.k0; k < cr.nk; ++k, ++it) {
                         const int s = it % a.stages;
                         const uint32_t use = it / a.stages;
-                        if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, err, kErrWaitEmpty)) {
+                        if (use > 0 && !mbar_wait<kWaitFirst<D>>(&empty[s], (use - 1) & 1, err, kErrWaitEmpty)) {
                             ok = false;
                             break;
                         }
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__((D > 128 ? 4 + (SMALL ? 2 : 1) : 8 + (SMALL ? 
             const uint32_t issued = it;
             for (uint32_t d = issued > (uint32_t)a.stages ? issued - a.stages : 0; d < issued; ++d) {
                 const int s = d % a.stages;
-                if (!mbar_wait(&empty[s], (d / a.stages) & 1, err, kErrWaitDrain)) break;
+                if (!mbar_wait<kWaitFirst<D>>(&empty[s], (d / a.stages) & 1, err, kErrWaitDrain)) break;
             }
         }
         return;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__((D > 128 ? 4 + (SMALL ? 2 : 1) : 8 + (SMALL ? 
             const int s = it % a.stages;
             // a wait that gives up clears ok; the warp still walks its tiles so that the
             // consumer warps keep meeting at their named barriers (no time limit there)
-            ok = ok && mbar_wait(&full[s], (it / a.stages) & 1, err, kErrWaitFull);
+            ok = ok && mbar_wait<kWaitFirst<D>>(&full[s], (it / a.stages) & 1, err, kErrWaitFull);
             uint8_t *st = smem + (size_t)s * a.stage_bytes;
             const uint32_t sbase = smem_u32(st);
             const int pos0 = cr.base + k * kDecodeKeysPerStage;

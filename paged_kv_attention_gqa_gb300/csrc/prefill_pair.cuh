@@ -68,10 +68,6 @@ struct PpSmem {
 // address here is below 256 KB).
 __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t off_bytes) { return d + (off_bytes >> 4); }
 
-// The form of the barrier waits (mbar_wait says what each measured).
-template <int D>
-constexpr bool kWaitFirst = D != 64;
-
 template <int D, int G>
 __global__ void __launch_bounds__(kPpThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_v,

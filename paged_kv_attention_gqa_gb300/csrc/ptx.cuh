@@ -49,9 +49,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 
 // Wait for the phase with `parity` to complete.  Returns false (after recording `code`
 // in *err) if it does not complete within `limit` polls.  FIRST: one poll stands before the loop, so that a
-// phase that is complete costs no loop (the expanded latent kernel 327 -> 281 us with it, prefill of head_dim
-// 128 1,214 -> 1,278 TFLOP/s, of 256 1,108 -> 1,239; of 64, where waits are seldom for complete phases,
-// 668 -> 659).
+// phase that is complete costs no loop.
 template <bool FIRST = true>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *err, int code,
                                           uint32_t limit = kWaitLimit) {
@@ -67,6 +65,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *e
     if (err) atomicCAS(err, 0, code);
     return false;
 }
+
+// The form of the waits of the decode and the two-query-tile prefill kernel, by head_dim.  With the poll
+// before the loop: prefill of head_dim 128 1,214 -> 1,278 TFLOP/s, decode of 8/1/128 4,366 -> 4,487 GB/s and of
+// 32/8/128 6,648 -> 6,665; of head_dim 64, prefill 668 -> 659 and decode of 32/8/64 6,138 -> 6,086.  (The
+// head_dim-256 prefill gained 1,108 -> 1,239, the expanded latent kernel 327 -> 281 us.)
+template <int D>
+constexpr bool kWaitFirst = D != 64;
 
 // Barrier `id` (1..15) over `count` threads of the CTA (a multiple of 32): the warps that
 // execute it with this id.
