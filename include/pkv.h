@@ -28,6 +28,9 @@
  * lo = max(0, p - window_left) if window_left >= 0, else 0 (FlashInferPrefillWrapper.plan:
  * window_left is the number of preceding positions a query sees, -1 unbounded);
  *   out = softmax(sm_scale * q K^T) V (bf16), lse = natural-log log-sum-exp (fp32).
+ * Slots that hold no token of the rows may hold anything.  A row's own tokens that a query does not
+ * see (later ones, ones before its window) must hold finite V in the calls of a pkv_handle_t: their
+ * weight is 0, and 0 * NaN is NaN (the latent calls have no such condition).
  *
  * Call order for one step:  pkv_plan (host)  ->  per layer: pkv_kv_append (or
  * pkv_kv_append_planned), then pkv_run_decode / pkv_run_prefill / pkv_run_mixed.  One

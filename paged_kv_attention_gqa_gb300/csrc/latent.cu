@@ -16,8 +16,8 @@
 //    the lower ones, and S (two buffers of 64 columns) the upper ones.  An M = 64 MMA takes as long as
 //    M = 128, and 32 cycles at least (measured at N = 64 and at N = 32: a tile of 32 keys costs as much
 //    S time as one of 64): 2,183 cycles a tile, below the 3,190 in which an SM's share of HBM delivers it.
-//  * Shared memory: Q 72 KB, two tiles of 72 KB (a tile serves as keys and, its first 512 columns, as
-//    values), P 8 KB.  A step is bounded by the time a tile's buffer waits for its copy, S, the softmax
+//  * Shared memory: Q 72 KB (64 rows, whatever the unit has), two tiles of 72 KB (a tile serves as keys
+//    and, its first 512 columns, as values), P 8 KB.  A step is bounded by the time a tile's buffer waits for its copy, S, the softmax
 //    and PV (two of them: half that time a tile; bringing later tiles into L2 ahead shortened the copies
 //    and lengthened the start by as much).  Pages of 64 slots and more are copied with one TMA
 //    instruction a tile; smaller ones with one per page and 64 columns, spread over four warps, because
