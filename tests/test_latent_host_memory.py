@@ -1,5 +1,6 @@
 """A plan whose host buffers cannot be had says so (no GPU): run in a process of its own, whose memory is
 limited before the call."""
+import os
 import subprocess
 import sys
 
@@ -27,7 +28,8 @@ print(st, h.lib.pkv_latent_last_error(h.h).decode())
 
 def test_a_plan_that_runs_out_of_memory_says_so():
     pkv_build.build()
-    out = subprocess.run([sys.executable, "-c", CODE], capture_output=True, text=True, timeout=120)
+    out = subprocess.run([sys.executable, "-c", CODE], capture_output=True, text=True, timeout=120,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert out.returncode == 0, out.stderr
     status, text = out.stdout.strip().split(" ", 1)
     assert int(status) == 1 and "bad_alloc" in text, out.stdout
