@@ -69,11 +69,11 @@ typedef enum {
     PKV_ERR_TOO_MANY_PREFILL_ROWS = 4, /* mixed plan with more prompt rows than max_prefill_rows */
     PKV_ERR_NOT_PLANNED = 5,           /* run/append without a matching plan on that workspace */
     PKV_ERR_CUDA = 6,                  /* a CUDA runtime/driver call failed */
-    PKV_ERR_DEVICE = 7                 /* a kernel recorded a device-side error (wait limit hit) */
+    PKV_ERR_DEVICE = 7                 /* a kernel recorded a device-side error (wait limit hit; bad device arrays) */
 } pkv_status;
 
 enum { PKV_MODE_DECODE = 0, PKV_MODE_PREFILL = 1, PKV_MODE_MIXED = 2, PKV_MODE_DENSE = 3,
-       PKV_MODE_EVICT = 4, PKV_MODE_DECODE_WEIGHTS = 5, PKV_MODE_WEIGHTS = 6 };
+       PKV_MODE_EVICT = 4, PKV_MODE_DECODE_WEIGHTS = 5, PKV_MODE_WEIGHTS = 6, PKV_MODE_TREE = 8 };
 enum { PKV_NON_CAUSAL = 0, PKV_CAUSAL = 1, PKV_CONTEXT_ONLY = 2 };
 
 /*
@@ -373,6 +373,93 @@ pkv_status pkv_plan_evict(pkv_handle_t h, const int32_t *paged_kv_indptr, const 
  */
 pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t *kept, void *workspace,
                          pkv_stream_t stream);
+
+/* ---- the speculative step ---- */
+
+/*
+ * Several drafted tokens per row are verified in one pass.  How many of them hold is known on the GPU
+ * alone, so the step's index arrays are DEVICE arrays and no call waits for the device or reads them on
+ * the host: pkv_build_maps (pages, page lists, slots), pkv_plan_tree, pkv_run_tree for every layer,
+ * pkv_run_accept, and the next step's pkv_build_maps from the new lengths.  All four may be captured into one
+ * CUDA graph (after one uncaptured call of each), which then serves every step whose sizes stay within
+ * the captured ones.  Arrays that the kernels find inconsistent are skipped and reported:
+ * pkv_build_maps by its status, the others by pkv_check_device_error, code 5 (a row's index arrays do
+ * not agree: the row counts as empty), 6 (a page id outside the cache: read as zeros, not written) or
+ * 7 (a parent that does not stand before its child: taken as -1).
+ */
+
+/*
+ * Page and slot maps of a step.  Row r holds seq_lens[r] tokens in num_blocks[r] pages, block_table[r *
+ * table_stride + b] for b < num_blocks[r] <= max_blocks, and new_lens[r] new tokens come.  Afterwards it has the
+ * ceil((seq_lens[r] + new_lens[r]) / page_size) pages that these need, no more and no less.
+ * free_pages[0 .. *free_count) is a stack of free page ids.  First the pages that rows have too many are pushed
+ * onto it, rows and blocks ascending; then rows, ascending, pop their missing pages, the topmost going to
+ * the row's first missing block.  (A row that has ended has length 0 and no new tokens: all its pages go back.)
+ * Outputs: block_table (the new blocks' entries; others are left as they are), num_blocks_out[batch],
+ * *free_count_out, qo_indptr[batch + 1], kv_indptr[batch + 1], kv_indices (the rows' pages one after
+ * another; entries behind them are left), last_page_len[batch] (0 for a row without pages), and, where
+ * not NULL, slots[token_capacity] (page * page_size + offset of every new token in the cache's slots, -1
+ * behind the last) and positions[token_capacity] (0 behind the last).  num_blocks_out and free_count_out may be
+ * num_blocks and free_count themselves; no other array may overlap another.
+ * *status: 0, or nothing has changed and the step is empty (qo_indptr, kv_indptr and last_page_len all 0, slots
+ * -1): > 0 pages are missing, -1 a negative length or a row that needs or holds more than max_blocks
+ * pages, -2 more new tokens than token_capacity or pages than indices_capacity, -3 a free count outside
+ * its array, or a stack that the pages given back do not fit.
+ * The handle gives page_size and max_batch; no plan or workspace is involved.  At most 8,192 rows.
+ */
+pkv_status pkv_build_maps(pkv_handle_t h, const int32_t *seq_lens, const int32_t *new_lens, int batch,
+                          int32_t *block_table, int64_t table_stride, int max_blocks, const int32_t *num_blocks,
+                          int32_t *num_blocks_out, int32_t *free_pages, int free_capacity, const int32_t *free_count,
+                          int32_t *free_count_out, int32_t *qo_indptr, int32_t *kv_indptr, int32_t *kv_indices,
+                          int indices_capacity, int32_t *last_page_len, int32_t *slots, int32_t *positions,
+                          int token_capacity, int32_t *status, pkv_stream_t stream);
+
+/*
+ * Plan a step of drafted tokens.  qo_indptr, paged_kv_indptr, paged_kv_indices (num_indices entries) and
+ * paged_kv_last_page_len describe the rows with their drafted tokens in place, as for pkv_plan: row r has L_r tokens,
+ * of which the last n_r are drafted and C_r = L_r - n_r are cached.  The drafted tokens' slots hold
+ * anything: they are not read.  parents[t] is the parent of token t, as an index within its row that is
+ * smaller than its own, or -1; NULL makes every row a chain.  num_tokens: tokens of q, k_new, v_new and
+ * out (qo_indptr[batch] may be smaller, the tokens behind it are left alone); max_new: most drafted
+ * tokens of a row (1 to 256).  positions (DEVICE, num_tokens entries, or NULL) receives C_r + depth of
+ * each token.  paged_kv_indices is read by the step's later calls too and must stay as it is until they
+ * have run.  page_size 8 or more (else PKV_ERR_UNSUPPORTED).  sm_scale 0 selects 1/sqrt(head_dim).
+ * Makes the handle's current plan, as pkv_plan does, by kernels alone: the call can be captured.
+ */
+pkv_status pkv_plan_tree(pkv_handle_t h, const int32_t *qo_indptr, const int32_t *paged_kv_indptr,
+                         const int32_t *paged_kv_indices, int num_indices, const int32_t *paged_kv_last_page_len, int batch,
+                         const int32_t *parents, int num_tokens, int max_new, int window_left, float sm_scale,
+                         int32_t *positions, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+/*
+ * Attention of the planned tokens in one layer: token i of row r sees the row's cached tokens, its ancestors
+ * and itself; under a window those at most window_left positions above its own, C_r + its depth.
+ * q [num_tokens, Hq, D], k_new and v_new [num_tokens, Hkv, D]: device bf16, tokens *_stride elements apart
+ * (multiples of 8, at least a token's width), 16-byte aligned.  out [num_tokens, Hq, D] bf16, lse
+ * [num_tokens, Hq] fp32 or NULL.  The cache is only read.  Keys and values that a token does not see never
+ * reach it, NaN and infinities in them included.
+ */
+pkv_status pkv_run_tree(pkv_handle_t h, const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
+                        const void *v_new, int64_t v_stride, const void *kv_layer, void *out, float *lse, void *workspace,
+                        pkv_stream_t stream);
+/*
+ * Accept the drafted tokens that the model confirms.  A row's first drafted token is its root, the token
+ * chosen last, and always holds; from a token that holds, the first child j (in index order) holds
+ * whose draft_tokens[j] equals target_tokens of its parent, the model's choice behind that.  (Other tokens
+ * without a parent never hold.)  draft_tokens, target_tokens [num_tokens] and next_tokens [batch]: device
+ * integers of token_bytes (4 or 8).
+ * accepted [num_tokens] receives every row's path from its root, as indices within the row, from
+ * qo_indptr[r] on, -1 behind it (tokens of no row are left); num_accepted[batch] its length; next_tokens the target
+ * of its last token (-1 for a row without tokens); seq_lens[batch] (or NULL) C_r + the length (left for
+ * a row without tokens).  The path's keys and values are copied to the row's slots C_r, C_r + 1, ... of each
+ * of num_layers layers: k_new and v_new with layer and token strides in elements, kv_cache [num_layers][num_cache_pages,
+ * 2, page_size, Hkv, D], cache_layer_stride elements apart; strides are multiples of 8, pointers 16-byte
+ * aligned.  Nothing else in the cache is touched.  No page of a drafted slot may belong to two rows.
+ */
+pkv_status pkv_run_accept(pkv_handle_t h, const void *draft_tokens, const void *target_tokens, int token_bytes,
+                          const void *k_new, int64_t k_layer_stride, int64_t k_token_stride, const void *v_new,
+                          int64_t v_layer_stride, int64_t v_token_stride, void *kv_cache, int64_t cache_layer_stride,
+                          int num_layers, int32_t *accepted, int32_t *num_accepted, void *next_tokens, int32_t *seq_lens,
+                          void *workspace, pkv_stream_t stream);
 
 /* ---- latent attention ---- */
 

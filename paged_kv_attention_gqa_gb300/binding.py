@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_PKG, "libpkv.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_TOO_MANY_PREFILL_ROWS, ERR_NOT_PLANNED, ERR_CUDA, ERR_DEVICE = range(8)
 MODE_DECODE, MODE_PREFILL, MODE_MIXED, MODE_DENSE = 0, 1, 2, 3
-MODE_EVICT, MODE_DECODE_WEIGHTS, MODE_WEIGHTS = 4, 5, 6
+MODE_EVICT, MODE_DECODE_WEIGHTS, MODE_WEIGHTS, MODE_TREE = 4, 5, 6, 8
 NON_CAUSAL, CAUSAL, CONTEXT_ONLY = 0, 1, 2
 STATUS_NAMES = ["OK", "INVALID", "UNSUPPORTED", "WORKSPACE", "TOO_MANY_PREFILL_ROWS", "NOT_PLANNED", "CUDA", "DEVICE"]
 
@@ -26,7 +26,8 @@ EXPORTS = ["pkv_create", "pkv_destroy", "pkv_last_error", "pkv_workspace_size", 
            "pkv_run_decode", "pkv_run_prefill", "pkv_run_mixed", "pkv_check_device_error", "pkv_append_slots",
            "pkv_mixed_layout", "pkv_decode_split", "pkv_decode_head_rows", "pkv_run_decode_static", "pkv_context_only_views",
            "pkv_plan_dense", "pkv_run_dense", "pkv_gather_kv", "pkv_run_decode_append", "pkv_selftest_wait_timeout",
-           "pkv_run_decode_weights", "pkv_run_weights", "pkv_plan_evict", "pkv_run_evict", "pkv_latent_create", "pkv_latent_destroy", "pkv_latent_last_error", "pkv_latent_workspace_size",
+           "pkv_run_decode_weights", "pkv_run_weights", "pkv_plan_evict", "pkv_run_evict",
+           "pkv_build_maps", "pkv_plan_tree", "pkv_run_tree", "pkv_run_accept", "pkv_latent_create", "pkv_latent_destroy", "pkv_latent_last_error", "pkv_latent_workspace_size",
            "pkv_latent_plan", "pkv_latent_append_planned", "pkv_latent_run", "pkv_latent_plan_dense",
            "pkv_latent_run_dense", "pkv_latent_check_device_error"]
 
@@ -90,6 +91,10 @@ def load(path: str = LIB_PATH):
         "pkv_run_weights": ([vp, vp, vp, vp, vp, ctypes.c_float, vp, vp], i),
         "pkv_plan_evict": ([vp, i32p, i32p, i32p, i, i32p, i, i, i32p, i32p, vp, ctypes.c_size_t, vp], i),
         "pkv_run_evict": ([vp, vp, vp, vp, vp, vp], i),
+        "pkv_build_maps": ([vp, vp, vp, i, vp, i64, i, vp, vp, vp, i, vp, vp, vp, vp, vp, i, vp, vp, vp, i, vp, vp], i),
+        "pkv_plan_tree": ([vp, vp, vp, vp, i, vp, i, vp, i, i, i, ctypes.c_float, vp, vp, ctypes.c_size_t, vp], i),
+        "pkv_run_tree": ([vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp], i),
+        "pkv_run_accept": ([vp, vp, vp, i, vp, i64, i64, vp, i64, i64, vp, i64, i, vp, vp, vp, vp, vp, vp], i),
         "pkv_latent_create": ([ctypes.POINTER(LatentConfig), ctypes.POINTER(vp)], i),
         "pkv_latent_destroy": ([vp], None),
         "pkv_latent_last_error": ([vp], ctypes.c_char_p),
@@ -215,7 +220,8 @@ class Handle:
             raise PkvError(st, self.lib.pkv_last_error(None).decode())
         self.h = h
         self._keep = []
-        self._planned_tokens = self._kept = 0
+        self._planned_tokens = self._planned_rows = self._kept = 0
+        self._tree_pages = None
 
     def close(self):
         if getattr(self, "h", None):
@@ -345,6 +351,118 @@ class Handle:
         _check_tensor("kept", kept, torch.int32, (self._kept,), device)
         self._check(self.lib.pkv_run_evict(
             self.h, kv_layer.data_ptr(), scores.data_ptr(), kept.data_ptr(), _workspace(workspace, device),
+            _raw_stream(device) if stream is None else _stream(stream)))
+
+    # ---- the speculative step: its index arrays are device tensors (int32) ----
+
+    def build_maps(self, seq_lens, new_lens, block_table, num_blocks, free_pages, free_count, *, qo_indptr, kv_indptr,
+                   kv_indices, last_page_len, slots=None, positions=None, status, num_blocks_out=None,
+                   free_count_out=None, stream=None):
+        """Pages, page lists, slots and positions of a step from the rows' lengths; num_blocks and free_count are
+        updated in place unless the *_out tensors are given.  status[0]: 0, or why nothing was done."""
+        torch = _torch or _load_torch()
+        device, i32, batch = torch.cuda.current_device(), torch.int32, seq_lens.shape[0]
+        held_out = num_blocks if num_blocks_out is None else num_blocks_out
+        count_out = free_count if free_count_out is None else free_count_out
+        if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("block_table must be [batch, blocks] with unit stride in its last dimension")
+        width = block_table.shape[1]
+        if slots is not None and positions is not None and slots.shape != positions.shape:
+            raise ValueError("slots and positions must have the same length")
+        tokens = 0 if slots is None and positions is None else (slots if slots is not None else positions).shape[0]
+        for name, t, shape in (
+                ("seq_lens", seq_lens, (batch,)), ("new_lens", new_lens, (batch,)), ("num_blocks", num_blocks, (batch,)),
+                ("num_blocks_out", held_out, (batch,)), ("free_pages", free_pages, (free_pages.numel(),)),
+                ("free_count", free_count, (1,)), ("free_count_out", count_out, (1,)), ("qo_indptr", qo_indptr, (batch + 1,)),
+                ("kv_indptr", kv_indptr, (batch + 1,)), ("kv_indices", kv_indices, (kv_indices.numel(),)),
+                ("last_page_len", last_page_len, (batch,)), ("status", status, (1,))):
+            _check_tensor(name, t, i32, shape, device)
+        _check_tensor("block_table", block_table, i32, (batch, width), device, contiguous=False)
+        for name, t in (("slots", slots), ("positions", positions)):
+            if t is not None:
+                _check_tensor(name, t, i32, (tokens,), device)
+        if slots is None and positions is None:
+            tokens = 2 ** 31 - 1  # nothing is listed by token
+        self._check(self.lib.pkv_build_maps(
+            self.h, seq_lens.data_ptr(), new_lens.data_ptr(), batch, block_table.data_ptr(), _stride(block_table, 0, width),
+            width, num_blocks.data_ptr(), held_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+            free_count.data_ptr(), count_out.data_ptr(), qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
+            kv_indices.numel(), last_page_len.data_ptr(), _dptr(slots), _dptr(positions), tokens, status.data_ptr(),
+            _raw_stream(device) if stream is None else _stream(stream)))
+
+    def plan_tree(self, qo_indptr, kv_indptr, kv_indices, last_page_len, parents=None, *, num_tokens, max_new,
+                  positions=None, workspace, window_left=-1, sm_scale=0.0, stream=None):
+        """Plan a step of drafted tokens from device index arrays; parents None: every row is a chain."""
+        torch = _torch or _load_torch()
+        device, i32, batch = torch.cuda.current_device(), torch.int32, kv_indptr.shape[0] - 1
+        for name, t, shape in (("qo_indptr", qo_indptr, (batch + 1,)), ("kv_indptr", kv_indptr, (batch + 1,)),
+                               ("kv_indices", kv_indices, (kv_indices.numel(),)), ("last_page_len", last_page_len, (batch,)),
+                               ("parents", parents, (num_tokens,)), ("positions", positions, (num_tokens,))):
+            if t is not None:
+                _check_tensor(name, t, i32, shape, device)
+        self._check(self.lib.pkv_plan_tree(
+            self.h, qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(),
+            last_page_len.data_ptr(), batch, _dptr(parents), int(num_tokens), int(max_new), int(window_left), float(sm_scale),
+            _dptr(positions), _workspace(workspace, device), workspace.numel() * workspace.element_size(),
+            _raw_stream(device) if stream is None else _stream(stream)))
+        self._planned_tokens, self._planned_rows = int(num_tokens), batch
+        self._tree_pages = kv_indices  # the step's later calls read it
+
+    def _new_kv(self, name, t, lead, torch, device):
+        """A tensor of new keys or values [*lead, tokens, kv heads, head_dim] with strides of its own before the heads."""
+        c = self.cfg
+        _check_tensor(name, t, torch.bfloat16, (*lead, self._planned_tokens, c.num_kv_heads, c.head_dim), device, contiguous=False)
+        if t.stride(-1) != 1 or (c.num_kv_heads > 1 and t.stride(-2) != c.head_dim):
+            raise ValueError(f"{name} must have its heads side by side")
+        return t.data_ptr(), _stride(t, len(lead), c.num_kv_heads * c.head_dim)
+
+    def run_tree(self, q, k_new, v_new, kv_layer, out, lse=None, *, workspace, stream=None):
+        """Attention of the planned drafted tokens over the row's cached tokens, their ancestors and
+        themselves: q [T, Hq, D], k_new and v_new [T, Hkv, D] (token strides free), out [T, Hq, D]."""
+        torch, c = _torch or _load_torch(), self.cfg
+        device, tokens = torch.cuda.current_device(), self._planned_tokens
+        k, ks = self._new_kv("k_new", k_new, (), torch, device)
+        v, vs = self._new_kv("v_new", v_new, (), torch, device)
+        _check_tensor("q", q, torch.bfloat16, (tokens, c.num_qo_heads, c.head_dim), device, contiguous=False)
+        if q.stride(2) != 1 or (c.num_qo_heads > 1 and q.stride(1) != c.head_dim):
+            raise ValueError("q must have its heads side by side")
+        _check_tensor("kv_layer", kv_layer, torch.bfloat16,
+                      (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim), device)
+        _check_tensor("out", out, torch.bfloat16, (tokens, c.num_qo_heads, c.head_dim), device)
+        if lse is not None:
+            _check_tensor("lse", lse, torch.float32, (tokens, c.num_qo_heads), device)
+        self._check(self.lib.pkv_run_tree(
+            self.h, q.data_ptr(), _stride(q, 0, c.num_qo_heads * c.head_dim), k, ks, v, vs, kv_layer.data_ptr(),
+            out.data_ptr(), _dptr(lse), _workspace(workspace, device),
+            _raw_stream(device) if stream is None else _stream(stream)))
+
+    def run_accept(self, draft_tokens, target_tokens, k_new, v_new, kv_cache, accepted, num_accepted, next_tokens,
+                   seq_lens=None, *, workspace, stream=None):
+        """The path of every row's drafted tokens that target_tokens confirm, and its keys and values into the
+        row's next slots of every layer: k_new and v_new [layers, T, Hkv, D] (layer and token strides free),
+        kv_cache [layers, pages, 2, page_size, Hkv, D] (layers may be strided)."""
+        torch, c = _torch or _load_torch(), self.cfg
+        device, tokens, batch = torch.cuda.current_device(), self._planned_tokens, self._planned_rows
+        kind, layers = draft_tokens.dtype, kv_cache.shape[0]
+        if kind not in (torch.int32, torch.int64):
+            raise TypeError(f"draft_tokens must be int32 or int64, got {kind}")
+        for name, t, dtype, shape in (
+                ("draft_tokens", draft_tokens, kind, (tokens,)), ("target_tokens", target_tokens, kind, (tokens,)),
+                ("accepted", accepted, torch.int32, (tokens,)), ("num_accepted", num_accepted, torch.int32, (batch,)),
+                ("next_tokens", next_tokens, kind, (batch,)), ("seq_lens", seq_lens, torch.int32, (batch,))):
+            if t is not None or name != "seq_lens":
+                _check_tensor(name, t, dtype, shape, device)
+        k, ks = self._new_kv("k_new", k_new, (layers,), torch, device)
+        v, vs = self._new_kv("v_new", v_new, (layers,), torch, device)
+        layer = (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim)
+        _check_tensor("kv_cache", kv_cache, torch.bfloat16, (layers, *layer), device, contiguous=False)
+        if layers and not kv_cache[0].is_contiguous():
+            raise ValueError("kv_cache must have contiguous layers")
+        width, each = c.num_kv_heads * c.head_dim, c.num_kv_heads * c.head_dim * 2 * c.page_size * c.num_cache_pages
+        self._check(self.lib.pkv_run_accept(
+            self.h, draft_tokens.data_ptr(), target_tokens.data_ptr(), kind.itemsize, k, _stride(k_new, 0, width), ks, v,
+            _stride(v_new, 0, width), vs, kv_cache.data_ptr(), _stride(kv_cache, 0, each), layers, accepted.data_ptr(),
+            num_accepted.data_ptr(), next_tokens.data_ptr(), _dptr(seq_lens), _workspace(workspace, device),
             _raw_stream(device) if stream is None else _stream(stream)))
 
     def gather_kv(self, kv_layer, pages, num_tokens, k_out, v_out, stream=None):

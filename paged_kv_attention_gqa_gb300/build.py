@@ -14,8 +14,9 @@ ROOT = os.path.dirname(PKG)
 OUT = os.path.join(PKG, "libpkv.so")
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["pkv_api.cu", "decode.cu", "prefill.cu", "prefill_gather.cu", "prefill_pair.cu", "prefill_wide.cu",
-           "decode_weights.cu", "weights.cu", "evict.cu", "latent.cu", "latent_dense.cu", "latent_api.cu", "planner.cpp", "latent_plan.cpp", "evict_plan.cpp"]
-HEADERS = ["plan.h", "launch.h", "handle.h", "latent.h", "evict.h", "decode_kernel.cuh", "ptx.cuh", "tcgen05.cuh", "prefill_kernel.cuh", "prefill_pair.cuh",
+           "decode_weights.cu", "weights.cu", "evict.cu", "latent.cu", "latent_dense.cu", "latent_api.cu", "tree.cu", "tree_plan.cu", "tree_api.cu", "maps.cu",
+           "planner.cpp", "latent_plan.cpp", "evict_plan.cpp"]
+HEADERS = ["plan.h", "launch.h", "handle.h", "latent.h", "evict.h", "tree.h", "decode_kernel.cuh", "ptx.cuh", "tcgen05.cuh", "prefill_kernel.cuh", "prefill_pair.cuh",
            "prefill_wide.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -12,6 +12,7 @@
 #include "../../include/pkv.h"
 #include "evict.h"
 #include "plan.h"
+#include "tree.h"
 
 // Page-locked staging ring (PinnedIndexRing: depth 2; a set is rewritten only after
 // the copy out of it has completed, fenced by an event recorded after that copy).
@@ -35,6 +36,7 @@ struct pkv_handle_s {
     std::vector<uint8_t> spare_image;
     pkv::WeightsPlan weights;  // the score arrays of DECODE_WEIGHTS / WEIGHTS plans
     pkv::EvictPlan evict;      // EVICT plans
+    pkv::TreePlan tree;        // TREE plans
     void *planned_ws = nullptr;
     PkvStaging staging;
     // side stream + fork/join events of the mixed step's concurrent passes

@@ -89,7 +89,14 @@ extern "C" const char *pkv_last_error(pkv_handle_t h) { return h ? h->err.c_str(
 
 extern "C" pkv_status pkv_workspace_size(pkv_handle_t h, int mode, size_t *bytes) {
     if (!h || !bytes) return fail(h, PKV_ERR_INVALID, "null argument");
-    if (mode < PKV_MODE_DECODE || mode > PKV_MODE_WEIGHTS) return fail(h, PKV_ERR_INVALID, "unknown mode");
+    if (mode != PKV_MODE_TREE && (mode < PKV_MODE_DECODE || mode > PKV_MODE_WEIGHTS))
+        return fail(h, PKV_ERR_INVALID, "unknown mode");
+    if (mode == PKV_MODE_TREE) {
+        pkv::TreePlan p;
+        pkv::tree_layout(h->shape, h->shape.max_batch, h->shape.max_total_tokens, pkv::kTreeMaxNew, p);
+        *bytes = p.total;
+        return PKV_OK;
+    }
     *bytes = mode >= PKV_MODE_EVICT ? pkv::evict_workspace_bound(h->shape, mode) : pkv::workspace_bound(h->shape, mode);
     return PKV_OK;
 }
@@ -434,7 +441,12 @@ extern "C" pkv_status pkv_check_device_error(pkv_handle_t h, void *workspace, pk
         e = cudaMemcpyAsync(static_cast<uint8_t *>(workspace) + h->plan.lay.err, &zero, sizeof(int),
                             cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-        return fail(h, PKV_ERR_DEVICE, "a kernel gave up waiting (device error " + std::to_string(v) + ")");
+        const std::string code_text = " (device error " + std::to_string(v) + ")";
+        if (v == pkv::kErrTreeRow) return fail(h, PKV_ERR_DEVICE, "a row's index arrays do not agree" + code_text);
+        if (v == pkv::kErrTreePage) return fail(h, PKV_ERR_DEVICE, "a page id is outside the cache" + code_text);
+        if (v == pkv::kErrTreeParent)
+            return fail(h, PKV_ERR_DEVICE, "a drafted token's parent does not stand before it" + code_text);
+        return fail(h, PKV_ERR_DEVICE, "a kernel gave up waiting" + code_text);
     }
     return PKV_OK;
 }

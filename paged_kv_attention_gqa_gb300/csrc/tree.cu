@@ -1,0 +1,758 @@
+// Attention of a tree of drafted tokens over a paged cache (pkv_run_tree), and the join of its cut units.
+//
+// Row r has C cached tokens and n drafted ones; node i's parent stands before it.  Node i sees the cached
+// keys and those of its ancestors and itself (under a window, those at most window_left positions above
+// its own, C + depth):
+//     s_ij = sm_scale <q_i, k_j>,  p_i = softmax_j(s_i),  o_i = sum_j p_ij v_j.
+// The drafted tokens' K and V come from the step's own tensors; the cache is only read.  n * g rows (g query
+// heads a kv head) share a head's keys: 4 D n g operations on 4 D bytes a key.  The tensor cores and HBM
+// balance near n g = 280; below it the cached K and V, read once, are the floor.
+//
+// Work: a unit is one query tile of up to 128 rows (row m = token * g + head), or two (PAIR) that share every
+// K and V tile, over the 64-key tiles of its row: those of the cached keys, then those of the drafted
+// ones, which so begin at a tile's first key.  A persistent CTA per SM takes an equal run of tiles, cut
+// by the plan; a unit that several CTAs share leaves normalised partials, joined by a second kernel.
+//  * warps 0-3 and 4-7 are two softmax groups (thread = query row = tensor-memory lane).  With PAIR
+//    group x has query tile x; else the groups take the pieces in turn, and one's epilogue runs under
+//    the other's tiles.  Each has two S buffers of 64 columns, so that S of the next tile runs under the
+//    softmax, and an accumulator (one for both groups at head_dim 256).
+//  * warp 8 copies Q of each piece (two buffers where they fit) and the K tiles, warp 11 the V tiles, into
+//    one ring of 16 KB stages (8 at head_dim 64, 32 at 256): one lane a box of a page and 64 columns.
+//  * warp 9 issues S = Q K^T, warp 10 O += P V (P from tensor memory, over its S).
+//  * A key that a row does not see has weight 0, but 0 * NaN would reach O.  Those that no row sees are
+//    zeroed in shared memory by warp 10; a tile with keys that some rows see and others do not is
+//    looked over by it, and if it holds NaN or infinities each row adds the keys it sees alone.
+//  * The running maximum moves (and O is rescaled) only when it grows by more than 2^8.  Maxima and
+//    sums are 32-bit; P is rounded to bf16 for the MMA (relative 2^-8 a weight at most), the sum adds it unrounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "tcgen05.cuh"
+#include "tree.h"
+
+namespace pkv {
+namespace dev {
+
+constexpr int kTrThreads = 384;
+constexpr float kTrRescale = 8.f;  // log2
+constexpr float kTrLn2 = 0.6931471805599453f;
+
+template <int D>
+struct TrSmem {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t Q_BYTES = 2 * 128u * 128u * (D > 128 ? 2 : HALVES);  // both buffers (at 256: one of 128 rows or two of 64)
+    static constexpr uint32_t STAGE = kTreeKeys * D * 2u;
+    static constexpr int NS = D == 64 ? 20 : D == 128 ? 10 : 4;  // even: a stage holds K tiles or V tiles
+    static_assert(NS % 2 == 0, "each stage has one producer and one reader");
+    static constexpr uint32_t HALF = STAGE / HALVES;
+    static constexpr uint32_t RING_OFF = Q_BYTES;
+    static constexpr uint32_t BAR_OFF = RING_OFF + NS * STAGE;
+    static constexpr uint32_t BYTES = BAR_OFF + 1024;
+};
+static_assert(1024 + TrSmem<64>::BYTES <= 227 * 1024 && 1024 + TrSmem<128>::BYTES <= 227 * 1024 &&
+                  1024 + TrSmem<256>::BYTES <= 227 * 1024,
+              "the tree kernel fits shared memory");
+static_assert(1024 + TrSmem<64>::BYTES > 228 * 1024 / 2, "one CTA an SM: each takes all tensor-memory columns");
+
+struct TreeArgs {
+    __nv_bfloat16 *out;
+    float *lse;
+    const TreeRow *rows;
+    const TreeStart *starts;
+    const TreeNode *nodes;
+    const unsigned long long *masks;
+    const int32_t *pages;
+    float *part_o;    // [slot][part_rows][D], normalised
+    float *part_lse;  // [slot][part_rows], base 2
+    TreeHeader *hdr;
+    float scale_log2;
+    int window_left, words, num_qo_heads, num_kv_heads, group, page_size, page_shift, num_cache_pages;
+    int tile_tokens;  // query tokens of a 128-row tile
+    int box_rows, box_new, box_q;
+    int q_rows;       // rows of a Q buffer: 128, or 64 at head_dim 256 where two then fit
+    int oob_row;      // a row past the cache: TMA fills zeros
+};
+
+// A piece: tiles [tile, tile + cnt) of a unit.
+struct TreePiece {
+    TreeRow row;
+    int kvh, qt, tile, cnt;
+    int partial;  // slot, -1 = the whole unit
+    int index;    // of the CTA
+};
+
+template <typename F>
+__device__ __forceinline__ void tree_pieces(const TreeArgs &a, const TreeStart &s, F &&piece) {
+    TreePiece p;
+    p.row = s.row;
+    p.index = 0;
+    int r = s.r, unit = s.unit, tile = s.tile, left = s.left;
+    const bool cut = tile > 0;
+    while (left > 0) {
+        const int units = p.row.nq * a.num_kv_heads;
+        if (unit >= units) {
+            p.row = a.rows[++r];
+            unit = 0;
+            continue;
+        }
+        p.kvh = unit / p.row.nq;
+        p.qt = unit % p.row.nq;
+        p.tile = tile;
+        p.cnt = min(left, p.row.nt - tile);
+        p.partial = p.index == 0 && cut ? 2 * (int)blockIdx.x : tile + p.cnt < p.row.nt ? 2 * (int)blockIdx.x + 1 : -1;
+        if (!piece(p)) return;
+        left -= p.cnt;
+        tile = 0;
+        ++unit;
+        ++p.index;
+    }
+}
+
+// The tile of keys `t` of a row: how many there are, and which the row's nodes do not all see.
+struct TreeTile {
+    bool drafted;
+    int key0;       // cached: position of the first key; drafted: its node
+    int keys;       // 1..64 (0: a window that begins behind the cached keys)
+    int first;      // keys below it are seen by no node
+    int mixed0, mixed1;  // keys in [mixed0, mixed1) are seen by some and may be not by others
+    bool special;   // keys to zero or to look at
+};
+__device__ __forceinline__ TreeTile tree_tile(const TreeRow &row, int t, int window_left) {
+    TreeTile k;
+    k.drafted = t >= row.nc;
+    k.key0 = (k.drafted ? t - row.nc : row.kt0 + t) * kTreeKeys;
+    k.keys = min(kTreeKeys, (k.drafted ? row.n : row.ctx) - k.key0);
+    k.first = k.mixed0 = k.mixed1 = 0;
+    if (k.drafted) {
+        k.mixed1 = row.n > 1 ? k.keys : 0;
+        k.special = true;
+        return k;
+    }
+    if (window_left >= 0) {
+        // a root's first key, and that of a node below n - 1 others
+        const int lo = max(0, row.ctx - window_left) - k.key0, hi = max(0, row.ctx + row.n - 1 - window_left) - k.key0;
+        k.first = max(0, min(lo, k.keys));
+        k.mixed0 = k.first;
+        k.mixed1 = max(k.first, min(hi, k.keys));
+    }
+    k.special = k.keys < kTreeKeys || k.first > 0 || k.mixed1 > k.mixed0;
+    return k;
+}
+
+// O += P V of one tile without the tensor cores: the row of this thread adds the keys in `vis` alone.
+template <int D>
+__device__ __noinline__ void tree_pv_rows(uint32_t o_addr, uint32_t p_addr, const uint8_t *tile, unsigned long long vis,
+                                          float alpha, bool first) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t r[32];
+        float o[32];
+        __syncwarp();
+        tmem_ld32(o_addr + c0, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = first ? 0.f : __uint_as_float(r[i]) * alpha;
+        const uint8_t *half = tile + (c0 >> 6) * TrSmem<D>::HALF;
+#pragma unroll 1
+        for (int k = 0; k < kTreeKeys; ++k) {
+            const uint32_t w = tmem_ld1(p_addr + (k >> 1));
+            tmem_wait_ld();
+            if ((vis >> k) & 1) {
+                const float p = __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(half + swz128(k, ((c0 & 32) >> 3) + c));
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[8 * c + 2 * i] = fmaf(p, __uint_as_float(u[i] << 16), o[8 * c + 2 * i]);
+                        o[8 * c + 2 * i + 1] = fmaf(p, __uint_as_float(u[i] & 0xffff0000u), o[8 * c + 2 * i + 1]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i]);
+        tmem_st32(o_addr + c0, r);
+    }
+    tmem_wait_st();
+}
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kTrThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q, const TreeArgs a) {
+    using L = TrSmem<D>;
+    constexpr int HALVES = L::HALVES, NS = L::NS;
+    constexpr bool ONE_O = D > 128;  // both groups' accumulators are the same columns
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR_OFF);
+    // Every waiter waits for the consecutive phases of a barrier, or for one that cannot be passed before the
+    // waiter has provided something; so none is ever two phases behind or ahead.
+    uint64_t *q_full = bars + 0;    // [2] Q buffer of a piece landed
+    uint64_t *q_empty = bars + 2;   // [2] its last S completed
+    uint64_t *s_full = bars + 4;    // [group][buffer]
+    uint64_t *p_full = bars + 8;    // [group][buffer] P written (and O rescaled if it had to be)
+    uint64_t *pv_done = bars + 12;  // [group][buffer] PV completed: the buffer may be overwritten
+    uint64_t *o_final = bars + 16;  // [group] the piece's last PV completed
+    uint64_t *o_free = bars + 18;   // [group] the piece's O has been read
+    uint64_t *checked = bars + 20;  // [group] a special tile's V has been looked over
+    uint64_t *kv_full = bars + 22;           // [NS]
+    uint64_t *kv_empty = bars + 22 + NS;     // [NS]
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 22 + 2 * NS);
+    uint32_t *by_rows = tmem_holder + 1;     // [group] that tile's PV goes by rows
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *const err = &a.hdr->err;
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&q_full[x], 1);
+            mbar_init(&q_empty[x], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&s_full[2 * x + b], 1);
+                mbar_init(&p_full[2 * x + b], 4);
+                mbar_init(&pv_done[2 * x + b], 1);
+            }
+            mbar_init(&o_final[x], 1);
+            mbar_init(&o_free[x], 4);
+            mbar_init(&checked[x], 1);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        fence_barrier_init();
+        prefetch_tmap(&tm_kv);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_q);
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();  // the plan, q, k, v and the cache may come from the previous kernels
+    griddep_launch();
+    const uint32_t tmem = *tmem_holder;
+    const TreeStart start = a.starts[blockIdx.x];
+    auto S_col = [tmem](int x, int b) { return tmem + 128u * (uint32_t)x + 64u * (uint32_t)b; };
+    auto O_col = [tmem](int x) { return tmem + 256u + (ONE_O ? 0u : (uint32_t)(D * x)); };
+    const int unit_tokens = a.tile_tokens * (PAIR ? 2 : 1);
+    const bool two_q = a.q_rows == 64 || D <= 128;  // Q buffers: one at head_dim 256 with 128 rows
+    const uint32_t q_half = (uint32_t)a.q_rows * 128u, q_buf = q_half * HALVES;
+    // PAIR: the unit's tokens reach into the second query tile
+    auto second = [&](const TreePiece &p) { return PAIR && p.row.n - p.qt * unit_tokens > a.tile_tokens; };
+    auto q_slot = [&](const TreePiece &p) { return PAIR || !two_q ? 0 : p.index & 1; };
+    auto q_phase = [&](const TreePiece &p) { return (uint32_t)(PAIR || !two_q ? p.index : p.index >> 1); };
+
+    if (warp == 8 || warp == 11) {
+        // ------------------------------------------------ copies: warp 8 Q and K, warp 11 V
+        const int kv = warp == 11;
+        const int P = a.page_size, R = a.box_rows, half = lane % HALVES, box = lane / HALVES;
+        const bool mine = box < kTreeKeys / R;
+        uint32_t i = kv;  // ring position: K of tile it at 2 it, V at 2 it + 1
+        bool ok = true;
+        tree_pieces(a, start, [&](const TreePiece &p) {
+            if (!kv) {
+                const int qs = q_slot(p);
+                const uint32_t ph = q_phase(p);
+                if (ph > 0) ok = mbar_wait(&q_empty[qs], (ph - 1) & 1, err, kErrWaitEmpty);
+                if (!__all_sync(0xffffffffu, ok)) return ok = false;
+                const int tiles = second(p) ? 2 : 1;
+                if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(tiles * HALVES * a.box_q * a.group) * 128u);
+                __syncwarp();
+                if (lane < tiles * HALVES)
+                    tma_load_3d(sm + (PAIR ? lane / HALVES : qs) * q_buf + lane % HALVES * q_half, &tm_q, &q_full[qs],
+                                lane % HALVES * 64, p.kvh * a.group,
+                                p.row.q_begin + p.qt * unit_tokens + lane / HALVES * a.tile_tokens);
+            }
+            // the cache row of this lane's box of cached tile t
+            auto box_row = [&](int t) {
+                const int kb = (p.row.kt0 + t) * kTreeKeys + box * R;
+                if (!mine || t >= p.row.nc || kb >= p.row.ctx) return a.oob_row;
+                const int page = a.pages[p.row.kv_base + (kb >> a.page_shift)];
+                if ((unsigned)page >= (unsigned)a.num_cache_pages) {
+                    atomicCAS(err, 0, kErrTreePage);
+                    return a.oob_row;
+                }
+                return page * 2 * P + (kb & (P - 1)) + kv * P;
+            };
+            int row = box_row(p.tile);
+            for (int j = 0; j < p.cnt; ++j, i += 2) {
+                const int s = i % NS, t = p.tile + j;
+                const uint32_t use = i / NS;
+                if (use > 0) ok = mbar_wait(&kv_empty[s], (use - 1) & 1, err, kErrWaitEmpty);
+                if (!__all_sync(0xffffffffu, ok)) return ok = false;
+                const bool drafted = t >= p.row.nc;
+                if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], drafted ? (uint32_t)(a.box_new * D * 2) : L::STAGE);
+                __syncwarp();
+                uint8_t *dst = sm + L::RING_OFF + s * L::STAGE + half * L::HALF;
+                if (drafted) {
+                    if (box == 0)
+                        tma_load_3d(dst, kv ? &tm_v : &tm_k, &kv_full[s], half * 64, p.row.q_begin + (t - p.row.nc) * kTreeKeys,
+                                    p.kvh);
+                } else if (mine) {
+                    tma_load_3d(dst + box * R * 128, &tm_kv, &kv_full[s], half * 64, row, p.kvh);
+                }
+                if (j + 1 < p.cnt) row = box_row(t + 1);  // lands while the next stage is awaited
+            }
+            return true;
+        });
+        // copies in flight land before the CTA may end (they have, unless a wait gave up)
+        if (!ok) {
+            for (uint32_t b = 0; b < 2 && !kv; ++b) mbar_wait(&q_full[b], 0, nullptr, 0, 1u << 12);
+            const uint32_t end = (i - kv) / 2;
+            for (uint32_t d = end > NS ? end - NS : 0; d < end; ++d) {
+                const uint32_t k = 2 * d + kv;
+                mbar_wait(&kv_full[k % NS], (k / NS) & 1, nullptr, 0, 1u << 12);
+            }
+            for (uint32_t d = 0; d < 1024; ++d) __nanosleep(1000);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------ S = Q K^T
+        constexpr uint32_t ID_S = idesc_bf16_f32(128, kTreeKeys, 0, 0);
+        auto add = [](uint64_t d, uint32_t off) { return d + (off >> 4); };
+        const uint64_t dQ = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+        const uint64_t dK = smem_desc(smem_u32(sm + L::RING_OFF), 16, 1024, kSwizzle128B);
+        uint32_t i = 0, done[2] = {0, 0};  // tiles of each group
+        bool ok = true;
+        tree_pieces(a, start, [&](const TreePiece &p) {
+            const int qs = q_slot(p), x0 = PAIR ? 0 : p.index & 1, x1 = PAIR ? (second(p) ? 2 : 1) : x0 + 1;
+            ok = mbar_wait(&q_full[qs], q_phase(p) & 1, err, kErrWaitFull);
+            for (int j = 0; j < p.cnt && ok; ++j, i += 2) {
+                const int s = i % NS;
+                ok = mbar_wait(&kv_full[s], (i / NS) & 1, err, kErrWaitFull);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x < x0 || x >= x1 || !ok) continue;
+                    const uint32_t it = done[x], b = it & 1;
+                    // S overwrites P of two tiles before, which that tile's PV reads
+                    if (it >= 2) ok = mbar_wait(&pv_done[2 * x + b], ((it >> 1) - 1) & 1, err, kErrWaitFull);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    const uint64_t q = add(dQ, (PAIR ? x : qs) * q_buf), k = add(dK, s * L::STAGE);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss_elect(S_col(x, b), add(q, (kk / 4) * q_half + (kk % 4) * 32),
+                                     add(k, (kk / 4) * L::HALF + (kk % 4) * 32), ID_S, kk > 0 ? 1u : 0u);
+                    mma_commit_elect(&s_full[2 * x + b]);
+                    ++done[x];
+                }
+                if (ok) mma_commit_elect(&kv_empty[s]);
+            }
+            if (ok) mma_commit_elect(&q_empty[qs]);
+            return ok;
+        });
+        if (!ok)  // a wait gave up: let the MMAs in flight finish before the tensor memory is released
+            for (uint32_t d = 0; d < 1024; ++d) __nanosleep(1000);
+    } else if (warp == 10) {
+        // ------------------------------------------------ O += P V
+        constexpr uint32_t ID_O = idesc_bf16_f32(128, D, 0, 1);
+        auto add = [](uint64_t d, uint32_t off) { return d + (off >> 4); };
+        const uint64_t dV = smem_desc(smem_u32(sm + L::RING_OFF), L::HALF, 1024, kSwizzle128B);
+        uint32_t i = 1, done[2] = {0, 0}, pieces[2] = {0, 0};
+        bool ok = true;
+        tree_pieces(a, start, [&](const TreePiece &p) {
+            const int x0 = PAIR ? 0 : p.index & 1, x1 = PAIR ? (second(p) ? 2 : 1) : x0 + 1;
+            // O may be overwritten once what it held has been read
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (x < x0 || x >= x1 || !ok) continue;
+                const int y = ONE_O ? 1 - x : x;
+                if (pieces[y] > 0) ok = mbar_wait(&o_free[y], (pieces[y] - 1) & 1, err, kErrWaitEmpty);
+            }
+            for (int j = 0; j < p.cnt && ok; ++j, i += 2) {
+                const int s = i % NS;
+                const TreeTile k = tree_tile(p.row, p.tile + j, a.window_left);
+                ok = mbar_wait(&kv_full[s], (i / NS) & 1, err, kErrWaitFull);
+                if (!ok) break;
+                uint8_t *const tile = sm + L::RING_OFF + s * L::STAGE;
+                const int steps = (k.keys + 15) / 16;  // k-steps of 16 keys
+                bool rows = false;
+                if (k.special) {
+                    // keys that no row sees: their P is 0, but 0 * NaN would reach O
+                    const int n_zero = k.first + steps * 16 - k.keys;
+                    for (int e = lane; e < n_zero * (D / 8); e += 32) {
+                        const int n = e / (D / 8), c = e % (D / 8), key = n < k.first ? n : k.keys + n - k.first;
+                        *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::HALF + swz128(key, c & 7)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    uint32_t f0 = 0, f1 = 0;
+                    const int n = (k.mixed1 - k.mixed0) * (D / 8);
+                    for (int e0 = lane; e0 < n; e0 += 4 * 32) {  // four vectors in flight
+                        uint4 v[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int e = min(e0 + 32 * u, n - 1), c = e % (D / 8);
+                            v[u] = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * L::HALF +
+                                                                    swz128(k.mixed0 + e / (D / 8), c & 7));
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            f0 = keep_nonfinite(v[u].x, keep_nonfinite(v[u].y, f0));
+                            f1 = keep_nonfinite(v[u].z, keep_nonfinite(v[u].w, f1));
+                        }
+                    }
+                    rows = __any_sync(0xffffffffu, has_nan(f0) || has_nan(f1));
+                    if (lane == 0)
+                        for (int x = x0; x < x1; ++x) {
+                            by_rows[x] = rows;
+                            mbar_arrive(&checked[x]);
+                        }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x < x0 || x >= x1 || !ok) continue;
+                    const uint32_t it = done[x], b = it & 1;
+                    ok = mbar_wait(&p_full[2 * x + b], (it >> 1) & 1, err, kErrWaitFull);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    if (!rows) {
+                        const uint64_t v = add(dV, s * L::STAGE);
+                        if (steps == kTreeKeys / 16) {
+#pragma unroll
+                            for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                        } else {
+                            for (int kk = 0; kk < steps; ++kk)
+                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    mma_commit_elect(&pv_done[2 * x + b]);
+                    if (j == p.cnt - 1) {
+                        mma_commit_elect(&o_final[x]);
+                        ++pieces[x];
+                    }
+                    ++done[x];
+                }
+                if (ok) mma_commit_elect(&kv_empty[s]);
+            }
+            return ok;
+        });
+        if (!ok)
+            for (uint32_t d = 0; d < 1024; ++d) __nanosleep(1000);
+    } else {
+        // ------------------------------------------------ softmax and epilogue: warps 0-7
+        const int x = warp >> 2, m = (warp & 3) * 32 + lane;  // group; query row = lane of tensor memory
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const float sl = a.scale_log2;
+        const uint32_t O = O_col(x) + lane_off;
+        const int tok_in_tile = m / a.group, head = m % a.group;
+        uint32_t it = 0, pieces = 0, checks = 0, before = 0;  // before: tiles of the CTA's earlier pieces, both groups'
+        bool ok = true;
+        tree_pieces(a, start, [&](const TreePiece &p) {
+            const uint32_t tiles0 = before;
+            before += p.cnt;
+            if (PAIR ? (x == 1 && !second(p)) : (p.index & 1) != x) return true;
+            const int tok = p.qt * unit_tokens + (PAIR ? x * a.tile_tokens : 0) + tok_in_tile;
+            const bool live = tok_in_tile < a.tile_tokens && tok < p.row.n;
+            const bool idle = !__any_sync(0xffffffffu, live);  // the warp has no row of this unit
+            const size_t node = (size_t)p.row.q_begin + tok;
+            int lo = 0;  // first cached key that the row sees
+            if (live && a.window_left >= 0) lo = max(0, p.row.ctx + a.nodes[node].depth - a.window_left);
+            float m_run = -INFINITY, l_run = 0.f;
+            bool seen = false;
+            for (int j = 0; j < p.cnt; ++j, ++it) {
+                const uint32_t b = it & 1, S = S_col(x, b) + lane_off;
+                const TreeTile k = tree_tile(p.row, p.tile + j, a.window_left);
+                unsigned long long vis = ~0ull;
+                if (k.drafted) {
+                    if (live) vis = a.masks[node * a.words + (k.key0 >> 6)];
+                } else if (k.special) {
+                    const int begin = min(max(lo - k.key0, 0), 64);
+                    vis = begin < 64 ? ~0ull << begin : 0ull;
+                    if (k.keys < 64) vis &= (1ull << max(k.keys, 0)) - 1;
+                }
+                if (!mbar_wait(&s_full[2 * x + b], (it >> 1) & 1, err, kErrWaitFull)) return ok = false;
+                if (idle) {  // P's rows of this warp stay as they are: O's are never read
+                    if (k.special && !mbar_wait(&checked[x], checks++ & 1, err, kErrWaitFull)) return ok = false;
+                    if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t r0[32], r1[32];
+                tmem_ld32(S, r0);
+                tmem_ld32(S + 32, r1);
+                tmem_wait_ld();
+                float sv[kTreeKeys];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    sv[c] = __uint_as_float(r0[c]);
+                    sv[32 + c] = __uint_as_float(r1[c]);
+                }
+                if (k.special) {
+                    const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        sv[c] = (v0 >> c) & 1u ? sv[c] : -INFINITY;
+                        sv[32 + c] = (v1 >> c) & 1u ? sv[32 + c] : -INFINITY;
+                    }
+                }
+                seen |= vis != 0;
+                float mx;
+                {
+                    float a0 = sv[0], a1 = sv[1], a2 = sv[2], a3 = sv[3];
+#pragma unroll
+                    for (int c = 4; c < 60; c += 8) {
+                        a0 = max3f(a0, sv[c], sv[c + 1]);
+                        a1 = max3f(a1, sv[c + 2], sv[c + 3]);
+                        a2 = max3f(a2, sv[c + 4], sv[c + 5]);
+                        a3 = max3f(a3, sv[c + 6], sv[c + 7]);
+                    }
+                    a0 = max3f(a0, sv[60], sv[61]);
+                    a1 = max3f(a1, sv[62], sv[63]);
+                    mx = max3f(fmaxf(a0, a1), a2, a3);
+                }
+                const float m_tile = live ? mx * sl : -INFINITY;
+                const bool grow = m_tile > m_run + kTrRescale;
+                const bool warp_grow = __any_sync(0xffffffffu, grow);
+                float alpha = 1.f;
+                if (grow) {
+                    alpha = ex2_ftz(m_run - m_tile);  // 0 when m_run = -inf
+                    m_run = m_tile;
+                }
+                const float mref = m_run == -INFINITY ? 0.f : m_run;
+                // p = 2^(s * sl - mref), two columns per packed FMA; sums in four packed chains
+                const uint64_t sl2 = f2_make(sl, sl), nm2 = f2_make(-mref, -mref);
+                uint64_t acc[4] = {0, 0, 0, 0};
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float y0, y1;
+                    f2_split(ffma2(f2_make(sv[2 * c], sv[2 * c + 1]), sl2, nm2), y0, y1);
+                    const float p0 = ex2_ftz(y0), p1 = ex2_ftz(y1);
+                    acc[c & 3] = fadd2(acc[c & 3], f2_make(p0, p1));
+                    pk[c] = pack_bf16(p0, p1);
+                }
+                float u0, u1;
+                f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), u0, u1);
+                l_run = l_run * alpha + (u0 + u1);
+                tmem_st32(S, pk);
+                tmem_wait_st();
+                bool rows = false;
+                if (k.special) {
+                    if (!mbar_wait(&checked[x], checks++ & 1, err, kErrWaitFull)) return ok = false;
+                    rows = by_rows[x] != 0;
+                }
+                if (rows || (warp_grow && j > 0)) {
+                    // O holds the piece's earlier tiles: wait for the last of those MMAs
+                    if (j > 0 && !mbar_wait(&pv_done[2 * x + (1 - b)], ((it - 1) >> 1) & 1, err, kErrWaitFull)) return ok = false;
+                    tc_fence_after();
+                    if (rows) {
+                        const uint32_t at = 2 * (tiles0 + j) + 1, s = at % NS;  // V's stage (it has landed: `checked`)
+                        if (!mbar_wait(&kv_full[s], (at / NS) & 1, err, kErrWaitFull)) return ok = false;
+                        tree_pv_rows<D>(O, S, sm + L::RING_OFF + s * L::STAGE, vis, alpha, j == 0);
+                    } else {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(O + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            tmem_st32(O + c0, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
+            }
+            // the piece's O
+            if (!mbar_wait(&o_final[x], pieces & 1, err, kErrWaitFull)) return ok = false;
+            ++pieces;
+            tc_fence_after();
+            if (!idle) {
+                // A piece may hold no key that a row sees: weight 0, lse -inf.  Keys whose scores are all -inf
+                // weigh nothing against other pieces, but 0 * inf of their values stays; a row that has
+                // no others is NaN (0 / 0).
+                const float inv = !seen ? 0.f : l_run == 0.f && p.partial >= 0 ? 1.f : 1.f / l_run;
+                const float lse2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
+                const size_t orow = node * a.num_qo_heads + p.kvh * a.group + head;
+                const size_t prow = (size_t)max(p.partial, 0) * (PAIR ? 256 : 128) + (PAIR ? x * 128 : 0) + m;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld32(O + c0, o);
+                    tmem_wait_ld();
+                    float f[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)  // select, not multiply: O may hold NaN of keys the row does not see
+                        f[c] = inv == 0.f ? 0.f : __uint_as_float(o[c]) * inv;
+                    if (!live) continue;
+                    if (p.partial < 0) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c0);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            dst[c] = make_uint4(pack_bf16(f[8 * c], f[8 * c + 1]), pack_bf16(f[8 * c + 2], f[8 * c + 3]),
+                                                pack_bf16(f[8 * c + 4], f[8 * c + 5]), pack_bf16(f[8 * c + 6], f[8 * c + 7]));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D + c0);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) dst[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+                    }
+                }
+                if (live) {
+                    if (p.partial >= 0)
+                        a.part_lse[prow] = lse2;
+                    else if (a.lse)
+                        a.lse[orow] = lse2 * kTrLn2;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[x]);
+            return true;
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Join of the pieces of a cut unit: with w_i = 2^(lse_i - max lse), o = sum w_i o_i / sum w_i.  Column x of the
+// grid looks at the boundary between CTAs x and x + 1, and joins the unit that is cut there first there; a warp
+// per query row, four pieces in flight.
+constexpr int kTrMergeWarps = 8;
+struct TreeMergeArgs {
+    const TreeStart *starts;
+    const float *part_o, *part_lse;
+    __nv_bfloat16 *out;
+    float *lse;
+    int ctas, part_rows, tile_tokens, unit_tokens, group, num_qo_heads;
+};
+template <int D>
+__global__ void __launch_bounds__(32 * kTrMergeWarps) tree_merge_kernel(const TreeMergeArgs a) {
+    constexpr int V = D / 64, BATCH = 4;  // float2 a lane and piece
+    const int lane = threadIdx.x & 31, c = blockIdx.x + 1, f = blockIdx.y * kTrMergeWarps + (threadIdx.x >> 5);
+    griddep_wait();
+    griddep_launch();
+    const TreeStart s = a.starts[c];
+    if (s.r < 0 || s.tile == 0) return;
+    const int2 before = make_int2(a.starts[c - 1].r, a.starts[c - 1].unit);
+    if (before.x == s.r && before.y == s.unit && a.starts[c - 1].tile > 0) return;
+    const int qt = s.unit % s.row.nq, kvh = s.unit / s.row.nq;
+    const int tokens = min(a.unit_tokens, s.row.n - qt * a.unit_tokens);
+    if (f >= tokens * a.group) return;
+    int count = 1;  // pieces: the last of CTA c - 1, the first of those behind it that begin inside the unit
+    for (int c0 = c; c0 < a.ctas; c0 += 32) {
+        const int y = c0 + lane;
+        const bool in = y < a.ctas && a.starts[y].r == s.r && a.starts[y].unit == s.unit && a.starts[y].tile > 0;
+        const unsigned most = __ballot_sync(0xffffffffu, in);
+        const int n = most == 0xffffffffu ? 32 : __ffs(~most) - 1;
+        count += n;
+        if (n < 32) break;
+    }
+    const int tok = f / a.group, x = tok / a.tile_tokens, m = f - x * a.tile_tokens * a.group;
+    auto row_of = [&](int i) {
+        const int slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1);
+        return (size_t)slot * a.part_rows + x * 128 + m;
+    };
+    float mx = -INFINITY;
+    for (int i = lane; i < count; i += 32) mx = fmaxf(mx, __ldcg(a.part_lse + row_of(i)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float sum = 0.f;
+    float2 acc[V] = {};
+    for (int i0 = 0; i0 < count; i0 += BATCH) {
+        float2 v[BATCH][V];
+        float l[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+            if (i0 + b < count) {
+                const size_t row = row_of(i0 + b);
+                l[b] = __ldcg(a.part_lse + row);
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+                    v[b][u] = __ldcg(reinterpret_cast<const float2 *>(a.part_o + row * D) + u * 32 + lane);
+            }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+            if (i0 + b < count) {
+                const float w = exp2f(l[b] - mx);
+                sum += w;
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    acc[u].x += w * v[b][u].x;
+                    acc[u].y += w * v[b][u].y;
+                }
+            }
+    }
+    const float inv = 1.f / sum;  // the largest weight is 1 (NaN if every key of the row scores -inf)
+    const size_t orow = ((size_t)s.row.q_begin + qt * a.unit_tokens + tok) * a.num_qo_heads + kvh * a.group + f % a.group;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+        *reinterpret_cast<uint32_t *>(a.out + orow * D + 2 * (u * 32 + lane)) = pack_bf16(acc[u].x * inv, acc[u].y * inv);
+    if (a.lse && lane == 0) a.lse[orow] = (mx == -INFINITY ? mx : mx + log2f(sum)) * kTrLn2;
+}
+
+template <int D, bool PAIR>
+static cudaError_t launch(const TreeArgs &a, const TreeMergeArgs &m, int rows, const CUtensorMap &tm_kv,
+                          const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CUtensorMap &tm_q, cudaStream_t st) {
+    const size_t smem = 1024 + TrSmem<D>::BYTES;
+    cudaError_t e = set_smem_limit((const void *)tree_kernel<D, PAIR>, smem, st);
+    if (e == cudaSuccess)
+        e = launch_pdl(tree_kernel<D, PAIR>, dim3(m.ctas), dim3(kTrThreads), smem, st, tm_kv, tm_k, tm_v, tm_q, a);
+    if (e == cudaSuccess && m.ctas > 1)
+        e = launch_pdl(tree_merge_kernel<D>, dim3(m.ctas - 1, (rows + kTrMergeWarps - 1) / kTrMergeWarps),
+                       dim3(32 * kTrMergeWarps), 0, st, m);
+    return e;
+}
+
+}  // namespace dev
+
+cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm_kv, const CUtensorMap &tm_k,
+                        const CUtensorMap &tm_v, const CUtensorMap &tm_q, int box_new, int box_q, void *ws, void *out,
+                        float *lse, cudaStream_t st) {
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    dev::TreeArgs a;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.lse = lse;
+    a.rows = reinterpret_cast<const TreeRow *>(w + p.off_rows);
+    a.starts = reinterpret_cast<const TreeStart *>(w + p.off_starts);
+    a.nodes = reinterpret_cast<const TreeNode *>(w + p.off_nodes);
+    a.masks = reinterpret_cast<const unsigned long long *>(w + p.off_masks);
+    a.pages = p.pages;
+    a.part_o = reinterpret_cast<float *>(w + p.off_part_o);
+    a.part_lse = reinterpret_cast<float *>(w + p.off_part_lse);
+    a.hdr = reinterpret_cast<TreeHeader *>(w);
+    a.scale_log2 = p.scale_log2;
+    a.window_left = p.window_left;
+    a.words = p.words;
+    a.num_qo_heads = s.num_qo_heads;
+    a.num_kv_heads = s.num_kv_heads;
+    a.group = s.group();
+    a.page_size = s.page_size;
+    a.page_shift = s.page_shift();
+    a.num_cache_pages = s.num_cache_pages;
+    a.tile_tokens = tree_tile_tokens(s);
+    a.box_rows = s.page_size < kTreeKeys ? s.page_size : kTreeKeys;
+    a.box_new = box_new;
+    a.box_q = box_q;
+    a.q_rows = s.head_dim == 256 && box_q * a.group <= 64 ? 64 : 128;
+    a.oob_row = s.num_cache_pages * 2 * s.page_size;
+    const int unit_tokens = a.tile_tokens * (p.pair ? 2 : 1);
+    const dev::TreeMergeArgs m{a.starts, a.part_o, a.part_lse, a.out, lse, s.sm_count, p.part_rows, a.tile_tokens, unit_tokens,
+                               a.group, s.num_qo_heads};
+    const int rows = (p.max_new < unit_tokens ? p.max_new : unit_tokens) * a.group;
+    if (s.head_dim == 64)
+        return p.pair ? dev::launch<64, true>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<64, false>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st);
+    if (s.head_dim == 128)
+        return p.pair ? dev::launch<128, true>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<128, false>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st);
+    return dev::launch<256, false>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st);
+}
+
+}  // namespace pkv

@@ -1,0 +1,107 @@
+// Plan structures and launchers of the speculative step: page and slot maps built on the GPU, attention of
+// a tree of drafted tokens, acceptance of a path.  Its index arrays live on the device, so the plan is
+// made there too.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "plan.h"
+
+namespace pkv {
+
+constexpr int kTreeKeys = 64;        // keys of one tile
+constexpr int kTreeMaxNew = 256;     // most drafted tokens of a row
+constexpr int kTreeMinPage = 8;      // a TMA box fills whole 8-row swizzle atoms
+constexpr int kTreePieceCost = 2;    // what a piece costs beside its tiles, in tiles
+constexpr int kTreeLeastCost = 6;    // least share of a CTA
+static_assert(kTreeLeastCost > kTreePieceCost, "the CTAs' first tiles are all different");
+constexpr int kMapsMaxRows = 8192;   // rows whose offsets fit the shared memory of the maps kernel
+
+// Device error words of the speculative step (beside those of the bounded waits in ptx.cuh).
+enum TreeError : int { kErrTreeRow = 5, kErrTreePage = 6, kErrTreeParent = 7 };
+
+struct TreeHeader {
+    int32_t err;  // the device error word
+};
+
+// One row as the plan read it.  A row without drafted tokens, or an inconsistent one, has n = nq = 0.
+struct alignas(16) TreeRow {
+    int32_t q_begin;  // its first token
+    int32_t n;        // drafted tokens
+    int32_t ctx;      // cached tokens (-1: inconsistent row)
+    int32_t kv_base;  // offset of its first page in the page list
+    int32_t kt0;      // first key tile (keys 64 * kt0 ..; after 0 under a window)
+    int32_t nc;       // tiles of cached keys
+    int32_t nt;       // tiles, those of the drafted keys behind them
+    int32_t nq;       // units per kv head: query tiles (or pairs of them)
+};
+static_assert(sizeof(TreeRow) == 32, "TreeRow is 8 ints");
+
+// Where a CTA begins: `left` tiles from tile `tile` of unit `unit` of the row, on through its units (kv
+// heads, query tiles inner) and the rows behind it.
+struct alignas(16) TreeStart {
+    TreeRow row;
+    int32_t r, unit, tile, left;  // r = -1: nothing to do
+    long long first;              // tiles before it in the step
+    long long pad;
+};
+static_assert(sizeof(TreeStart) == 64, "TreeStart is 64 bytes");
+
+struct TreeNode {
+    int32_t parent, depth;
+};
+
+struct TreePlan {
+    int batch = 0, num_tokens = 0, max_new = 0, words = 0;  // words: 64-bit words of a node's mask
+    int window_left = -1;
+    float scale_log2 = 0.f;
+    bool pair = false;                     // two query tiles of 128 rows per unit
+    int part_rows = 0;                     // rows of a partial
+    const int32_t *pages = nullptr;        // the caller's page list (device)
+    size_t off_rows = 0, off_starts = 0, off_nodes = 0, off_masks = 0, off_cost = 0, off_units = 0, off_part_o = 0,
+           off_part_lse = 0, total = 0;
+};
+
+// Query tokens of one 128-row tile.
+inline int tree_tile_tokens(const Shape &s) { return 128 / s.group(); }
+// The workspace of a step of `batch` rows, `tokens` tokens and up to `max_new` a row.
+void tree_layout(const Shape &s, int batch, int tokens, int max_new, TreePlan &p);
+
+struct TreeIndex {  // device arrays
+    const int32_t *qo, *kvp, *kvi, *last, *parents;
+    int num_indices;
+    int32_t *positions;
+};
+cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex &x, void *ws, cudaStream_t st);
+// `tm_kv`: boxes of 64 columns x min(page_size, 64) slots of the layer slice; `tm_k`, `tm_v`: of 64 columns x
+// box_new rows of the new keys and values; `tm_q`: of 64 columns x the group's heads x box_q tokens.
+cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm_kv, const CUtensorMap &tm_k,
+                        const CUtensorMap &tm_v, const CUtensorMap &tm_q, int box_new, int box_q, void *ws, void *out,
+                        float *lse, cudaStream_t st);
+
+struct TreeAccept {
+    const void *draft, *target;
+    int wide;  // the tokens are 64-bit
+    const void *k, *v;
+    long long k_layer, k_token, v_layer, v_token;  // strides in elements
+    void *cache;
+    long long cache_layer;
+    int layers;
+    int32_t *accepted, *count;
+    void *next;
+    int32_t *seq;
+};
+cudaError_t launch_tree_accept(const Shape &s, const TreePlan &p, const TreeAccept &x, void *ws, cudaStream_t st);
+
+struct MapsArgs {
+    const int32_t *seq, *fresh, *held, *free_count;
+    int32_t *table, *free_pages;
+    long long table_stride;
+    int rows, max_blocks, free_capacity, indices_capacity, token_capacity, page_shift;
+    int32_t *held_out, *free_count_out, *qo, *kvp, *kvi, *last, *slots, *positions, *status;
+};
+cudaError_t launch_maps(const MapsArgs &a, cudaStream_t st);
+
+}  // namespace pkv

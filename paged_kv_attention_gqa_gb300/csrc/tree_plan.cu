@@ -1,0 +1,354 @@
+// The plan of a speculative step, made on the device (pkv_plan_tree), and the acceptance of a path
+// (pkv_run_accept).
+//
+// Plan.  Block 0 reads the rows' index arrays and gives every attention CTA an equal share of the step's
+// key tiles (a piece of a unit costs two tiles beside its own): prefix sums over the rows, then the place
+// of each CTA's first tile by bisection.  The other blocks take a row per warp and walk each node's parents
+// to its root: depth, and a bit for every ancestor.
+//
+// Accept.  A CTA per row and a few layers.  One warp walks from the root to the first child whose token is the
+// model's choice, then all threads copy the path's keys and values to the row's next slots.  The walk
+// is a chain of shared-memory reads and every CTA of the row repeats it: it costs less than a launch that
+// would pass its result on.  HBM-bound for batches (each accepted vector read and written once).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "tree.h"
+
+namespace pkv {
+
+static size_t put(size_t &at, size_t bytes) {
+    const size_t here = at;
+    at = align_up(at + bytes);
+    return here;
+}
+
+void tree_layout(const Shape &s, int batch, int tokens, int max_new, TreePlan &p) {
+    p.batch = batch;
+    p.num_tokens = tokens;
+    p.max_new = max_new;
+    p.words = (max_new + 63) / 64;
+    // head_dim 256 has no tensor memory for two query tiles' accumulators
+    p.pair = s.head_dim <= 128 && max_new * s.group() > 128;
+    p.part_rows = p.pair ? 256 : 128;
+    size_t at = kAlign;
+    p.off_rows = put(at, (size_t)batch * sizeof(TreeRow));
+    p.off_starts = put(at, (size_t)s.sm_count * sizeof(TreeStart));
+    p.off_nodes = put(at, (size_t)tokens * sizeof(TreeNode));
+    p.off_masks = put(at, (size_t)tokens * p.words * 8);
+    p.off_cost = put(at, (size_t)(batch + 1) * 8);
+    p.off_units = put(at, (size_t)(batch + 1) * 8);
+    p.off_part_o = put(at, (size_t)2 * s.sm_count * p.part_rows * s.head_dim * 4);
+    p.off_part_lse = put(at, (size_t)2 * s.sm_count * p.part_rows * 4);
+    p.total = at;
+}
+
+namespace dev {
+
+struct TreePlanArgs {
+    TreeIndex x;
+    int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, ctas;
+    TreeHeader *hdr;
+    TreeRow *rows;
+    TreeStart *starts;
+    TreeNode *nodes;
+    unsigned long long *masks;
+    long long *cost, *units;
+};
+
+// The row's numbers if its index arrays agree (n = 0 and ctx = -1 if not).
+__device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, bool &ok) {
+    TreeRow t = {};
+    const int q0 = __ldg(a.x.qo + r), q1 = __ldg(a.x.qo + r + 1), k0 = __ldg(a.x.kvp + r), k1 = __ldg(a.x.kvp + r + 1);
+    const int fill = __ldg(a.x.last + r);
+    ok = q0 >= 0 && q1 >= q0 && q1 <= a.tokens && q1 - q0 <= a.max_new && k0 >= 0 && k1 >= k0 && k1 <= a.x.num_indices;
+    if (r == 0) ok = ok && q0 == 0 && k0 == 0;
+    long long length = 0;
+    if (ok && k1 > k0) {
+        ok = fill >= 1 && fill <= a.page_size;
+        length = ((long long)(k1 - k0 - 1) << a.page_shift) + fill;
+    }
+    ok = ok && length >= q1 - q0 && length < (1ll << 31) - 2 * kTreeKeys;
+    t.ctx = -1;
+    if (!ok) return t;
+    t.q_begin = q0;
+    t.n = q1 - q0;
+    t.ctx = (int)length - t.n;
+    t.kv_base = k0;
+    if (t.n == 0) return t;
+    const int lo = a.window_left >= 0 ? max(0, t.ctx - a.window_left) : 0;  // the root's first key
+    t.kt0 = lo / kTreeKeys;
+    t.nc = (t.ctx + kTreeKeys - 1) / kTreeKeys - t.kt0;
+    t.nt = t.nc + (t.n + kTreeKeys - 1) / kTreeKeys;
+    t.nq = (t.n + a.unit_tokens - 1) / a.unit_tokens;
+    return t;
+}
+
+constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
+
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanArgs a) {
+    __shared__ int32_t parent[kPlanWarps][kTreeMaxNew];
+    __shared__ long long sums[2][kPlanWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_wait();
+    griddep_launch();
+    if (blockIdx.x > 0) {
+        // ------------------------------------------------ the nodes of a row
+        const int r = (blockIdx.x - 1) * kPlanWarps + warp;
+        if (r >= a.batch) return;
+        bool ok;
+        const TreeRow t = tree_row(a, r, ok);
+        int32_t *const p = parent[warp];
+        for (int i = lane; i < t.n; i += 32) {
+            int32_t up = a.x.parents ? a.x.parents[t.q_begin + i] : i - 1;
+            if (up < -1 || up >= i) {
+                atomicCAS(&a.hdr->err, 0, kErrTreeParent);
+                up = -1;
+            }
+            p[i] = up;
+        }
+        __syncwarp();
+        for (int i = lane; i < t.n; i += 32) {
+            unsigned long long m[kTreeMaxNew / 64] = {};
+            int depth = -1;
+            for (int j = i; j >= 0; j = p[j]) {
+                ++depth;
+                if (a.window_left < 0 || depth <= a.window_left) {
+#pragma unroll
+                    for (int w = 0; w < kTreeMaxNew / 64; ++w)
+                        if (j >> 6 == w) m[w] |= 1ull << (j & 63);
+                }
+            }
+            a.nodes[t.q_begin + i] = TreeNode{p[i], depth};
+            for (int w = 0; w < a.words; ++w) {
+                unsigned long long v = m[0];
+#pragma unroll
+                for (int u = 1; u < kTreeMaxNew / 64; ++u)
+                    if (w == u) v = m[u];
+                a.masks[(size_t)(t.q_begin + i) * a.words + w] = v;
+            }
+            if (a.x.positions) a.x.positions[t.q_begin + i] = t.ctx + depth;
+        }
+        return;
+    }
+    // ------------------------------------------------ the rows, and each CTA's share
+    long long cost_before = 0, units_before = 0;
+    for (int r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
+        const int r = r0 + threadIdx.x;
+        long long cost = 0, units = 0;
+        if (r < a.batch) {
+            bool ok;
+            const TreeRow t = tree_row(a, r, ok);
+            if (!ok) atomicCAS(&a.hdr->err, 0, kErrTreeRow);
+            a.rows[r] = t;
+            units = (long long)t.nq * a.kv_heads;
+            cost = units * (t.nt + kTreePieceCost);
+        }
+        long long c = cost, u = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, c, o), y = __shfl_up_sync(0xffffffffu, u, o);
+            if (lane >= o) {
+                c += x;
+                u += y;
+            }
+        }
+        if (lane == 31) {
+            sums[0][warp] = c;
+            sums[1][warp] = u;
+        }
+        __syncthreads();
+        long long cw = 0, uw = 0, ct = 0, ut = 0;
+        for (int w = 0; w < kPlanWarps; ++w) {
+            if (w < warp) {
+                cw += sums[0][w];
+                uw += sums[1][w];
+            }
+            ct += sums[0][w];
+            ut += sums[1][w];
+        }
+        __syncthreads();
+        if (r < a.batch) {
+            a.cost[r] = cost_before + cw + c - cost;
+            a.units[r] = units_before + uw + u - units;
+        }
+        cost_before += ct;
+        units_before += ut;
+    }
+    __syncthreads();
+    const long long total = cost_before, tiles = total - kTreePieceCost * units_before;
+    const long long share = max((total + a.ctas - 1) / a.ctas, (long long)kTreeLeastCost);
+    for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
+        TreeStart s = {};
+        const long long at = c * share;
+        s.r = -1;
+        s.first = tiles;
+        if (at < total) {
+            int lo = 0, hi = a.batch - 1;  // the last row that begins at or before `at`
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (a.cost[mid] <= at)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            s.r = lo;
+            s.row = a.rows[lo];
+            const long long off = at - a.cost[lo];
+            const int each = s.row.nt + kTreePieceCost;
+            s.unit = (int)(off / each);
+            s.tile = max(0, (int)(off % each) - kTreePieceCost);
+            s.first = a.cost[lo] - kTreePieceCost * a.units[lo] + (long long)s.unit * s.row.nt + s.tile;
+        }
+        a.starts[c] = s;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
+        const long long next = c + 1 < a.ctas ? a.starts[c + 1].first : tiles;
+        a.starts[c].left = (int)(next - a.starts[c].first);
+    }
+}
+
+struct AcceptArgs {
+    TreeAccept x;
+    const TreeRow *rows;
+    const TreeNode *nodes;
+    const int32_t *pages;
+    TreeHeader *hdr;
+    int layers_per_cta, page_size, page_shift, vecs, num_cache_pages;  // vecs: 16-byte vectors of a token's K (or V)
+};
+
+constexpr int kAcceptThreads = 256;
+
+template <typename Token>
+__global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const AcceptArgs a) {
+    __shared__ int32_t parent[kTreeMaxNew], path[kTreeMaxNew];
+    __shared__ Token draft[kTreeMaxNew], target[kTreeMaxNew];
+    __shared__ long long slot[kTreeMaxNew];  // the cache row of K of path node i, -1 = its page is not one
+    __shared__ int found;
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    griddep_wait();
+    griddep_launch();
+    const TreeRow t = a.rows[r];
+    const Token *const d = static_cast<const Token *>(a.x.draft), *const g = static_cast<const Token *>(a.x.target);
+    for (int i = tid; i < t.n; i += kAcceptThreads) {
+        parent[i] = a.nodes[t.q_begin + i].parent;
+        draft[i] = d[t.q_begin + i];
+        target[i] = g[t.q_begin + i];
+    }
+    __syncthreads();
+    if (tid < 32) {
+        int at = 0, len = 0;
+        while (t.n > 0) {
+            if (lane == 0) path[len] = at;
+            ++len;
+            int next = -1;
+            for (int i0 = (at + 1) & ~31; i0 < t.n && next < 0; i0 += 32) {  // children come behind their parent
+                const int i = i0 + lane;
+                const unsigned hit = __ballot_sync(0xffffffffu, i < t.n && parent[i] == at && draft[i] == target[at]);
+                if (hit) next = i0 + __ffs(hit) - 1;
+            }
+            if (next < 0) break;
+            at = next;
+        }
+        if (lane == 0) found = len;
+    }
+    __syncthreads();
+    const int len = found;
+    for (int i = tid; i < len; i += kAcceptThreads) {
+        const int pos = t.ctx + i, page = a.pages[t.kv_base + (pos >> a.page_shift)];
+        const bool fine = (unsigned)page < (unsigned)a.num_cache_pages;
+        if (!fine) atomicCAS(&a.hdr->err, 0, kErrTreePage);
+        slot[i] = fine ? (long long)page * 2 * a.page_size + (pos & (a.page_size - 1)) : -1;
+    }
+    if (blockIdx.y == 0) {
+        for (int i = tid; i < t.n; i += kAcceptThreads) a.x.accepted[t.q_begin + i] = i < len ? path[i] : -1;
+        if (tid == 0) {
+            a.x.count[r] = len;
+            static_cast<Token *>(a.x.next)[r] = len ? target[path[len - 1]] : Token(-1);
+            if (a.x.seq && len) a.x.seq[r] = t.ctx + len;
+        }
+    }
+    __syncthreads();
+    const int l0 = blockIdx.y * a.layers_per_cta, l1 = min(a.x.layers, l0 + a.layers_per_cta);
+    // vectors (layer, path node, K or V, column): four in flight a thread
+    const int per_layer = len * 2 * a.vecs, work = (l1 - l0) * per_layer;
+    constexpr int BATCH = 4;
+    for (int e0 = tid; e0 < work; e0 += BATCH * kAcceptThreads) {
+        uint4 v[BATCH];
+        uint4 *to[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int e = e0 + b * kAcceptThreads;
+            to[b] = nullptr;
+            if (e >= work) continue;
+            const int layer = e / per_layer, f = e % per_layer, i = f / (2 * a.vecs), kv = f % (2 * a.vecs) >= a.vecs;
+            const int c = f % a.vecs;
+            const long long l = l0 + layer, token = t.q_begin + path[i];
+            const uint4 *from = kv ? static_cast<const uint4 *>(a.x.v) + (l * a.x.v_layer + token * a.x.v_token) / 8 + c
+                                   : static_cast<const uint4 *>(a.x.k) + (l * a.x.k_layer + token * a.x.k_token) / 8 + c;
+            if (slot[i] < 0) continue;
+            v[b] = *from;
+            to[b] = static_cast<uint4 *>(a.x.cache) + l * (a.x.cache_layer / 8) + (slot[i] + (kv ? a.page_size : 0)) * a.vecs + c;
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+            if (to[b]) *to[b] = v[b];
+    }
+}
+
+}  // namespace dev
+
+cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex &x, void *ws, cudaStream_t st) {
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(TreeHeader), st);  // the blocks record errors in any order
+    if (e != cudaSuccess) return e;
+    dev::TreePlanArgs a;
+    a.x = x;
+    a.batch = p.batch;
+    a.tokens = p.num_tokens;
+    a.max_new = p.max_new;
+    a.words = p.words;
+    a.window_left = p.window_left;
+    a.page_size = s.page_size;
+    a.page_shift = s.page_shift();
+    a.kv_heads = s.num_kv_heads;
+    a.unit_tokens = tree_tile_tokens(s) * (p.pair ? 2 : 1);
+    a.ctas = s.sm_count;
+    a.hdr = reinterpret_cast<TreeHeader *>(w);
+    a.rows = reinterpret_cast<TreeRow *>(w + p.off_rows);
+    a.starts = reinterpret_cast<TreeStart *>(w + p.off_starts);
+    a.nodes = reinterpret_cast<TreeNode *>(w + p.off_nodes);
+    a.masks = reinterpret_cast<unsigned long long *>(w + p.off_masks);
+    a.cost = reinterpret_cast<long long *>(w + p.off_cost);
+    a.units = reinterpret_cast<long long *>(w + p.off_units);
+    return launch_pdl(dev::tree_plan_kernel, dim3(1 + (p.batch + dev::kPlanWarps - 1) / dev::kPlanWarps),
+                      dim3(dev::kPlanThreads), 0, st, a);
+}
+
+cudaError_t launch_tree_accept(const Shape &s, const TreePlan &p, const TreeAccept &x, void *ws, cudaStream_t st) {
+    if (p.batch == 0) return cudaSuccess;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    dev::AcceptArgs a;
+    a.x = x;
+    a.rows = reinterpret_cast<const TreeRow *>(w + p.off_rows);
+    a.nodes = reinterpret_cast<const TreeNode *>(w + p.off_nodes);
+    a.pages = p.pages;
+    a.hdr = reinterpret_cast<TreeHeader *>(w);
+    a.page_size = s.page_size;
+    a.page_shift = s.page_shift();
+    a.vecs = s.num_kv_heads * s.head_dim / 8;
+    a.num_cache_pages = s.num_cache_pages;
+    // a layer a CTA while the rows do not fill the GPU with eight CTAs an SM
+    const int most = std::max(1, 8 * s.sm_count / p.batch), chunks = std::max(1, std::min(x.layers, most));
+    a.layers_per_cta = std::max(1, (x.layers + chunks - 1) / chunks);
+    a.layers_per_cta = std::min<int>(a.layers_per_cta, std::max(1, (1 << 29) / (kTreeMaxNew * 2 * a.vecs)));  // 32-bit counts
+    const dim3 grid(p.batch, std::max(1, (x.layers + a.layers_per_cta - 1) / a.layers_per_cta));
+    return x.wide ? launch_pdl(dev::tree_accept_kernel<long long>, grid, dim3(dev::kAcceptThreads), 0, st, a)
+                  : launch_pdl(dev::tree_accept_kernel<int>, grid, dim3(dev::kAcceptThreads), 0, st, a);
+}
+
+}  // namespace pkv
