@@ -157,6 +157,7 @@ def _dptr(t):
 
 _torch = None       # torch, imported by the first call that needs it
 _raw_stream = None  # the current stream of a device as an integer
+_marshal = None     # the compiled marshalling of the speculative step's calls (csrc/marshal.cpp)
 
 
 def _load_torch():
@@ -167,6 +168,25 @@ def _load_torch():
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     return torch
+
+
+def _load_marshal():
+    """The module _marshal, built beside the library, connected to the library's entry points; raises if absent."""
+    global _marshal
+    _load_torch()  # its libraries first
+    from . import _marshal as module
+    lib = load()
+    module.connect(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                     for name in ("pkv_build_maps", "pkv_plan_tree", "pkv_run_tree", "pkv_run_accept")))
+    _marshal = module
+
+
+def _place(stream):
+    """The current device's index and the stream of a call, as integers."""
+    if _marshal is None:
+        _load_marshal()
+    device = _torch.cuda.current_device()
+    return device, _raw_stream(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _stream(stream):
@@ -222,6 +242,7 @@ class Handle:
         self._keep = []
         self._planned_tokens = self._planned_rows = self._kept = 0
         self._tree_pages = None
+        self._dims = (num_cache_pages, page_size, num_qo_heads, num_kv_heads, head_dim)
 
     def close(self):
         if getattr(self, "h", None):
@@ -233,6 +254,9 @@ class Handle:
             self.close()
         except Exception:
             pass
+
+    def _address(self):
+        return self.h.value if self.h else 0
 
     def _check(self, st):
         if st != OK:
@@ -360,110 +384,38 @@ class Handle:
                    free_count_out=None, stream=None):
         """Pages, page lists, slots and positions of a step from the rows' lengths; num_blocks and free_count are
         updated in place unless the *_out tensors are given.  status[0]: 0, or why nothing was done."""
-        torch = _torch or _load_torch()
-        device, i32, batch = torch.cuda.current_device(), torch.int32, seq_lens.shape[0]
-        held_out = num_blocks if num_blocks_out is None else num_blocks_out
-        count_out = free_count if free_count_out is None else free_count_out
-        if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-            raise ValueError("block_table must be [batch, blocks] with unit stride in its last dimension")
-        width = block_table.shape[1]
-        if slots is not None and positions is not None and slots.shape != positions.shape:
-            raise ValueError("slots and positions must have the same length")
-        tokens = 0 if slots is None and positions is None else (slots if slots is not None else positions).shape[0]
-        for name, t, shape in (
-                ("seq_lens", seq_lens, (batch,)), ("new_lens", new_lens, (batch,)), ("num_blocks", num_blocks, (batch,)),
-                ("num_blocks_out", held_out, (batch,)), ("free_pages", free_pages, (free_pages.numel(),)),
-                ("free_count", free_count, (1,)), ("free_count_out", count_out, (1,)), ("qo_indptr", qo_indptr, (batch + 1,)),
-                ("kv_indptr", kv_indptr, (batch + 1,)), ("kv_indices", kv_indices, (kv_indices.numel(),)),
-                ("last_page_len", last_page_len, (batch,)), ("status", status, (1,))):
-            _check_tensor(name, t, i32, shape, device)
-        _check_tensor("block_table", block_table, i32, (batch, width), device, contiguous=False)
-        for name, t in (("slots", slots), ("positions", positions)):
-            if t is not None:
-                _check_tensor(name, t, i32, (tokens,), device)
-        if slots is None and positions is None:
-            tokens = 2 ** 31 - 1  # nothing is listed by token
-        self._check(self.lib.pkv_build_maps(
-            self.h, seq_lens.data_ptr(), new_lens.data_ptr(), batch, block_table.data_ptr(), _stride(block_table, 0, width),
-            width, num_blocks.data_ptr(), held_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
-            free_count.data_ptr(), count_out.data_ptr(), qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
-            kv_indices.numel(), last_page_len.data_ptr(), _dptr(slots), _dptr(positions), tokens, status.data_ptr(),
-            _raw_stream(device) if stream is None else _stream(stream)))
+        device, stream = _place(stream)
+        self._check(_marshal.build_maps(
+            self._address(), device, stream, seq_lens, new_lens, block_table, num_blocks,
+            num_blocks if num_blocks_out is None else num_blocks_out, free_pages, free_count,
+            free_count if free_count_out is None else free_count_out, qo_indptr, kv_indptr, kv_indices, last_page_len, slots,
+            positions, status))
 
     def plan_tree(self, qo_indptr, kv_indptr, kv_indices, last_page_len, parents=None, *, num_tokens, max_new,
                   positions=None, workspace, window_left=-1, sm_scale=0.0, stream=None):
         """Plan a step of drafted tokens from device index arrays; parents None: every row is a chain."""
-        torch = _torch or _load_torch()
-        device, i32, batch = torch.cuda.current_device(), torch.int32, kv_indptr.shape[0] - 1
-        for name, t, shape in (("qo_indptr", qo_indptr, (batch + 1,)), ("kv_indptr", kv_indptr, (batch + 1,)),
-                               ("kv_indices", kv_indices, (kv_indices.numel(),)), ("last_page_len", last_page_len, (batch,)),
-                               ("parents", parents, (num_tokens,)), ("positions", positions, (num_tokens,))):
-            if t is not None:
-                _check_tensor(name, t, i32, shape, device)
-        self._check(self.lib.pkv_plan_tree(
-            self.h, qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(), kv_indices.numel(),
-            last_page_len.data_ptr(), batch, _dptr(parents), int(num_tokens), int(max_new), int(window_left), float(sm_scale),
-            _dptr(positions), _workspace(workspace, device), workspace.numel() * workspace.element_size(),
-            _raw_stream(device) if stream is None else _stream(stream)))
-        self._planned_tokens, self._planned_rows = int(num_tokens), batch
+        device, stream = _place(stream)
+        self._check(_marshal.plan_tree(self._address(), device, stream, qo_indptr, kv_indptr, kv_indices, last_page_len, parents,
+                                       num_tokens, max_new, positions, workspace, window_left, sm_scale))
+        self._planned_tokens, self._planned_rows = int(num_tokens), kv_indptr.shape[0] - 1
         self._tree_pages = kv_indices  # the step's later calls read it
-
-    def _new_kv(self, name, t, lead, torch, device):
-        """A tensor of new keys or values [*lead, tokens, kv heads, head_dim] with strides of its own before the heads."""
-        c = self.cfg
-        _check_tensor(name, t, torch.bfloat16, (*lead, self._planned_tokens, c.num_kv_heads, c.head_dim), device, contiguous=False)
-        if t.stride(-1) != 1 or (c.num_kv_heads > 1 and t.stride(-2) != c.head_dim):
-            raise ValueError(f"{name} must have its heads side by side")
-        return t.data_ptr(), _stride(t, len(lead), c.num_kv_heads * c.head_dim)
 
     def run_tree(self, q, k_new, v_new, kv_layer, out, lse=None, *, workspace, stream=None):
         """Attention of the planned drafted tokens over the row's cached tokens, their ancestors and
         themselves: q [T, Hq, D], k_new and v_new [T, Hkv, D] (token strides free), out [T, Hq, D]."""
-        torch, c = _torch or _load_torch(), self.cfg
-        device, tokens = torch.cuda.current_device(), self._planned_tokens
-        k, ks = self._new_kv("k_new", k_new, (), torch, device)
-        v, vs = self._new_kv("v_new", v_new, (), torch, device)
-        _check_tensor("q", q, torch.bfloat16, (tokens, c.num_qo_heads, c.head_dim), device, contiguous=False)
-        if q.stride(2) != 1 or (c.num_qo_heads > 1 and q.stride(1) != c.head_dim):
-            raise ValueError("q must have its heads side by side")
-        _check_tensor("kv_layer", kv_layer, torch.bfloat16,
-                      (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim), device)
-        _check_tensor("out", out, torch.bfloat16, (tokens, c.num_qo_heads, c.head_dim), device)
-        if lse is not None:
-            _check_tensor("lse", lse, torch.float32, (tokens, c.num_qo_heads), device)
-        self._check(self.lib.pkv_run_tree(
-            self.h, q.data_ptr(), _stride(q, 0, c.num_qo_heads * c.head_dim), k, ks, v, vs, kv_layer.data_ptr(),
-            out.data_ptr(), _dptr(lse), _workspace(workspace, device),
-            _raw_stream(device) if stream is None else _stream(stream)))
+        device, stream = _place(stream)
+        self._check(_marshal.run_tree(self._address(), device, stream, self._dims, self._planned_tokens, q, k_new, v_new, kv_layer,
+                                      out, lse, workspace))
 
     def run_accept(self, draft_tokens, target_tokens, k_new, v_new, kv_cache, accepted, num_accepted, next_tokens,
                    seq_lens=None, *, workspace, stream=None):
         """The path of every row's drafted tokens that target_tokens confirm, and its keys and values into the
         row's next slots of every layer: k_new and v_new [layers, T, Hkv, D] (layer and token strides free),
         kv_cache [layers, pages, 2, page_size, Hkv, D] (layers may be strided)."""
-        torch, c = _torch or _load_torch(), self.cfg
-        device, tokens, batch = torch.cuda.current_device(), self._planned_tokens, self._planned_rows
-        kind, layers = draft_tokens.dtype, kv_cache.shape[0]
-        if kind not in (torch.int32, torch.int64):
-            raise TypeError(f"draft_tokens must be int32 or int64, got {kind}")
-        for name, t, dtype, shape in (
-                ("draft_tokens", draft_tokens, kind, (tokens,)), ("target_tokens", target_tokens, kind, (tokens,)),
-                ("accepted", accepted, torch.int32, (tokens,)), ("num_accepted", num_accepted, torch.int32, (batch,)),
-                ("next_tokens", next_tokens, kind, (batch,)), ("seq_lens", seq_lens, torch.int32, (batch,))):
-            if t is not None or name != "seq_lens":
-                _check_tensor(name, t, dtype, shape, device)
-        k, ks = self._new_kv("k_new", k_new, (layers,), torch, device)
-        v, vs = self._new_kv("v_new", v_new, (layers,), torch, device)
-        layer = (c.num_cache_pages, 2, c.page_size, c.num_kv_heads, c.head_dim)
-        _check_tensor("kv_cache", kv_cache, torch.bfloat16, (layers, *layer), device, contiguous=False)
-        if layers and not kv_cache[0].is_contiguous():
-            raise ValueError("kv_cache must have contiguous layers")
-        width, each = c.num_kv_heads * c.head_dim, c.num_kv_heads * c.head_dim * 2 * c.page_size * c.num_cache_pages
-        self._check(self.lib.pkv_run_accept(
-            self.h, draft_tokens.data_ptr(), target_tokens.data_ptr(), kind.itemsize, k, _stride(k_new, 0, width), ks, v,
-            _stride(v_new, 0, width), vs, kv_cache.data_ptr(), _stride(kv_cache, 0, each), layers, accepted.data_ptr(),
-            num_accepted.data_ptr(), next_tokens.data_ptr(), _dptr(seq_lens), _workspace(workspace, device),
-            _raw_stream(device) if stream is None else _stream(stream)))
+        device, stream = _place(stream)
+        self._check(_marshal.run_accept(self._address(), device, stream, self._dims, self._planned_tokens, self._planned_rows,
+                                        draft_tokens, target_tokens, k_new, v_new, kv_cache, accepted, num_accepted, next_tokens,
+                                        seq_lens, workspace))
 
     def gather_kv(self, kv_layer, pages, num_tokens, k_out, v_out, stream=None):
         """pages: a device int32 tensor of page ids."""

@@ -1,12 +1,15 @@
-"""Build libpkv.so in-tree: nvcc for sm_103a, one process per translation unit.
+"""Build libpkv.so in-tree: nvcc for sm_103a, one process per translation unit; and the Python module _marshal, which
+hands the tensors of the speculative step's calls to it.
 
     python -m paged_kv_attention_gqa_gb300.build [--force] [--verbose]
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -18,6 +21,7 @@ SOURCES = ["pkv_api.cu", "decode.cu", "prefill.cu", "prefill_gather.cu", "prefil
            "planner.cpp", "latent_plan.cpp", "evict_plan.cpp"]
 HEADERS = ["plan.h", "launch.h", "handle.h", "latent.h", "evict.h", "tree.h", "decode_kernel.cuh", "ptx.cuh", "tcgen05.cuh", "prefill_kernel.cuh", "prefill_pair.cuh",
            "prefill_wide.cuh"]
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,12 +39,24 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _marshal_command(out: str):
+    """g++ with torch's headers and libraries, found without importing it."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    lib = os.path.join(torch, "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-isystem", os.path.join(torch, "include"), "-isystem",
+            sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-Wl,-rpath," + lib, "-o", out]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OBJ, exist_ok=True)
     nvcc = _nvcc()
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "pkv.h")]
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra_flags]
-    procs, objs = [], []
+    procs, objs, marshal = [], [], None
+    if force or _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(ROOT, "include", "pkv.h")]):
+        marshal = MARSHAL + f".{os.getpid()}.tmp"
+        procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(marshal), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in SOURCES:
         path = os.path.join(CSRC, src)
         obj = os.path.join(OBJ, src + ".o")
@@ -62,7 +78,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed on {failed}")
+        raise RuntimeError(f"compilation failed of {failed}")
+    if marshal:
+        os.replace(marshal, MARSHAL)
     if force or procs or _stale(OUT, objs):
         tmp = OUT + f".{os.getpid()}.tmp"
         subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"],

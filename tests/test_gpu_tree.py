@@ -336,3 +336,28 @@ def test_the_same_call_gives_the_same_bits():
     for _ in range(3):
         s.run()
         assert torch.equal(first[0], s.out) and torch.equal(first[1], s.lse)
+
+
+def test_refused_strides_and_alignment():
+    s = Step([30], [R.tree(4, 2)], 8, 2, 64, 16, 31)
+    s.plan()
+    q, k, v, kv = s.inputs()
+    out, T = torch.empty_like(q), len(q)
+    wide = torch.zeros(T, 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")  # rows 4 elements too long: not a multiple of 8
+    odd = torch.zeros(T * 128 + 8, dtype=torch.bfloat16, device="cuda")[4:4 + T * 128].view(T, 2, 64)
+    over = torch.zeros(128, dtype=torch.bfloat16, device="cuda").as_strided((T, 2, 64), (0, 64, 1))
+    for bad in (wide[:, :128].view(T, 2, 64), odd, over):
+        with pytest.raises(B.PkvError) as e:
+            s.h.run_tree(q, bad, v, kv, out, workspace=s.ws)
+        assert e.value.status == B.ERR_INVALID
+        with pytest.raises(B.PkvError):
+            s.h.run_tree(q, k, bad, kv, out, workspace=s.ws)
+    with pytest.raises(B.PkvError) as e:
+        s.h.run_decode(q, kv, out, workspace=s.ws)
+    assert e.value.status == B.ERR_NOT_PLANNED
+    other = torch.empty_like(s.ws)
+    with pytest.raises(B.PkvError) as e:
+        s.h.run_tree(q, k, v, kv, out, workspace=other)
+    assert e.value.status == B.ERR_NOT_PLANNED
+    s.run()
+    s.check("after the refusals")

@@ -100,67 +100,30 @@ def test_workspace_sizes():
     assert 2 * 152 * 256 * 65 * 4 <= a < b < a + (1 << 20)
 
 
-class Tensor:
-    """A stand-in that says what it is."""
-
-    def __init__(self, dtype, *shape, device=1, strides=None):
-        self.dtype, self.shape, self.device, self._strides = dtype, shape, device, strides
-
-    def get_device(self):
-        return self.device
-
-    def dim(self):
-        return len(self.shape)
-
-    def numel(self):
-        n = 1
-        for x in self.shape:
-            n *= x
-        return n
-
-    def element_size(self):
-        return 4
-
-    def stride(self, dim):
-        if self._strides:
-            return self._strides[dim]
-        n = 1
-        for x in self.shape[dim % len(self.shape) + 1:]:
-            n *= x
-        return n
-
-    def is_contiguous(self):
-        return not self._strides
-
-    def data_ptr(self):
-        return 256
-
-    def __getitem__(self, i):
-        return Tensor(self.dtype, *self.shape[1:], device=self.device)
+I32, I64, BF, F32, U8 = torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8
 
 
-class Library:
-    def __init__(self):
-        self.calls = []
-
-    def __getattr__(self, name):
-        return lambda *a: self.calls.append(name) or B.OK
-
-
-I32, I64, BF, F32, U8 = (types.SimpleNamespace(itemsize=n, name=i) for i, n in enumerate((4, 8, 2, 4, 1)))
+def Tensor(dtype, *shape, strides=None):
+    """A tensor on the host, whose device index is -1: the fixture makes that the current one."""
+    return torch.empty(1 << 20, dtype=dtype).as_strided(shape, strides) if strides else torch.empty(shape, dtype=dtype)
 
 
 @pytest.fixture
 def called(monkeypatch):
-    torch = types.SimpleNamespace(bfloat16=BF, float32=F32, int32=I32, int64=I64, uint8=U8,
-                                  cuda=types.SimpleNamespace(current_device=lambda: 1))
-    monkeypatch.setattr(B, "_torch", torch)
-    monkeypatch.setattr(B, "_raw_stream", lambda device: 0)
+    """A handle whose library only counts the calls."""
+    calls, back = [], ctypes.CFUNCTYPE(ctypes.c_int)
     h = make()
     h._planned_tokens, h._planned_rows = 5, 2
-    real, h.lib = h.lib, Library()
+    B._load_marshal()
+    fake = [back(lambda i=i: calls.append(i) or B.OK) for i in range(4)]
+    B._marshal.connect(*(ctypes.cast(f, ctypes.c_void_p).value for f in fake))
+    h.device = -1
+    monkeypatch.setattr(B, "_torch", types.SimpleNamespace(cuda=types.SimpleNamespace(current_device=lambda: h.device)))
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 0)
+    h.calls = calls
     yield h
-    h.lib = real
+    monkeypatch.undo()
+    B._load_marshal()
 
 
 def ints(**kw):
@@ -198,35 +161,58 @@ CALLS = {"maps": do_maps, "plan": do_plan, "tree": do_tree, "accept": do_accept}
 @pytest.mark.parametrize("call", sorted(CALLS))
 def test_the_binding_passes_good_arguments(called, call):
     CALLS[call](called, ints())
-    assert len(called.lib.calls) == 1
+    assert called.calls == [list(CALLS).index(call)]
 
 
-@pytest.mark.parametrize("call,kw,error", [
-    ("maps", dict(seq=Tensor(I64, 2)), TypeError), ("maps", dict(new=Tensor(I32, 3)), ValueError),
-    ("maps", dict(table=Tensor(I32, 18)), ValueError), ("maps", dict(table=Tensor(I32, 2, 9, strides=(1, 2))), ValueError),
-    ("maps", dict(table=Tensor(I32, 3, 9)), ValueError), ("maps", dict(held=Tensor(I32, 2, device=0)), ValueError),
-    ("maps", dict(count=Tensor(I32, 2)), ValueError), ("maps", dict(qo=Tensor(I32, 2)), ValueError),
-    ("maps", dict(kvi=Tensor(I32, 9, strides=(2,))), ValueError), ("maps", dict(pos=Tensor(I32, 6)), ValueError),
-    ("maps", dict(slots=Tensor(F32, 5)), TypeError), ("maps", dict(status=Tensor(I32, 1, device=-1)), ValueError),
-    ("plan", dict(parents=Tensor(I32, 4)), ValueError), ("plan", dict(parents=Tensor(I64, 5)), TypeError),
-    ("plan", dict(qo=Tensor(I32, 4)), ValueError), ("plan", dict(last=Tensor(I32, 3)), ValueError),
-    ("plan", dict(kvi=Tensor(I32, 9, device=-1)), ValueError), ("plan", dict(ws=Tensor(U8, 4096, device=0)), ValueError),
-    ("tree", dict(q=Tensor(F32, 5, 8, 64)), TypeError), ("tree", dict(q=Tensor(BF, 4, 8, 64)), ValueError),
-    ("tree", dict(q=Tensor(BF, 5, 8, 64, strides=(1024, 128, 1))), ValueError),
-    ("tree", dict(k=Tensor(BF, 5, 2, 64, strides=(256, 128, 1))), ValueError),
-    ("tree", dict(v=Tensor(BF, 5, 2, 64, strides=(256, 64, 2))), ValueError),
-    ("tree", dict(out=Tensor(BF, 5, 8, 64, strides=(1024, 64, 1))), ValueError), ("tree", dict(lse=Tensor(BF, 5, 8)), TypeError),
-    ("tree", dict(kv=Tensor(BF, 61, 2, 16, 2, 64)), ValueError), ("tree", dict(ws=Tensor(U8, 4096, device=0)), ValueError),
-    ("accept", dict(draft=Tensor(F32, 5)), TypeError), ("accept", dict(target=Tensor(I32, 5)), TypeError),
-    ("accept", dict(next=Tensor(I32, 2)), TypeError), ("accept", dict(num=Tensor(I32, 3)), ValueError),
-    ("accept", dict(seq=Tensor(I32, 3)), ValueError), ("accept", dict(k=Tensor(BF, 2, 5, 2, 64)), ValueError),
-    ("accept", dict(cache=Tensor(BF, 3, 60, 2, 8, 2, 64)), ValueError), ("accept", dict(accepted=Tensor(I64, 5)), TypeError),
-    ("accept", dict(ws=Tensor(U8, 4096, device=0)), ValueError),
-])
-def test_the_binding_refuses(called, call, kw, error):
-    with pytest.raises(error):
+@pytest.mark.parametrize("call", sorted(CALLS))
+def test_tensors_on_another_device_are_refused(called, call):
+    called.device = 0
+    with pytest.raises(ValueError, match="on the current CUDA device"):
+        CALLS[call](called, ints())
+    assert not called.calls
+
+
+def test_a_closed_handle_is_refused(called):
+    """Address 0 reaches the library, which refuses it (test_runs_without_a_plan_are_refused)."""
+    called.close()
+    assert called._address() == 0
+
+
+WRONG = [
+    ("maps", dict(seq=Tensor(I64, 2)), TypeError, "seq_lens"), ("maps", dict(new=Tensor(I32, 3)), ValueError, "new_lens"),
+    ("maps", dict(seq=Tensor(I32, 2, 1)), ValueError, "seq_lens"), ("maps", dict(seq=[1, 2]), TypeError, "seq_lens"),
+    ("maps", dict(table=Tensor(I32, 18)), ValueError, "block_table"),
+    ("maps", dict(table=Tensor(I32, 2, 9, strides=(1, 2))), ValueError, "block_table"),
+    ("maps", dict(table=Tensor(I32, 3, 9)), ValueError, "block_table"), ("maps", dict(table=Tensor(I64, 2, 9)), TypeError, "block_table"),
+    ("maps", dict(held=Tensor(I32, 3)), ValueError, "num_blocks"), ("maps", dict(free=Tensor(I32, 7, 1)), ValueError, "free_pages"),
+    ("maps", dict(count=Tensor(I32, 2)), ValueError, "free_count"), ("maps", dict(qo=Tensor(I32, 2)), ValueError, "qo_indptr"),
+    ("maps", dict(kvp=Tensor(I32, 4)), ValueError, "kv_indptr"), ("maps", dict(last=None), TypeError, "last_page_len"),
+    ("maps", dict(kvi=Tensor(I32, 9, strides=(2,))), ValueError, "kv_indices"), ("maps", dict(pos=Tensor(I32, 6)), ValueError, "positions"),
+    ("maps", dict(slots=Tensor(F32, 5)), TypeError, "slots"), ("maps", dict(status=Tensor(I32, 2)), ValueError, "status"),
+    ("plan", dict(parents=Tensor(I32, 4)), ValueError, "parents"), ("plan", dict(parents=Tensor(I64, 5)), TypeError, "parents"),
+    ("plan", dict(qo=Tensor(I32, 4)), ValueError, "qo_indptr"), ("plan", dict(last=Tensor(I32, 3)), ValueError, "last_page_len"),
+    ("plan", dict(kvp=Tensor(I32, 0), qo=Tensor(I32, 0)), ValueError, "kv_indptr"), ("plan", dict(pos=Tensor(I32, 4)), ValueError, "positions"),
+    ("plan", dict(ws=None), TypeError, "workspace"), ("plan", dict(ws=Tensor(U8, 64, strides=(2,))), ValueError, "workspace"),
+    ("tree", dict(q=Tensor(F32, 5, 8, 64)), TypeError, "q must"), ("tree", dict(q=Tensor(BF, 4, 8, 64)), ValueError, "q must"),
+    ("tree", dict(q=Tensor(BF, 5, 8, 64, strides=(1024, 128, 1))), ValueError, "side by side"),
+    ("tree", dict(k=Tensor(BF, 5, 2, 64, strides=(256, 128, 1))), ValueError, "side by side"),
+    ("tree", dict(v=Tensor(BF, 5, 2, 64, strides=(256, 64, 2))), ValueError, "side by side"),
+    ("tree", dict(out=Tensor(BF, 5, 8, 64, strides=(1024, 64, 1))), ValueError, "out"), ("tree", dict(lse=Tensor(BF, 5, 8)), TypeError, "lse"),
+    ("tree", dict(kv=Tensor(BF, 61, 2, 16, 2, 64)), ValueError, "kv_layer"), ("tree", dict(k=None), TypeError, "k_new"),
+    ("accept", dict(draft=Tensor(F32, 5)), TypeError, "draft_tokens"), ("accept", dict(target=Tensor(I32, 5)), TypeError, "target_tokens"),
+    ("accept", dict(next=Tensor(I32, 2)), TypeError, "next_tokens"), ("accept", dict(num=Tensor(I32, 3)), ValueError, "num_accepted"),
+    ("accept", dict(seq=Tensor(I32, 3)), ValueError, "seq_lens"), ("accept", dict(k=Tensor(BF, 2, 5, 2, 64)), ValueError, "k_new"),
+    ("accept", dict(cache=Tensor(BF, 3, 60, 2, 8, 2, 64)), ValueError, "kv_cache"), ("accept", dict(cache=Tensor(BF, 60, 2, 16, 2, 64)), ValueError, "kv_cache"),
+    ("accept", dict(cache=Tensor(BF, 1, 60, 2, 16, 2, 64, strides=(0, 4096, 2048, 64, 1024, 1)), k=Tensor(BF, 1, 5, 2, 64), v=Tensor(BF, 1, 5, 2, 64)), ValueError, "contiguous layers"),
+    ("accept", dict(accepted=Tensor(I64, 5)), TypeError, "accepted"), ("accept", dict(ws=7), TypeError, "workspace"),
+]
+
+
+@pytest.mark.parametrize("call,kw,error,word", WRONG, ids=[f"{i}-{w[0]}-{w[3].split()[0]}" for i, w in enumerate(WRONG)])
+def test_the_binding_refuses(called, call, kw, error, word):
+    with pytest.raises(error, match=word):
         CALLS[call](called, ints(**kw))
-    assert not called.lib.calls
+    assert not called.calls
 
 
 def test_reference_trees():
