@@ -1,4 +1,4 @@
-// Attention of a tree of drafted tokens over a paged cache (pkv_run_tree), and the join of its cut units.
+// Attention of a tree of drafted tokens over a paged cache (pkv_run_tree).
 //
 // Row r has C cached tokens and n drafted ones; node i's parent stands before it.  Node i sees the cached
 // keys and those of its ancestors and itself (under a window, those at most window_left positions above
@@ -8,14 +8,18 @@
 // heads a kv head) share a head's keys: 4 D n g operations on 4 D bytes a key.  The tensor cores and HBM
 // balance near n g = 280; below it the cached K and V, read once, are the floor.
 //
-// Work: a unit is one query tile of up to 128 rows (row m = token * g + head), or two (PAIR) that share every
+// Work: a unit is one query tile of up to 128 rows (row m = token * g + head), or two that share every
 // K and V tile, over the 64-key tiles of its row: those of the cached keys, then those of the drafted
 // ones, which so begin at a tile's first key.  A persistent CTA per SM takes an equal run of tiles, cut
 // by the plan; a unit that several CTAs share leaves normalised partials, joined by a second kernel.
-//  * warps 0-3 and 4-7 are two softmax groups (thread = query row = tensor-memory lane).  With PAIR
-//    group x has query tile x; else the groups take the pieces in turn, and one's epilogue runs under
-//    the other's tiles.  Each has two S buffers of 64 columns, so that S of the next tile runs under the
-//    softmax, and an accumulator (one for both groups at head_dim 256).
+//  * warps 0-3 and 4-7 are two softmax groups (thread = query row = tensor-memory lane), each with two S
+//    buffers of 64 columns, so that S of its next tile runs under its softmax, and an accumulator.
+//    SPLIT: a unit's tiles in turn, each group with a running maximum, sum and O of its own, joined in the
+//    epilogue, where a group reads half of the columns of both (one group alone takes 950 cycles a tile: more
+//    than the 700 in which HBM delivers one of head_dim 64).
+//    PAIR: group x has query tile x of two.
+//    TURNS (head_dim 256, where tensor memory has room for one O): the pieces in turn, so that one group's
+//    epilogue runs under the other's tiles.
 //  * warp 8 copies Q of each piece (two buffers where they fit) and the K tiles, warp 11 the V tiles, into
 //    one ring of 16 KB stages (8 at head_dim 64, 32 at 256): one lane a box of a page and 64 columns.
 //  * warp 9 issues S = Q K^T, warp 10 O += P V (P from tensor memory, over its S).
@@ -36,6 +40,15 @@ namespace pkv {
 namespace dev {
 
 constexpr int kTrThreads = 384;
+// Registers: launched with 168 a thread (384 x 168 = 64,512 of the SM's 65,536); warps 8-11 give most of their share
+// to the softmax groups: 128 x 96 + 256 x 200 = 63,488.
+constexpr int kTrLaunchRegs = 168, kTrSoftmaxRegs = 200, kTrOtherRegs = 96;
+static_assert(128 * kTrOtherRegs + 256 * kTrSoftmaxRegs <= kTrThreads * kTrLaunchRegs, "the split fits the launch");
+enum TreeForm { SPLIT, PAIR, TURNS };
+template <int N>
+struct IntConstant {
+    static constexpr int value = N;
+};
 constexpr float kTrRescale = 8.f;  // log2
 constexpr float kTrLn2 = 0.6931471805599453f;
 
@@ -44,12 +57,13 @@ struct TrSmem {
     static constexpr int HALVES = D / 64;
     static constexpr uint32_t Q_BYTES = 2 * 128u * 128u * (D > 128 ? 2 : HALVES);  // both buffers (at 256: one of 128 rows or two of 64)
     static constexpr uint32_t STAGE = kTreeKeys * D * 2u;
-    static constexpr int NS = D == 64 ? 20 : D == 128 ? 10 : 4;  // even: a stage holds K tiles or V tiles
+    static constexpr int NS = D == 64 ? 18 : D == 128 ? 8 : 4;  // even: a stage holds K tiles or V tiles
     static_assert(NS % 2 == 0, "each stage has one producer and one reader");
     static constexpr uint32_t HALF = STAGE / HALVES;
     static constexpr uint32_t RING_OFF = Q_BYTES;
     static constexpr uint32_t BAR_OFF = RING_OFF + NS * STAGE;
-    static constexpr uint32_t BYTES = BAR_OFF + 1024;
+    static constexpr uint32_t ML_OFF = BAR_OFF + 1024;  // [2][group][128 rows] maximum and sum (SPLIT)
+    static constexpr uint32_t BYTES = ML_OFF + 2 * 2 * 128 * 8;
 };
 static_assert(1024 + TrSmem<64>::BYTES <= 227 * 1024 && 1024 + TrSmem<128>::BYTES <= 227 * 1024 &&
                   1024 + TrSmem<256>::BYTES <= 227 * 1024,
@@ -64,11 +78,11 @@ struct TreeArgs {
     const TreeNode *nodes;
     const unsigned long long *masks;
     const int32_t *pages;
-    float *part_o;    // [slot][part_rows][D], normalised
+    float4 *part_o;   // [slot][D / 4][part_rows], normalised: a warp's rows lie side by side
     float *part_lse;  // [slot][part_rows], base 2
     TreeHeader *hdr;
     float scale_log2;
-    int window_left, words, num_qo_heads, num_kv_heads, group, page_size, page_shift, num_cache_pages;
+    int batch, window_left, words, num_qo_heads, num_kv_heads, group, page_size, page_shift, num_cache_pages;
     int tile_tokens;  // query tokens of a 128-row tile
     int box_rows, box_new, box_q;
     int q_rows;       // rows of a Q buffer: 128, or 64 at head_dim 256 where two then fit
@@ -79,8 +93,8 @@ struct TreeArgs {
 struct TreePiece {
     TreeRow row;
     int kvh, qt, tile, cnt;
-    int partial;  // slot, -1 = the whole unit
-    int index;    // of the CTA
+    int slot;   // of its partial, -1 = the whole unit
+    int index;  // of the CTA
 };
 
 template <typename F>
@@ -88,22 +102,23 @@ __device__ __forceinline__ void tree_pieces(const TreeArgs &a, const TreeStart &
     TreePiece p;
     p.row = s.row;
     p.index = 0;
-    int r = s.r, unit = s.unit, tile = s.tile, left = s.left;
-    const bool cut = tile > 0;
-    while (left > 0) {
-        const int units = p.row.nq * a.num_kv_heads;
-        if (unit >= units) {
-            p.row = a.rows[++r];
+    int r = s.r, unit = s.unit, tile = s.tile;
+    while (r < s.r_end || (r == s.r_end && (unit < s.unit_end || (unit == s.unit_end && tile < s.tile_end)))) {
+        const int tiles = p.row.nq > s.q0 ? (p.row.nq - s.q0 + s.qi - 1) / s.qi : 0;  // query tiles of this lane
+        if (unit >= a.num_kv_heads / s.hi * tiles) {
+            ++r;
             unit = 0;
+            if (r < a.batch) p.row = a.rows[r];
             continue;
         }
-        p.kvh = unit / p.row.nq;
-        p.qt = unit % p.row.nq;
+        const bool cut = r == s.r_end && unit == s.unit_end;  // the next CTA goes on with it
+        p.kvh = unit / tiles * s.hi + s.h0;
+        p.qt = s.q0 + unit % tiles * s.qi;
         p.tile = tile;
-        p.cnt = min(left, p.row.nt - tile);
-        p.partial = p.index == 0 && cut ? 2 * (int)blockIdx.x : tile + p.cnt < p.row.nt ? 2 * (int)blockIdx.x + 1 : -1;
+        p.cnt = (cut ? s.tile_end : p.row.nt) - tile;
+        // a unit that began in another CTA, or goes on in the next one
+        p.slot = tile > 0 ? 2 * (int)blockIdx.x : cut ? 2 * (int)blockIdx.x + 1 : -1;
         if (!piece(p)) return;
-        left -= p.cnt;
         tile = 0;
         ++unit;
         ++p.index;
@@ -181,13 +196,14 @@ __device__ __noinline__ void tree_pv_rows(uint32_t o_addr, uint32_t p_addr, cons
     tmem_wait_st();
 }
 
-template <int D, bool PAIR>
+template <int D, TreeForm FORM>
 __global__ void __launch_bounds__(kTrThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q, const TreeArgs a) {
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                const __grid_constant__ TreeArgs a) {
     using L = TrSmem<D>;
     constexpr int HALVES = L::HALVES, NS = L::NS;
-    constexpr bool ONE_O = D > 128;  // both groups' accumulators are the same columns
+    constexpr int PART_ROWS = FORM == PAIR ? 256 : 128;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR_OFF);
@@ -198,12 +214,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     uint64_t *s_full = bars + 4;    // [group][buffer]
     uint64_t *p_full = bars + 8;    // [group][buffer] P written (and O rescaled if it had to be)
     uint64_t *pv_done = bars + 12;  // [group][buffer] PV completed: the buffer may be overwritten
-    uint64_t *o_final = bars + 16;  // [group] the piece's last PV completed
-    uint64_t *o_free = bars + 18;   // [group] the piece's O has been read
+    uint64_t *o_final = bars + 16;  // [group] the piece's last PV completed (SPLIT: of both groups, the first)
+    uint64_t *o_free = bars + 18;   // [group] the piece's O has been read (SPLIT: by both groups, the first)
     uint64_t *checked = bars + 20;  // [group] a special tile's V has been looked over
-    uint64_t *kv_full = bars + 22;           // [NS]
-    uint64_t *kv_empty = bars + 22 + NS;     // [NS]
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 22 + 2 * NS);
+    uint64_t *joint = bars + 22;    // SPLIT: both groups' maxima and sums of a piece are in shared memory
+    uint64_t *kv_full = bars + 23;           // [NS]
+    uint64_t *kv_empty = bars + 23 + NS;     // [NS]
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 23 + 2 * NS);
     uint32_t *by_rows = tmem_holder + 1;     // [group] that tile's PV goes by rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -218,9 +235,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 mbar_init(&pv_done[2 * x + b], 1);
             }
             mbar_init(&o_final[x], 1);
-            mbar_init(&o_free[x], 4);
+            mbar_init(&o_free[x], FORM == SPLIT ? 8 : 4);
             mbar_init(&checked[x], 1);
         }
+        mbar_init(joint, 8);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&kv_full[s], 1);
             mbar_init(&kv_empty[s], 1);
@@ -243,15 +261,22 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     const uint32_t tmem = *tmem_holder;
     const TreeStart start = a.starts[blockIdx.x];
     auto S_col = [tmem](int x, int b) { return tmem + 128u * (uint32_t)x + 64u * (uint32_t)b; };
-    auto O_col = [tmem](int x) { return tmem + 256u + (ONE_O ? 0u : (uint32_t)(D * x)); };
-    const int unit_tokens = a.tile_tokens * (PAIR ? 2 : 1);
+    auto O_col = [tmem](int x) { return tmem + 256u + (FORM == TURNS ? 0u : (uint32_t)(D * x)); };
+    const int unit_tokens = a.tile_tokens * (FORM == PAIR ? 2 : 1);
     const bool two_q = a.q_rows == 64 || D <= 128;  // Q buffers: one at head_dim 256 with 128 rows
     const uint32_t q_half = (uint32_t)a.q_rows * 128u, q_buf = q_half * HALVES;
     // PAIR: the unit's tokens reach into the second query tile
-    auto second = [&](const TreePiece &p) { return PAIR && p.row.n - p.qt * unit_tokens > a.tile_tokens; };
-    auto q_slot = [&](const TreePiece &p) { return PAIR || !two_q ? 0 : p.index & 1; };
-    auto q_phase = [&](const TreePiece &p) { return (uint32_t)(PAIR || !two_q ? p.index : p.index >> 1); };
+    auto second = [&](const TreePiece &p) { return FORM == PAIR && p.row.n - p.qt * unit_tokens > a.tile_tokens; };
+    // whether group x has a part in tile j of a piece
+    auto takes = [&](const TreePiece &p, int x, int j) {
+        return FORM == SPLIT ? (j & 1) == x : FORM == TURNS ? (p.index & 1) == x : x == 0 || second(p);
+    };
+    auto q_slot = [&](const TreePiece &p) { return FORM == PAIR || !two_q ? 0 : p.index & 1; };
+    auto q_phase = [&](const TreePiece &p) { return (uint32_t)(FORM == PAIR || !two_q ? p.index : p.index >> 1); };
 
+    // each group of four warps changes its register share at the top of its own branch
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTrOtherRegs));
     if (warp == 8 || warp == 11) {
         // ------------------------------------------------ copies: warp 8 Q and K, warp 11 V
         const int kv = warp == 11;
@@ -269,7 +294,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(tiles * HALVES * a.box_q * a.group) * 128u);
                 __syncwarp();
                 if (lane < tiles * HALVES)
-                    tma_load_3d(sm + (PAIR ? lane / HALVES : qs) * q_buf + lane % HALVES * q_half, &tm_q, &q_full[qs],
+                    tma_load_3d(sm + (FORM == PAIR ? lane / HALVES : qs) * q_buf + lane % HALVES * q_half, &tm_q, &q_full[qs],
                                 lane % HALVES * 64, p.kvh * a.group,
                                 p.row.q_begin + p.qt * unit_tokens + lane / HALVES * a.tile_tokens);
             }
@@ -324,20 +349,20 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         uint32_t i = 0, done[2] = {0, 0};  // tiles of each group
         bool ok = true;
         tree_pieces(a, start, [&](const TreePiece &p) {
-            const int qs = q_slot(p), x0 = PAIR ? 0 : p.index & 1, x1 = PAIR ? (second(p) ? 2 : 1) : x0 + 1;
+            const int qs = q_slot(p);
             ok = mbar_wait(&q_full[qs], q_phase(p) & 1, err, kErrWaitFull);
             for (int j = 0; j < p.cnt && ok; ++j, i += 2) {
                 const int s = i % NS;
                 ok = mbar_wait(&kv_full[s], (i / NS) & 1, err, kErrWaitFull);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (x < x0 || x >= x1 || !ok) continue;
+                    if (!takes(p, x, j) || !ok) continue;
                     const uint32_t it = done[x], b = it & 1;
                     // S overwrites P of two tiles before, which that tile's PV reads
                     if (it >= 2) ok = mbar_wait(&pv_done[2 * x + b], ((it >> 1) - 1) & 1, err, kErrWaitFull);
                     if (!ok) continue;
                     tc_fence_after();
-                    const uint64_t q = add(dQ, (PAIR ? x : qs) * q_buf), k = add(dK, s * L::STAGE);
+                    const uint64_t q = add(dQ, (FORM == PAIR ? x : qs) * q_buf), k = add(dK, s * L::STAGE);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         mma_ss_elect(S_col(x, b), add(q, (kk / 4) * q_half + (kk % 4) * 32),
@@ -352,21 +377,24 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         });
         if (!ok)  // a wait gave up: let the MMAs in flight finish before the tensor memory is released
             for (uint32_t d = 0; d < 1024; ++d) __nanosleep(1000);
-    } else if (warp == 10) {
-        // ------------------------------------------------ O += P V
+    } else {
+        // ------------------------------------------------ warp 10: O += P V
         constexpr uint32_t ID_O = idesc_bf16_f32(128, D, 0, 1);
         auto add = [](uint64_t d, uint32_t off) { return d + (off >> 4); };
         const uint64_t dV = smem_desc(smem_u32(sm + L::RING_OFF), L::HALF, 1024, kSwizzle128B);
         uint32_t i = 1, done[2] = {0, 0}, pieces[2] = {0, 0};
         bool ok = true;
         tree_pieces(a, start, [&](const TreePiece &p) {
-            const int x0 = PAIR ? 0 : p.index & 1, x1 = PAIR ? (second(p) ? 2 : 1) : x0 + 1;
             // O may be overwritten once what it held has been read
+            if (FORM == SPLIT) {
+                if (p.index > 0) ok = mbar_wait(&o_free[0], (p.index - 1) & 1, err, kErrWaitEmpty);
+            } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x < x0 || x >= x1 || !ok) continue;
-                const int y = ONE_O ? 1 - x : x;
-                if (pieces[y] > 0) ok = mbar_wait(&o_free[y], (pieces[y] - 1) & 1, err, kErrWaitEmpty);
+                for (int x = 0; x < 2; ++x) {
+                    if (!takes(p, x, 0) || !ok) continue;
+                    const int y = FORM == TURNS ? 1 - x : x;
+                    if (pieces[y] > 0) ok = mbar_wait(&o_free[y], (pieces[y] - 1) & 1, err, kErrWaitEmpty);
+                }
             }
             for (int j = 0; j < p.cnt && ok; ++j, i += 2) {
                 const int s = i % NS;
@@ -402,7 +430,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     }
                     rows = __any_sync(0xffffffffu, has_nan(f0) || has_nan(f1));
                     if (lane == 0)
-                        for (int x = x0; x < x1; ++x) {
+                        for (int x = 0; x < 2; ++x) {
+                            if (!takes(p, x, j)) continue;
                             by_rows[x] = rows;
                             mbar_arrive(&checked[x]);
                         }
@@ -410,25 +439,26 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (x < x0 || x >= x1 || !ok) continue;
+                    if (!takes(p, x, j) || !ok) continue;
                     const uint32_t it = done[x], b = it & 1;
                     ok = mbar_wait(&p_full[2 * x + b], (it >> 1) & 1, err, kErrWaitFull);
                     if (!ok) continue;
                     tc_fence_after();
                     if (!rows) {
                         const uint64_t v = add(dV, s * L::STAGE);
+                        const uint32_t more = j >= (FORM == SPLIT ? 2 : 1) ? 1u : 0u;  // not the group's first tile
                         if (steps == kTreeKeys / 16) {
 #pragma unroll
                             for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, kk > 0 ? 1u : more);
                         } else {
                             for (int kk = 0; kk < steps; ++kk)
-                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, (j > 0 || kk > 0) ? 1u : 0u);
+                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, kk > 0 ? 1u : more);
                         }
                     }
                     mma_commit_elect(&pv_done[2 * x + b]);
                     if (j == p.cnt - 1) {
-                        mma_commit_elect(&o_final[x]);
+                        mma_commit_elect(&o_final[FORM == SPLIT ? 0 : x]);
                         ++pieces[x];
                     }
                     ++done[x];
@@ -439,7 +469,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         });
         if (!ok)
             for (uint32_t d = 0; d < 1024; ++d) __nanosleep(1000);
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTrSoftmaxRegs));
         // ------------------------------------------------ softmax and epilogue: warps 0-7
         const int x = warp >> 2, m = (warp & 3) * 32 + lane;  // group; query row = lane of tensor memory
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -451,8 +483,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         tree_pieces(a, start, [&](const TreePiece &p) {
             const uint32_t tiles0 = before;
             before += p.cnt;
-            if (PAIR ? (x == 1 && !second(p)) : (p.index & 1) != x) return true;
-            const int tok = p.qt * unit_tokens + (PAIR ? x * a.tile_tokens : 0) + tok_in_tile;
+            if (FORM != SPLIT && !takes(p, x, 0)) return true;
+            const int tok = p.qt * unit_tokens + (FORM == PAIR ? x * a.tile_tokens : 0) + tok_in_tile;
             const bool live = tok_in_tile < a.tile_tokens && tok < p.row.n;
             const bool idle = !__any_sync(0xffffffffu, live);  // the warp has no row of this unit
             const size_t node = (size_t)p.row.q_begin + tok;
@@ -460,7 +492,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             if (live && a.window_left >= 0) lo = max(0, p.row.ctx + a.nodes[node].depth - a.window_left);
             float m_run = -INFINITY, l_run = 0.f;
             bool seen = false;
-            for (int j = 0; j < p.cnt; ++j, ++it) {
+            for (int j = FORM == SPLIT ? x : 0; j < p.cnt; j += FORM == SPLIT ? 2 : 1, ++it) {
+                const bool first = j < (FORM == SPLIT ? 2 : 1);  // the group's first tile of the piece
                 const uint32_t b = it & 1, S = S_col(x, b) + lane_off;
                 const TreeTile k = tree_tile(p.row, p.tile + j, a.window_left);
                 unsigned long long vis = ~0ull;
@@ -542,14 +575,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (!mbar_wait(&checked[x], checks++ & 1, err, kErrWaitFull)) return ok = false;
                     rows = by_rows[x] != 0;
                 }
-                if (rows || (warp_grow && j > 0)) {
-                    // O holds the piece's earlier tiles: wait for the last of those MMAs
-                    if (j > 0 && !mbar_wait(&pv_done[2 * x + (1 - b)], ((it - 1) >> 1) & 1, err, kErrWaitFull)) return ok = false;
+                if (rows || (warp_grow && !first)) {
+                    // O holds the group's earlier tiles: wait for the last of those MMAs
+                    if (!first && !mbar_wait(&pv_done[2 * x + (1 - b)], ((it - 1) >> 1) & 1, err, kErrWaitFull)) return ok = false;
                     tc_fence_after();
                     if (rows) {
                         const uint32_t at = 2 * (tiles0 + j) + 1, s = at % NS;  // V's stage (it has landed: `checked`)
                         if (!mbar_wait(&kv_full[s], (at / NS) & 1, err, kErrWaitFull)) return ok = false;
-                        tree_pv_rows<D>(O, S, sm + L::RING_OFF + s * L::STAGE, vis, alpha, j == 0);
+                        tree_pv_rows<D>(O, S, sm + L::RING_OFF + s * L::STAGE, vis, alpha, first);
                     } else {
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -567,51 +600,76 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
             }
-            // the piece's O
-            if (!mbar_wait(&o_final[x], pieces & 1, err, kErrWaitFull)) return ok = false;
+            // the piece's O = w0 O of group 0 + w1 O of group 1 (SPLIT), or this group's alone, normalised.
+            // A piece may hold no key that a row sees: weight 0, lse -inf.  Keys whose scores are all -inf weigh
+            // nothing against other pieces, but 0 * inf of their values stays; a row that has no others is NaN (0 / 0).
+            float w0 = 1.f, w1 = 0.f;
+            bool seen0 = seen, seen1 = false;
+            if constexpr (FORM == SPLIT) {
+                float2 *const ml = reinterpret_cast<float2 *>(sm + L::ML_OFF) + (pieces & 1) * 256;
+                ml[x * 128 + m] = make_float2(m_run, seen ? l_run : -1.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(joint);
+                if (!mbar_wait(joint, pieces & 1, err, kErrWaitFull)) return ok = false;
+                const float2 e0 = ml[m], e1 = ml[128 + m];
+                seen0 = !(e0.y < 0.f);
+                seen1 = !(e1.y < 0.f);
+                m_run = fmaxf(e0.x, e1.x);
+                const float ref = m_run == -INFINITY ? 0.f : m_run;
+                w0 = !seen0 ? 0.f : m_run == -INFINITY ? 1.f : ex2_ftz(e0.x - ref);
+                w1 = !seen1 ? 0.f : m_run == -INFINITY ? 1.f : ex2_ftz(e1.x - ref);
+                l_run = (seen0 ? w0 * e0.y : 0.f) + (seen1 ? w1 * e1.y : 0.f);
+                seen = seen0 || seen1;
+            }
+            if (!mbar_wait(&o_final[FORM == SPLIT ? 0 : x], pieces & 1, err, kErrWaitFull)) return ok = false;
             ++pieces;
             tc_fence_after();
             if (!idle) {
-                // A piece may hold no key that a row sees: weight 0, lse -inf.  Keys whose scores are all -inf
-                // weigh nothing against other pieces, but 0 * inf of their values stays; a row that has
-                // no others is NaN (0 / 0).
-                const float inv = !seen ? 0.f : l_run == 0.f && p.partial >= 0 ? 1.f : 1.f / l_run;
+                const float inv = !seen ? 0.f : l_run == 0.f && p.slot >= 0 ? 1.f : 1.f / l_run;
                 const float lse2 = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
                 const size_t orow = node * a.num_qo_heads + p.kvh * a.group + head;
-                const size_t prow = (size_t)max(p.partial, 0) * (PAIR ? 256 : 128) + (PAIR ? x * 128 : 0) + m;
+                const int prow = (FORM == PAIR ? x * 128 : 0) + m;
+                w0 *= inv;
+                w1 *= inv;
+                const uint32_t O0 = O_col(FORM == SPLIT ? 0 : x) + lane_off, O1 = O_col(1) + lane_off;
+                const int c_begin = FORM == SPLIT ? x * (D / 2) : 0, c_end = FORM == SPLIT ? c_begin + D / 2 : D;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
+                for (int c0 = c_begin; c0 < c_end; c0 += 32) {
+                    uint32_t o[32], o1[32];
                     __syncwarp();
-                    tmem_ld32(O + c0, o);
+                    tmem_ld32(O0 + c0, o);
+                    if (FORM == SPLIT) tmem_ld32(O1 + c0, o1);
                     tmem_wait_ld();
                     float f[32];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)  // select, not multiply: O may hold NaN of keys the row does not see
-                        f[c] = inv == 0.f ? 0.f : __uint_as_float(o[c]) * inv;
+                    for (int c = 0; c < 32; ++c) {  // select, not multiply: O may hold anything if the row saw no key
+                        f[c] = seen0 ? __uint_as_float(o[c]) * w0 : 0.f;
+                        if (FORM == SPLIT) f[c] = seen1 ? fmaf(__uint_as_float(o1[c]), w1, f[c]) : f[c];
+                    }
                     if (!live) continue;
-                    if (p.partial < 0) {
+                    if (p.slot < 0) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + c0);
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             dst[c] = make_uint4(pack_bf16(f[8 * c], f[8 * c + 1]), pack_bf16(f[8 * c + 2], f[8 * c + 3]),
                                                 pack_bf16(f[8 * c + 4], f[8 * c + 5]), pack_bf16(f[8 * c + 6], f[8 * c + 7]));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D + c0);
+                        float4 *dst = a.part_o + ((size_t)p.slot * (D / 4) + c0 / 4) * PART_ROWS + prow;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) dst[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+                        for (int c = 0; c < 8; ++c)
+                            dst[c * PART_ROWS] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
                     }
                 }
-                if (live) {
-                    if (p.partial >= 0)
-                        a.part_lse[prow] = lse2;
+                if (live && (FORM != SPLIT || x == 0)) {
+                    if (p.slot >= 0)
+                        a.part_lse[(size_t)p.slot * PART_ROWS + prow] = lse2;
                     else if (a.lse)
                         a.lse[orow] = lse2 * kTrLn2;
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[x]);
+            if (lane == 0) mbar_arrive(&o_free[FORM == SPLIT ? 0 : x]);
             return true;
         });
     }
@@ -621,93 +679,136 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Join of the pieces of a cut unit: with w_i = 2^(lse_i - max lse), o = sum w_i o_i / sum w_i.  Column x of the
-// grid looks at the boundary between CTAs x and x + 1, and joins the unit that is cut there first there; a warp
-// per query row, four pieces in flight.
-constexpr int kTrMergeWarps = 8;
-struct TreeMergeArgs {
-    const TreeStart *starts;
-    const float *part_o, *part_lse;
-    __nv_bfloat16 *out;
-    float *lse;
-    int ctas, part_rows, tile_tokens, unit_tokens, group, num_qo_heads;
+// Join of a unit's pieces: with w_i = 2^(lse_i - max lse), o = sum w_i o_i / sum w_i.  Block (b, y) takes 32 rows of
+// the unit that begins in CTA b and goes on in the next ones; a thread has a row (neighbours neighbouring ones)
+// and four vectors of four columns, SETS sets of threads take the pieces in turn.  Bounded by trips to L2 (the plan's
+// record, the partials), so all of a thread's loads are in flight at once: two pieces' where units are cut
+// once or twice, up to four of each set's where few units share many CTAs.  Joining in the CTA that finishes last
+// took longer (wide trees 167 -> 185 us, long chains 42 -> 45): its few warps make those trips one after another.
+template <int D, int SETS>
+struct JoinShape {
+    static constexpr int GROUPS = D / 16;  // of threads with the same columns
+    static constexpr int THREADS = 32 * GROUPS * SETS, BATCH = SETS > 1 || D == 256 ? 4 : 2;
 };
-template <int D>
-__global__ void __launch_bounds__(32 * kTrMergeWarps) tree_merge_kernel(const TreeMergeArgs a) {
-    constexpr int V = D / 64, BATCH = 4;  // float2 a lane and piece
-    const int lane = threadIdx.x & 31, c = blockIdx.x + 1, f = blockIdx.y * kTrMergeWarps + (threadIdx.x >> 5);
+template <int D, int SETS>
+__global__ void __launch_bounds__(JoinShape<D, SETS>::THREADS) tree_join_kernel(const TreeArgs a, int unit_tokens, int part_rows) {
+    using J = JoinShape<D, SETS>;
+    constexpr int COLS = 4, BATCH = J::BATCH, C = D / 4;
+    __shared__ float4 others[SETS > 1 ? (SETS - 1) * C * 32 : 1];
+    __shared__ float2 sums[SETS > 1 ? (SETS - 1) * 32 : 1];
+    const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, set = warp / J::GROUPS;
+    const int c0 = warp % J::GROUPS * COLS, place = blockIdx.y * 32 + lane;
+    // the plan was complete before the attention kernel let this one start
+    const TreeStart &s = a.starts[b];
+    const int r = s.r_end, unit = s.unit_end, count = s.tail_count, tile_end = s.tile_end, lanes = s.hi * s.qi;
+    const bool begins = s.r != r || s.unit != unit || s.tile == 0;  // the unit that goes on begins here
+    if (r >= a.batch || tile_end == 0 || !begins) {
+        griddep_wait();
+        griddep_launch();
+        return;
+    }
+    const TreeRow row = a.rows[r];
+    const int tiles = (row.nq - s.q0 + s.qi - 1) / s.qi, kvh = unit / tiles * s.hi + s.h0, qt = s.q0 + unit % tiles * s.qi;
+    const int rows = min(unit_tokens, row.n - qt * unit_tokens) * a.group, tile_rows = a.tile_tokens * a.group;
+    const int f = (place >> 7) * tile_rows + (place & 127);  // token * group + head within the unit
+    const bool live = (place & 127) < tile_rows && f < rows;
     griddep_wait();
     griddep_launch();
-    const TreeStart s = a.starts[c];
-    if (s.r < 0 || s.tile == 0) return;
-    const int2 before = make_int2(a.starts[c - 1].r, a.starts[c - 1].unit);
-    if (before.x == s.r && before.y == s.unit && a.starts[c - 1].tile > 0) return;
-    const int qt = s.unit % s.row.nq, kvh = s.unit / s.row.nq;
-    const int tokens = min(a.unit_tokens, s.row.n - qt * a.unit_tokens);
-    if (f >= tokens * a.group) return;
-    int count = 1;  // pieces: the last of CTA c - 1, the first of those behind it that begin inside the unit
-    for (int c0 = c; c0 < a.ctas; c0 += 32) {
-        const int y = c0 + lane;
-        const bool in = y < a.ctas && a.starts[y].r == s.r && a.starts[y].unit == s.unit && a.starts[y].tile > 0;
-        const unsigned most = __ballot_sync(0xffffffffu, in);
-        const int n = most == 0xffffffffu ? 32 : __ffs(~most) - 1;
-        count += n;
-        if (n < 32) break;
-    }
-    const int tok = f / a.group, x = tok / a.tile_tokens, m = f - x * a.tile_tokens * a.group;
-    auto row_of = [&](int i) {
-        const int slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1);
-        return (size_t)slot * a.part_rows + x * 128 + m;
-    };
-    float mx = -INFINITY;
-    for (int i = lane; i < count; i += 32) mx = fmaxf(mx, __ldcg(a.part_lse + row_of(i)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float sum = 0.f;
-    float2 acc[V] = {};
-    for (int i0 = 0; i0 < count; i0 += BATCH) {
-        float2 v[BATCH][V];
+    float top = -INFINITY, sum = 0.f;
+    float4 acc[COLS] = {};
+    for (int i0 = set; live && i0 < count; i0 += BATCH * SETS) {
         float l[BATCH];
+        float4 v[BATCH][COLS];
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b)
-            if (i0 + b < count) {
-                const size_t row = row_of(i0 + b);
-                l[b] = __ldcg(a.part_lse + row);
+        for (int i = 0; i < BATCH; ++i) {
+            const int at = i0 + i * SETS;
+            l[i] = -INFINITY;
+            if (at >= count) continue;
+            const size_t slot = at == 0 ? 2 * b + 1 : 2 * (b + at * lanes);
+            l[i] = __ldcg(a.part_lse + slot * part_rows + place);
 #pragma unroll
-                for (int u = 0; u < V; ++u)
-                    v[b][u] = __ldcg(reinterpret_cast<const float2 *>(a.part_o + row * D) + u * 32 + lane);
+            for (int c = 0; c < COLS; ++c) v[i][c] = __ldcg(a.part_o + (slot * C + c0 + c) * part_rows + place);
+        }
+        const float before = top;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) top = fmaxf(top, l[i]);
+        const float ref = top == -INFINITY ? 0.f : top, keep = before == -INFINITY ? 0.f : exp2f(before - ref);
+        sum *= keep;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) acc[c] = make_float4(acc[c].x * keep, acc[c].y * keep, acc[c].z * keep, acc[c].w * keep);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            if (i0 + i * SETS >= count) continue;
+            const float w = exp2f(l[i] - ref);
+            sum += w;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                acc[c].x = fmaf(w, v[i][c].x, acc[c].x);
+                acc[c].y = fmaf(w, v[i][c].y, acc[c].y);
+                acc[c].z = fmaf(w, v[i][c].z, acc[c].z);
+                acc[c].w = fmaf(w, v[i][c].w, acc[c].w);
             }
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b)
-            if (i0 + b < count) {
-                const float w = exp2f(l[b] - mx);
-                sum += w;
-#pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    acc[u].x += w * v[b][u].x;
-                    acc[u].y += w * v[b][u].y;
-                }
-            }
+        }
     }
-    const float inv = 1.f / sum;  // the largest weight is 1 (NaN if every key of the row scores -inf)
-    const size_t orow = ((size_t)s.row.q_begin + qt * a.unit_tokens + tok) * a.num_qo_heads + kvh * a.group + f % a.group;
+    if constexpr (SETS > 1) {
+        if (set > 0) {
+            if (c0 == 0) sums[(set - 1) * 32 + lane] = make_float2(top, sum);
 #pragma unroll
-    for (int u = 0; u < V; ++u)
-        *reinterpret_cast<uint32_t *>(a.out + orow * D + 2 * (u * 32 + lane)) = pack_bf16(acc[u].x * inv, acc[u].y * inv);
-    if (a.lse && lane == 0) a.lse[orow] = (mx == -INFINITY ? mx : mx + log2f(sum)) * kTrLn2;
+            for (int c = 0; c < COLS; ++c) others[((set - 1) * C + c0 + c) * 32 + lane] = acc[c];
+        }
+        __syncthreads();
+        if (set > 0 || !live) return;
+        float all = top;
+#pragma unroll
+        for (int i = 1; i < SETS; ++i) all = fmaxf(all, sums[(i - 1) * 32 + lane].x);
+        const float ref = all == -INFINITY ? 0.f : all, own = exp2f(top - ref);
+        sum *= own;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) acc[c] = make_float4(acc[c].x * own, acc[c].y * own, acc[c].z * own, acc[c].w * own);
+#pragma unroll
+        for (int i = 1; i < SETS; ++i) {
+            if (i >= count) break;  // (a set without pieces)
+            const float2 e = sums[(i - 1) * 32 + lane];
+            const float w = exp2f(e.x - ref);
+            sum = fmaf(w, e.y, sum);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                const float4 v = others[((i - 1) * C + c0 + c) * 32 + lane];
+                acc[c].x = fmaf(w, v.x, acc[c].x);
+                acc[c].y = fmaf(w, v.y, acc[c].y);
+                acc[c].z = fmaf(w, v.z, acc[c].z);
+                acc[c].w = fmaf(w, v.w, acc[c].w);
+            }
+        }
+        top = all;
+    }
+    if (!live) return;
+    const float inv = 1.f / sum;  // (0 / 0 if every key of the row scores -inf)
+    const size_t out_row = ((size_t)row.q_begin + qt * unit_tokens + f / a.group) * a.num_qo_heads + kvh * a.group + f % a.group;
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + 4 * c0);
+#pragma unroll
+    for (int c = 0; c < COLS; c += 2)
+        dst[c / 2] = make_uint4(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv),
+                                pack_bf16(acc[c + 1].x * inv, acc[c + 1].y * inv), pack_bf16(acc[c + 1].z * inv, acc[c + 1].w * inv));
+    if (a.lse && c0 == 0) a.lse[out_row] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kTrLn2;
 }
 
-template <int D, bool PAIR>
-static cudaError_t launch(const TreeArgs &a, const TreeMergeArgs &m, int rows, const CUtensorMap &tm_kv,
-                          const CUtensorMap &tm_k, const CUtensorMap &tm_v, const CUtensorMap &tm_q, cudaStream_t st) {
+// `units`: at most so many in the step; `rows`: at most so many of a unit.
+template <int D, TreeForm FORM>
+static cudaError_t launch(const TreeArgs &a, int ctas, long long units, int rows, const CUtensorMap &tm_kv, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                          const CUtensorMap &tm_q, cudaStream_t st) {
     const size_t smem = 1024 + TrSmem<D>::BYTES;
-    cudaError_t e = set_smem_limit((const void *)tree_kernel<D, PAIR>, smem, st);
-    if (e == cudaSuccess)
-        e = launch_pdl(tree_kernel<D, PAIR>, dim3(m.ctas), dim3(kTrThreads), smem, st, tm_kv, tm_k, tm_v, tm_q, a);
-    if (e == cudaSuccess && m.ctas > 1)
-        e = launch_pdl(tree_merge_kernel<D>, dim3(m.ctas - 1, (rows + kTrMergeWarps - 1) / kTrMergeWarps),
-                       dim3(32 * kTrMergeWarps), 0, st, m);
-    return e;
+    cudaError_t e = set_smem_limit((const void *)tree_kernel<D, FORM>, smem, st);
+    if (e == cudaSuccess) e = launch_pdl(tree_kernel<D, FORM>, dim3(ctas), dim3(kTrThreads), smem, st, tm_kv, tm_k, tm_v, tm_q, a);
+    if (e != cudaSuccess || ctas == 1) return e;
+    constexpr int UNIT_TILES = FORM == PAIR ? 2 : 1;
+    const int unit_tokens = a.tile_tokens * UNIT_TILES, part_rows = 128 * UNIT_TILES;
+    const dim3 grid(ctas, rows > a.tile_tokens * a.group ? 8 : (rows + 31) / 32);
+    // units of many pieces: where there are fewer units than half the CTAs
+    constexpr int SETS = D == 256 ? 1 : 256 / D;
+    if (SETS > 1 && 2 * units <= ctas)
+        return launch_pdl(tree_join_kernel<D, SETS>, grid, dim3(JoinShape<D, SETS>::THREADS), 0, st, a, unit_tokens, part_rows);
+    return launch_pdl(tree_join_kernel<D, 1>, grid, dim3(JoinShape<D, 1>::THREADS), 0, st, a, unit_tokens, part_rows);
 }
 
 }  // namespace dev
@@ -724,10 +825,11 @@ cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm
     a.nodes = reinterpret_cast<const TreeNode *>(w + p.off_nodes);
     a.masks = reinterpret_cast<const unsigned long long *>(w + p.off_masks);
     a.pages = p.pages;
-    a.part_o = reinterpret_cast<float *>(w + p.off_part_o);
+    a.part_o = reinterpret_cast<float4 *>(w + p.off_part_o);
     a.part_lse = reinterpret_cast<float *>(w + p.off_part_lse);
     a.hdr = reinterpret_cast<TreeHeader *>(w);
     a.scale_log2 = p.scale_log2;
+    a.batch = p.batch;
     a.window_left = p.window_left;
     a.words = p.words;
     a.num_qo_heads = s.num_qo_heads;
@@ -743,16 +845,15 @@ cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm
     a.q_rows = s.head_dim == 256 && box_q * a.group <= 64 ? 64 : 128;
     a.oob_row = s.num_cache_pages * 2 * s.page_size;
     const int unit_tokens = a.tile_tokens * (p.pair ? 2 : 1);
-    const dev::TreeMergeArgs m{a.starts, a.part_o, a.part_lse, a.out, lse, s.sm_count, p.part_rows, a.tile_tokens, unit_tokens,
-                               a.group, s.num_qo_heads};
     const int rows = (p.max_new < unit_tokens ? p.max_new : unit_tokens) * a.group;
+    const long long units = (long long)p.batch * s.num_kv_heads * ((p.max_new + unit_tokens - 1) / unit_tokens);
     if (s.head_dim == 64)
-        return p.pair ? dev::launch<64, true>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st)
-                      : dev::launch<64, false>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st);
+        return p.pair ? dev::launch<64, dev::PAIR>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<64, dev::SPLIT>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
     if (s.head_dim == 128)
-        return p.pair ? dev::launch<128, true>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st)
-                      : dev::launch<128, false>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st);
-    return dev::launch<256, false>(a, m, rows, tm_kv, tm_k, tm_v, tm_q, st);
+        return p.pair ? dev::launch<128, dev::PAIR>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<128, dev::SPLIT>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
+    return dev::launch<256, dev::TURNS>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
 }
 
 }  // namespace pkv

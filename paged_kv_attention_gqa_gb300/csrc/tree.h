@@ -39,15 +39,19 @@ struct alignas(16) TreeRow {
 };
 static_assert(sizeof(TreeRow) == 32, "TreeRow is 8 ints");
 
-// Where a CTA begins: `left` tiles from tile `tile` of unit `unit` of the row, on through its units (kv
-// heads, query tiles inner) and the rows behind it.
+// What a CTA does: the tiles from (r, unit, tile) up to (r_end, unit_end, tile_end).  CTA b is in lane b % (hi * qi)
+// of the grid; a lane's units of a row are the kv heads h0, h0 + hi, .. (outer) with the query tiles q0, q0 + qi, ..
+// Lanes run side by side, so that CTAs that read the same pages (other heads, other query tiles) do so at the
+// same time.
 struct alignas(16) TreeStart {
-    TreeRow row;
-    int32_t r, unit, tile, left;  // r = -1: nothing to do
-    long long first;              // tiles before it in the step
-    long long pad;
+    TreeRow row;  // row r
+    int32_t r, unit, tile;
+    int32_t r_end, unit_end, tile_end;
+    int32_t h0, hi, q0, qi;
+    int32_t tail_count;  // pieces of the unit (r_end, unit_end), hi * qi CTAs apart, if it begins in this CTA
+    int32_t pad;
 };
-static_assert(sizeof(TreeStart) == 64, "TreeStart is 64 bytes");
+static_assert(sizeof(TreeStart) == 80, "TreeStart is 80 bytes");
 
 struct TreeNode {
     int32_t parent, depth;
@@ -60,7 +64,7 @@ struct TreePlan {
     bool pair = false;                     // two query tiles of 128 rows per unit
     int part_rows = 0;                     // rows of a partial
     const int32_t *pages = nullptr;        // the caller's page list (device)
-    size_t off_rows = 0, off_starts = 0, off_nodes = 0, off_masks = 0, off_cost = 0, off_units = 0, off_part_o = 0,
+    size_t off_rows = 0, off_starts = 0, off_nodes = 0, off_masks = 0, off_cost = 0, off_part_o = 0,
            off_part_lse = 0, total = 0;
 };
 

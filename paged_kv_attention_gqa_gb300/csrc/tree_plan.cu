@@ -1,9 +1,9 @@
 // The plan of a speculative step, made on the device (pkv_plan_tree), and the acceptance of a path
 // (pkv_run_accept).
 //
-// Plan.  Block 0 reads the rows' index arrays and gives every attention CTA an equal share of the step's
-// key tiles (a piece of a unit costs two tiles beside its own): prefix sums over the rows, then the place
-// of each CTA's first tile by bisection.  The other blocks take a row per warp and walk each node's parents
+// Plan.  Block 0 reads the rows' index arrays and gives every attention CTA of a lane (see TreeStart) an equal
+// share of the lane's key tiles (a piece of a unit costs two tiles beside its own): prefix sums over the
+// rows, then the place of each CTA's first tile by bisection.  The other blocks take a row per warp and walk each node's parents
 // to its root: depth, and a bit for every ancestor.
 //
 // Accept.  A CTA per row and a few layers.  One warp walks from the root to the first child whose token is the
@@ -39,8 +39,7 @@ void tree_layout(const Shape &s, int batch, int tokens, int max_new, TreePlan &p
     p.off_starts = put(at, (size_t)s.sm_count * sizeof(TreeStart));
     p.off_nodes = put(at, (size_t)tokens * sizeof(TreeNode));
     p.off_masks = put(at, (size_t)tokens * p.words * 8);
-    p.off_cost = put(at, (size_t)(batch + 1) * 8);
-    p.off_units = put(at, (size_t)(batch + 1) * 8);
+    p.off_cost = put(at, (size_t)batch * 16);
     p.off_part_o = put(at, (size_t)2 * s.sm_count * p.part_rows * s.head_dim * 4);
     p.off_part_lse = put(at, (size_t)2 * s.sm_count * p.part_rows * 4);
     p.total = at;
@@ -51,12 +50,13 @@ namespace dev {
 struct TreePlanArgs {
     TreeIndex x;
     int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, ctas;
+    int hi1, hi2;  // heads side by side: with all query tiles in turn, with two classes of them side by side
     TreeHeader *hdr;
     TreeRow *rows;
     TreeStart *starts;
     TreeNode *nodes;
     unsigned long long *masks;
-    long long *cost, *units;
+    longlong2 *cost;  // before row r: of its even query tiles, of the odd ones, one kv head each
 };
 
 // The row's numbers if its index arrays agree (n = 0 and ctx = -1 if not).
@@ -135,80 +135,94 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         return;
     }
     // ------------------------------------------------ the rows, and each CTA's share
-    long long cost_before = 0, units_before = 0;
+    longlong2 before = make_longlong2(0, 0);
     for (int r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
         const int r = r0 + threadIdx.x;
-        long long cost = 0, units = 0;
+        longlong2 v = make_longlong2(0, 0);
         if (r < a.batch) {
             bool ok;
             const TreeRow t = tree_row(a, r, ok);
             if (!ok) atomicCAS(&a.hdr->err, 0, kErrTreeRow);
             a.rows[r] = t;
-            units = (long long)t.nq * a.kv_heads;
-            cost = units * (t.nt + kTreePieceCost);
+            const long long each = t.nt + kTreePieceCost;
+            v = make_longlong2((t.nq + 1) / 2 * each, t.nq / 2 * each);
         }
-        long long c = cost, u = units;
+        longlong2 c = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, c, o), y = __shfl_up_sync(0xffffffffu, u, o);
+            const long long x = __shfl_up_sync(0xffffffffu, c.x, o), y = __shfl_up_sync(0xffffffffu, c.y, o);
             if (lane >= o) {
-                c += x;
-                u += y;
+                c.x += x;
+                c.y += y;
             }
         }
         if (lane == 31) {
-            sums[0][warp] = c;
-            sums[1][warp] = u;
+            sums[0][warp] = c.x;
+            sums[1][warp] = c.y;
         }
         __syncthreads();
-        long long cw = 0, uw = 0, ct = 0, ut = 0;
+        longlong2 mine = before;
         for (int w = 0; w < kPlanWarps; ++w) {
             if (w < warp) {
-                cw += sums[0][w];
-                uw += sums[1][w];
+                mine.x += sums[0][w];
+                mine.y += sums[1][w];
             }
-            ct += sums[0][w];
-            ut += sums[1][w];
+            before.x += sums[0][w];
+            before.y += sums[1][w];
         }
         __syncthreads();
-        if (r < a.batch) {
-            a.cost[r] = cost_before + cw + c - cost;
-            a.units[r] = units_before + uw + u - units;
-        }
-        cost_before += ct;
-        units_before += ut;
+        if (r < a.batch) a.cost[r] = make_longlong2(mine.x + c.x - v.x, mine.y + c.y - v.y);
     }
     __syncthreads();
-    const long long total = cost_before, tiles = total - kTreePieceCost * units_before;
-    const long long share = max((total + a.ctas - 1) / a.ctas, (long long)kTreeLeastCost);
+    // Two query tiles of a row side by side read its keys once (L2 keeps them); that wants as many odd tiles as even
+    // ones, or the lanes of the odd ones would idle
+    const int qi = a.hi2 > 0 && before.y * 16 >= before.x * 15 ? 2 : 1, hi = qi == 2 ? a.hi2 : a.hi1;
+    const int lanes = hi * qi, slices = a.ctas / lanes, heads = a.kv_heads / hi;
     for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
         TreeStart s = {};
-        const long long at = c * share;
-        s.r = -1;
-        s.first = tiles;
-        if (at < total) {
-            int lo = 0, hi = a.batch - 1;  // the last row that begins at or before `at`
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.cost[mid] <= at)
+        const int slice = c / lanes;
+        s.h0 = c % lanes % hi;
+        s.hi = hi;
+        s.q0 = c % lanes / hi;
+        s.qi = qi;
+        auto part = [&](const longlong2 &v) { return heads * (qi == 1 ? v.x + v.y : s.q0 ? v.y : v.x); };
+        const long long total = part(before), share = max((total + slices - 1) / slices, (long long)kTreeLeastCost);
+        struct Place {
+            int r, unit, tile;
+            long long first, last;  // the slices with the unit's first and last piece
+        };
+        auto place = [&](long long at) {
+            Place p = {a.batch, 0, 0, 0, 0};
+            if (at >= total) return p;
+            int lo = 0, hi_row = a.batch - 1;  // the last row that begins at or before `at`
+            while (lo < hi_row) {
+                const int mid = (lo + hi_row + 1) >> 1;
+                if (part(a.cost[mid]) <= at)
                     lo = mid;
                 else
-                    hi = mid - 1;
+                    hi_row = mid - 1;
             }
-            s.r = lo;
-            s.row = a.rows[lo];
-            const long long off = at - a.cost[lo];
-            const int each = s.row.nt + kTreePieceCost;
-            s.unit = (int)(off / each);
-            s.tile = max(0, (int)(off % each) - kTreePieceCost);
-            s.first = a.cost[lo] - kTreePieceCost * a.units[lo] + (long long)s.unit * s.row.nt + s.tile;
-        }
+            p.r = lo;
+            const long long off = at - part(a.cost[lo]);
+            const int each = a.rows[lo].nt + kTreePieceCost;
+            p.unit = (int)(off / each);
+            p.tile = max(0, (int)(off % each) - kTreePieceCost);
+            const long long begin = at - off % each;  // a CTA begins inside the unit if past its first two
+            p.first = (begin + kTreePieceCost) / share;
+            p.last = (begin + each - 1) / share;
+            return p;
+        };
+        const bool used = slice < slices;
+        const Place from = place(used ? slice * share : total), to = place(used ? (slice + 1) * share : total);
+        s.r = from.r;
+        s.unit = from.unit;
+        s.tile = from.tile;
+        if (from.r < a.batch) s.row = a.rows[from.r];
+        s.r_end = to.r;
+        s.unit_end = to.unit;
+        s.tile_end = to.tile;
+        s.tail_count = (int)(to.last - to.first) + 1;
         a.starts[c] = s;
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
-        const long long next = c + 1 < a.ctas ? a.starts[c + 1].first : tiles;
-        a.starts[c].left = (int)(next - a.starts[c].first);
     }
 }
 
@@ -323,8 +337,18 @@ cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex 
     a.starts = reinterpret_cast<TreeStart *>(w + p.off_starts);
     a.nodes = reinterpret_cast<TreeNode *>(w + p.off_nodes);
     a.masks = reinterpret_cast<unsigned long long *>(w + p.off_masks);
-    a.cost = reinterpret_cast<long long *>(w + p.off_cost);
-    a.units = reinterpret_cast<long long *>(w + p.off_units);
+    a.cost = reinterpret_cast<longlong2 *>(w + p.off_cost);
+    // as many heads side by side as leave no more than a 32nd of the CTAs without work
+    auto heads_beside = [&](int classes) {
+        for (int h = s.num_kv_heads; h > 0; --h)
+            if (s.num_kv_heads % h == 0) {
+                const int lanes = h * classes, idle = s.sm_count % lanes;
+                if (lanes <= s.sm_count && idle * 32 <= s.sm_count) return h;
+            }
+        return 0;
+    };
+    a.hi1 = heads_beside(1);  // (1 always does)
+    a.hi2 = heads_beside(2);
     return launch_pdl(dev::tree_plan_kernel, dim3(1 + (p.batch + dev::kPlanWarps - 1) / dev::kPlanWarps),
                       dim3(dev::kPlanThreads), 0, st, a);
 }
