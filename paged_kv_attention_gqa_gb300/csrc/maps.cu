@@ -7,7 +7,7 @@
 //     n + sum(back) - 1 - (T_r + b - held_r),
 // and everything follows from prefix sums over the rows.  Every CTA makes these sums for itself in shared
 // memory, which costs less than a second launch or a barrier over the grid; the outputs (page list, slots,
-// positions) are then cut evenly over the CTAs, and a thread finds its row by bisection.
+// positions) are then cut evenly over the CTAs, and a warp finds its first row by bisection.
 // The pages held and the free count may be updated in place: a CTA could then overwrite what another has yet to
 // read, so in that case a second kernel writes them.
 // Latency-bound: a chain of loads (lengths, offsets, table) and the stores.
@@ -100,7 +100,9 @@ __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int
         __syncthreads();
     }
     int status = bad;
-    if (!status && (before.fresh > a.token_capacity || before.need > a.indices_capacity)) status = kMapBadSize;
+    constexpr long long MOST = INT32_MAX - 4096;  // 32-bit steps past the last entry
+    if (!status && (before.fresh > min((long long)a.token_capacity, MOST) || before.need > min((long long)a.indices_capacity, MOST)))
+        status = kMapBadSize;
     if (!status && (F < 0 || F > a.free_capacity || F + before.back > a.free_capacity)) status = kMapBadStack;
     if (!status && before.taken > F + before.back) status = (int)min(before.taken - F - before.back, (long long)INT32_MAX);
     const int T = status ? 0 : (int)before.fresh, pages = status ? 0 : (int)before.need;
@@ -113,33 +115,71 @@ __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int
     }
     __syncthreads();
 
-    auto given_back = [&](int q) {  // page number q of those given back
+    auto given_back_at = [&](int q) -> const int32_t * {  // where page number q of those given back stands
         const int r = map_row(m.back, R, q);
-        return a.table[r * a.table_stride + (m.kvp[r + 1] - m.kvp[r]) + (q - m.back[r])];
+        return a.table + r * a.table_stride + (m.kvp[r + 1] - m.kvp[r]) + (q - m.back[r]);
     };
-    auto page_of = [&](int r, int b) {  // block b of row r
-        if (b < m.held[r]) return a.table[r * a.table_stride + b];
+    // where the id of block b of row r stands
+    auto page_at = [&](int r, int b) -> const int32_t * {
+        if (b < m.held[r]) return a.table + r * a.table_stride + b;
         const int at = F + back - 1 - (m.taken[r] + b - m.held[r]);
-        return at < F ? a.free_pages[at] : given_back(at - F);
+        return at < F ? a.free_pages + at : given_back_at(at - F);
     };
     const int id = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
-    for (int e = id; e < pages; e += step) {
-        const int r = map_row(m.kvp, R, e), b = e - m.kvp[r], page = page_of(r, b);
-        a.kvi[e] = page;
-        if (b >= m.held[r]) a.table[r * a.table_stride + b] = page;
-    }
-    for (int q = id; q < back; q += step) a.free_pages[F + q] = given_back(q);
-    if (a.slots || a.positions)
-        for (int t = id; t < a.token_capacity; t += step) {
-            int pos = 0, slot = -1;
-            if (t < T) {
-                const int r = map_row(m.qo, R, t);
-                pos = m.seq[r] + t - m.qo[r];
-                if (a.slots) slot = (page_of(r, pos >> a.page_shift) << a.page_shift) + (pos & (P - 1));
+    // A warp takes a run of entries, a thread every 32nd of it: their rows follow from the first one's.  Four page
+    // ids are in flight a thread.  The warps are shared out between pages and tokens, so that neither waits
+    // for the other
+    constexpr int BATCH = 4;
+    const int warps = gridDim.x * kMapWarps, my_warp = warp * gridDim.x + blockIdx.x, tokens = a.slots || a.positions ? T : 0;
+    const int page_warps = tokens ? max(1, min(warps - 1, (int)((long long)warps * pages / ((long long)pages + tokens)))) : warps;
+    auto entries = [&](int total, int w, int of, const int32_t *off, auto &&source, auto &&store) {
+        if (w < 0 || w >= of) return;
+        const int per = (int)(((long long)total + of - 1) / of + 31) & ~31;
+        const long long begin = (long long)w * per;
+        if (begin >= total) return;
+        const int end = (int)min((long long)total, begin + per);
+        int r = map_row(off, R, (int)begin);
+        for (int e0 = (int)begin + lane; e0 < end; e0 += 32 * BATCH) {
+            const int32_t *from[BATCH];
+            int row[BATCH], page[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int e = e0 + 32 * i;
+                from[i] = nullptr;
+                if (e >= end) continue;
+                while (off[r + 1] <= e) ++r;
+                row[i] = r;
+                from[i] = source(r, e);
             }
-            if (a.slots) a.slots[t] = slot;
-            if (a.positions) a.positions[t] = pos;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) page[i] = from[i] ? *from[i] : -1;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (e0 + 32 * i < end) store(row[i], e0 + 32 * i, page[i]);
         }
+    };
+    entries(
+        pages, my_warp, page_warps, m.kvp, [&](int r, int e) { return page_at(r, e - m.kvp[r]); },
+        [&](int r, int e, int page) {
+            a.kvi[e] = page;
+            const int b = e - m.kvp[r];
+            if (b >= m.held[r]) a.table[r * a.table_stride + b] = page;
+        });
+    for (int q = id; q < back; q += step) a.free_pages[F + q] = *given_back_at(q);
+    if (a.slots || a.positions) {
+        auto position = [&](int r, int t) { return m.seq[r] + t - m.qo[r]; };
+        entries(
+            T, my_warp - page_warps, warps - page_warps, m.qo, [&](int r, int t) { return a.slots ? page_at(r, position(r, t) >> a.page_shift) : nullptr; },
+            [&](int r, int t, int page) {
+                const int pos = position(r, t);
+                if (a.slots) a.slots[t] = (page << a.page_shift) + (pos & (P - 1));
+                if (a.positions) a.positions[t] = pos;
+            });
+        for (int t = T + id; t < a.token_capacity; t += step) {
+            if (a.slots) a.slots[t] = -1;
+            if (a.positions) a.positions[t] = 0;
+        }
+    }
     for (int r = id; r <= R; r += step) {
         a.qo[r] = status ? 0 : m.qo[r];
         a.kvp[r] = status ? 0 : m.kvp[r];
@@ -189,9 +229,9 @@ cudaError_t launch_maps(const MapsArgs &a, cudaStream_t st) {
     const size_t smem = (size_t)6 * (a.rows + 1) * 4;
     cudaError_t e = set_smem_limit((const void *)dev::maps_kernel, (size_t)6 * (kMapsMaxRows + 1) * 4, st);
     if (e != cudaSuccess) return e;
-    // four entries a thread, or as many CTAs as fit the GPU
+    // an entry a thread, or as many CTAs as fit the GPU
     const long long work = (long long)a.indices_capacity + (a.slots || a.positions ? a.token_capacity : 0);
-    const int ctas = (int)std::min<long long>(304, 1 + work / (4 * dev::kMapThreads));
+    const int ctas = (int)std::min<long long>(304, 1 + work / dev::kMapThreads);
     const bool in_place = a.held_out == a.held || a.free_count_out == a.free_count;
     e = launch_pdl(dev::maps_kernel, dim3(ctas), dim3(dev::kMapThreads), smem, st, a, in_place ? 0 : 1);
     if (e == cudaSuccess && in_place) e = launch_pdl(dev::maps_counts_kernel, dim3(1), dim3(dev::kMapThreads), 0, st, a);

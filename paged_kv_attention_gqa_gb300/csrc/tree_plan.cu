@@ -6,10 +6,12 @@
 // rows, then the place of each CTA's first tile by bisection.  The other blocks take a row per warp and walk each node's parents
 // to its root: depth, and a bit for every ancestor.
 //
-// Accept.  A CTA per row and a few layers.  One warp walks from the root to the first child whose token is the
-// model's choice, then all threads copy the path's keys and values to the row's next slots.  The walk
-// is a chain of shared-memory reads and every CTA of the row repeats it: it costs less than a launch that
-// would pass its result on.  HBM-bound for batches (each accepted vector read and written once).
+// Accept.  A CTA per row and a few layers, a thread per node.  A node goes on from its parent if it is the first
+// child whose token is the model's choice there; it is on the path if all nodes above it go on, up to
+// the root, which doubling the parents' pointers tells in log2(depth) rounds; its place is its depth.
+// Every CTA of the row does this for itself, which costs less than a launch that would pass it on.  Then all threads
+// copy the path's keys and values to the row's next slots.  HBM-bound for batches (each accepted vector read
+// and written once), a chain of loads for one row.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -235,78 +237,93 @@ struct AcceptArgs {
     int layers_per_cta, page_size, page_shift, vecs, num_cache_pages;  // vecs: 16-byte vectors of a token's K (or V)
 };
 
-constexpr int kAcceptThreads = 256;
+constexpr int kAcceptThreads = 256, kAcceptCtas = 4;  // CTAs an SM
+
+static_assert(kAcceptThreads == kTreeMaxNew, "a thread a node");
 
 template <typename Token>
-__global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const AcceptArgs a) {
-    __shared__ int32_t parent[kTreeMaxNew], path[kTreeMaxNew];
+__global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kernel(const AcceptArgs a) {
     __shared__ Token draft[kTreeMaxNew], target[kTreeMaxNew];
-    __shared__ long long slot[kTreeMaxNew];  // the cache row of K of path node i, -1 = its page is not one
-    __shared__ int found;
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    __shared__ int32_t first[kTreeMaxNew], path[kTreeMaxNew];
+    __shared__ int2 above[kTreeMaxNew];      // a node above it (-1: none) and whether all below that go on
+    __shared__ long long slot[kTreeMaxNew];  // the cache row of K of the row's token ctx + i, -1 = its page is not one
+    const int r = blockIdx.x, tid = threadIdx.x;
     griddep_wait();
     griddep_launch();
     const TreeRow t = a.rows[r];
-    const Token *const d = static_cast<const Token *>(a.x.draft), *const g = static_cast<const Token *>(a.x.target);
-    for (int i = tid; i < t.n; i += kAcceptThreads) {
-        parent[i] = a.nodes[t.q_begin + i].parent;
-        draft[i] = d[t.q_begin + i];
-        target[i] = g[t.q_begin + i];
+    const bool node = tid < t.n;
+    TreeNode self = {-1, 0};
+    if (node) {
+        const int pos = t.ctx + tid, page = a.pages[t.kv_base + (pos >> a.page_shift)];
+        self = a.nodes[t.q_begin + tid];
+        draft[tid] = static_cast<const Token *>(a.x.draft)[t.q_begin + tid];
+        target[tid] = static_cast<const Token *>(a.x.target)[t.q_begin + tid];
+        first[tid] = kTreeMaxNew;
+        slot[tid] = (unsigned)page < (unsigned)a.num_cache_pages ? (long long)page * 2 * a.page_size + (pos & (a.page_size - 1)) : -1;
     }
     __syncthreads();
-    if (tid < 32) {
-        int at = 0, len = 0;
-        while (t.n > 0) {
-            if (lane == 0) path[len] = at;
-            ++len;
-            int next = -1;
-            for (int i0 = (at + 1) & ~31; i0 < t.n && next < 0; i0 += 32) {  // children come behind their parent
-                const int i = i0 + lane;
-                const unsigned hit = __ballot_sync(0xffffffffu, i < t.n && parent[i] == at && draft[i] == target[at]);
-                if (hit) next = i0 + __ffs(hit) - 1;
-            }
-            if (next < 0) break;
-            at = next;
+    const bool agrees = node && self.parent >= 0 && draft[tid] == target[self.parent];
+    if (agrees) atomicMin(&first[self.parent], tid);
+    __syncthreads();
+    int up = node ? self.parent : -1;
+    bool on = tid == 0 || (agrees && first[self.parent] == tid);
+    while (__syncthreads_or(up >= 0)) {
+        above[tid] = make_int2(up, on);
+        __syncthreads();
+        if (up >= 0) {
+            const int2 e = above[up];
+            up = e.x;
+            on = on && e.y;
         }
-        if (lane == 0) found = len;
     }
-    __syncthreads();
-    const int len = found;
-    for (int i = tid; i < len; i += kAcceptThreads) {
-        const int pos = t.ctx + i, page = a.pages[t.kv_base + (pos >> a.page_shift)];
-        const bool fine = (unsigned)page < (unsigned)a.num_cache_pages;
-        if (!fine) atomicCAS(&a.hdr->err, 0, kErrTreePage);
-        slot[i] = fine ? (long long)page * 2 * a.page_size + (pos & (a.page_size - 1)) : -1;
-    }
+    on = on && node;
+    if (on) path[self.depth] = tid;
+    const int len = __syncthreads_count(on);
     if (blockIdx.y == 0) {
-        for (int i = tid; i < t.n; i += kAcceptThreads) a.x.accepted[t.q_begin + i] = i < len ? path[i] : -1;
+        if (node) a.x.accepted[t.q_begin + tid] = tid < len ? path[tid] : -1;
+        if (tid < len && slot[tid] < 0) atomicCAS(&a.hdr->err, 0, kErrTreePage);
         if (tid == 0) {
             a.x.count[r] = len;
             static_cast<Token *>(a.x.next)[r] = len ? target[path[len - 1]] : Token(-1);
             if (a.x.seq && len) a.x.seq[r] = t.ctx + len;
         }
     }
-    __syncthreads();
-    const int l0 = blockIdx.y * a.layers_per_cta, l1 = min(a.x.layers, l0 + a.layers_per_cta);
-    // vectors (layer, path node, K or V, column): four in flight a thread
-    const int per_layer = len * 2 * a.vecs, work = (l1 - l0) * per_layer;
-    constexpr int BATCH = 4;
-    for (int e0 = tid; e0 < work; e0 += BATCH * kAcceptThreads) {
+    // A vector is K's or V's 16 bytes of a path node in a layer.  The threads take whole nodes, several at a time where
+    // one has fewer vectors than there are threads, and keep their columns; eight vectors are in flight a thread
+    const int l0 = blockIdx.y * a.layers_per_cta, layers = min(a.x.layers - l0, a.layers_per_cta), each = 2 * a.vecs;
+    const int width = min(each, kAcceptThreads), beside = kAcceptThreads / width, c0 = tid % width;
+    int layer = 0, i = tid / width, c = c0;
+    if (len == 0 || i >= beside) return;
+    auto settle = [&] {
+        while (i >= len) {
+            i -= len;
+            ++layer;
+        }
+    };
+    settle();
+    constexpr int BATCH = 8;
+    while (layer < layers) {
         uint4 v[BATCH];
         uint4 *to[BATCH];
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            const int e = e0 + b * kAcceptThreads;
             to[b] = nullptr;
-            if (e >= work) continue;
-            const int layer = e / per_layer, f = e % per_layer, i = f / (2 * a.vecs), kv = f % (2 * a.vecs) >= a.vecs;
-            const int c = f % a.vecs;
-            const long long l = l0 + layer, token = t.q_begin + path[i];
-            const uint4 *from = kv ? static_cast<const uint4 *>(a.x.v) + (l * a.x.v_layer + token * a.x.v_token) / 8 + c
-                                   : static_cast<const uint4 *>(a.x.k) + (l * a.x.k_layer + token * a.x.k_token) / 8 + c;
-            if (slot[i] < 0) continue;
-            v[b] = *from;
-            to[b] = static_cast<uint4 *>(a.x.cache) + l * (a.x.cache_layer / 8) + (slot[i] + (kv ? a.page_size : 0)) * a.vecs + c;
+            if (layer >= layers) continue;
+            const bool is_v = c >= a.vecs;
+            const int col = is_v ? c - a.vecs : c;
+            const long long l = l0 + layer, token = t.q_begin + path[i], at = slot[i];
+            const uint4 *from = is_v ? static_cast<const uint4 *>(a.x.v) + (l * a.x.v_layer + token * a.x.v_token) / 8
+                                     : static_cast<const uint4 *>(a.x.k) + (l * a.x.k_layer + token * a.x.k_token) / 8;
+            if (at >= 0) {
+                v[b] = __ldcs(from + col);
+                to[b] = static_cast<uint4 *>(a.x.cache) + l * (a.x.cache_layer / 8) + (at + (is_v ? a.page_size : 0)) * a.vecs + col;
+            }
+            c += width;
+            if (c >= each) {
+                c = c0;
+                i += beside;
+                settle();
+            }
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b)
@@ -366,10 +383,9 @@ cudaError_t launch_tree_accept(const Shape &s, const TreePlan &p, const TreeAcce
     a.page_shift = s.page_shift();
     a.vecs = s.num_kv_heads * s.head_dim / 8;
     a.num_cache_pages = s.num_cache_pages;
-    // a layer a CTA while the rows do not fill the GPU with eight CTAs an SM
-    const int most = std::max(1, 8 * s.sm_count / p.batch), chunks = std::max(1, std::min(x.layers, most));
+    // a layer a CTA, more where the rows' CTAs would not all run at once
+    const int most = std::max(1, dev::kAcceptCtas * s.sm_count / p.batch), chunks = std::max(1, std::min(x.layers, most));
     a.layers_per_cta = std::max(1, (x.layers + chunks - 1) / chunks);
-    a.layers_per_cta = std::min<int>(a.layers_per_cta, std::max(1, (1 << 29) / (kTreeMaxNew * 2 * a.vecs)));  // 32-bit counts
     const dim3 grid(p.batch, std::max(1, (x.layers + a.layers_per_cta - 1) / a.layers_per_cta));
     return x.wide ? launch_pdl(dev::tree_accept_kernel<long long>, grid, dim3(dev::kAcceptThreads), 0, st, a)
                   : launch_pdl(dev::tree_accept_kernel<int>, grid, dim3(dev::kAcceptThreads), 0, st, a);
