@@ -25,11 +25,25 @@ namespace dev {
 constexpr int kMapThreads = 512, kMapWarps = kMapThreads / 32;
 constexpr int kMapBadRow = -1, kMapBadSize = -2, kMapBadStack = -3;
 
+// Sums over rows: 64-bit where the largest table could overflow 32 (see launch_maps).
+template <typename Int>
 struct MapSums {
-    long long fresh, need, back, taken;
+    Int fresh, need, back, taken;
 };
-__device__ __forceinline__ MapSums operator+(const MapSums &a, const MapSums &b) {
-    return MapSums{a.fresh + b.fresh, a.need + b.need, a.back + b.back, a.taken + b.taken};
+template <typename Int>
+__device__ __forceinline__ MapSums<Int> operator+(const MapSums<Int> &a, const MapSums<Int> &b) {
+    return MapSums<Int>{a.fresh + b.fresh, a.need + b.need, a.back + b.back, a.taken + b.taken};
+}
+// The sums of this lane and those before it.
+template <typename Int>
+__device__ __forceinline__ MapSums<Int> scan(MapSums<Int> s, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const MapSums<Int> u{__shfl_up_sync(0xffffffffu, s.fresh, o), __shfl_up_sync(0xffffffffu, s.need, o),
+                             __shfl_up_sync(0xffffffffu, s.back, o), __shfl_up_sync(0xffffffffu, s.taken, o)};
+        if (lane >= o) s = s + u;
+    }
+    return s;
 }
 
 // In shared memory: for row r, offsets of its new tokens, pages, pages given back and pages taken, and its length.
@@ -50,9 +64,11 @@ __device__ __forceinline__ int map_row(const int32_t *off, int rows, int at) {
     return lo;
 }
 
+template <typename Int>
 __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int own_counts) {
+    using Sums = MapSums<Int>;
     extern __shared__ __align__(16) int32_t map_raw[];
-    __shared__ MapSums warp_sums[kMapWarps];
+    __shared__ Sums warp_sums[kMapWarps + 1];  // of the warps before each, and of all
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = a.rows;
     const MapRows m{map_raw, map_raw + R + 1, map_raw + 2 * (R + 1), map_raw + 3 * (R + 1), map_raw + 4 * (R + 1),
@@ -62,49 +78,46 @@ __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int
     griddep_launch();
     __syncthreads();
     const int P = 1 << a.page_shift, F = *a.free_count;
-    MapSums before = {0, 0, 0, 0};
+    Sums before = {0, 0, 0, 0};
     for (int r0 = 0; r0 < R; r0 += kMapThreads) {
         const int r = r0 + tid;
-        MapSums v = {0, 0, 0, 0};
+        Sums v = {0, 0, 0, 0};
         if (r < R) {
             const int seq = a.seq[r], fresh = a.fresh[r], held = a.held[r];
             const long long need = ((long long)seq + fresh + P - 1) >> a.page_shift;
             if (seq < 0 || fresh < 0 || held < 0 || held > a.max_blocks || need > a.max_blocks || (long long)seq + fresh > INT32_MAX)
                 bad = kMapBadRow;
             else
-                v = MapSums{fresh, need, need < held ? held - need : 0, need > held ? need - held : 0};
+                v = Sums{fresh, (Int)need, (Int)(need < held ? held - need : 0), (Int)(need > held ? need - held : 0)};
             m.seq[r] = seq;
             m.held[r] = held;
         }
-        MapSums s = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const MapSums u{__shfl_up_sync(0xffffffffu, s.fresh, o), __shfl_up_sync(0xffffffffu, s.need, o),
-                            __shfl_up_sync(0xffffffffu, s.back, o), __shfl_up_sync(0xffffffffu, s.taken, o)};
-            if (lane >= o) s = s + u;
-        }
+        const Sums s = scan(v, lane);
         if (lane == 31) warp_sums[warp] = s;
         __syncthreads();
-        MapSums mine = before, all = before;
-        for (int w = 0; w < kMapWarps; ++w) {
-            if (w < warp) mine = mine + warp_sums[w];
-            all = all + warp_sums[w];
+        if (warp == 0) {
+            const Sums w = lane < kMapWarps ? warp_sums[lane] : Sums{0, 0, 0, 0}, t = scan(w, lane);
+            __syncwarp();
+            if (lane < kMapWarps) warp_sums[lane] = Sums{t.fresh - w.fresh, t.need - w.need, t.back - w.back, t.taken - w.taken};
+            if (lane == 31) warp_sums[kMapWarps] = t;
         }
+        __syncthreads();
+        const Sums mine = before + warp_sums[warp];
         if (r < R) {
             m.qo[r] = (int)(mine.fresh + s.fresh - v.fresh);
             m.kvp[r] = (int)(mine.need + s.need - v.need);
             m.back[r] = (int)(mine.back + s.back - v.back);
             m.taken[r] = (int)(mine.taken + s.taken - v.taken);
         }
-        before = all;
+        before = before + warp_sums[kMapWarps];
         __syncthreads();
     }
     int status = bad;
     constexpr long long MOST = INT32_MAX - 4096;  // 32-bit steps past the last entry
     if (!status && (before.fresh > min((long long)a.token_capacity, MOST) || before.need > min((long long)a.indices_capacity, MOST)))
         status = kMapBadSize;
-    if (!status && (F < 0 || F > a.free_capacity || F + before.back > a.free_capacity)) status = kMapBadStack;
-    if (!status && before.taken > F + before.back) status = (int)min(before.taken - F - before.back, (long long)INT32_MAX);
+    if (!status && (F < 0 || F > a.free_capacity || (long long)F + before.back > a.free_capacity)) status = kMapBadStack;
+    if (!status && before.taken > (long long)F + before.back) status = (int)min((long long)before.taken - F - before.back, (long long)INT32_MAX);
     const int T = status ? 0 : (int)before.fresh, pages = status ? 0 : (int)before.need;
     const int back = status ? 0 : (int)before.back, taken = status ? 0 : (int)before.taken;
     if (tid == 0) {
@@ -119,59 +132,68 @@ __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int
         const int r = map_row(m.back, R, q);
         return a.table + r * a.table_stride + (m.kvp[r + 1] - m.kvp[r]) + (q - m.back[r]);
     };
-    // where the id of block b of row r stands
-    auto page_at = [&](int r, int b) -> const int32_t * {
-        if (b < m.held[r]) return a.table + r * a.table_stride + b;
-        const int at = F + back - 1 - (m.taken[r] + b - m.held[r]);
-        return at < F ? a.free_pages + at : given_back_at(at - F);
-    };
     const int id = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
     // A warp takes a run of entries, a thread every 32nd of it: their rows follow from the first one's.  Four page
     // ids are in flight a thread.  The warps are shared out between pages and tokens, so that neither waits
     // for the other
     constexpr int BATCH = 4;
     const int warps = gridDim.x * kMapWarps, my_warp = warp * gridDim.x + blockIdx.x, tokens = a.slots || a.positions ? T : 0;
-    const int page_warps = tokens ? max(1, min(warps - 1, (int)((long long)warps * pages / ((long long)pages + tokens)))) : warps;
-    auto entries = [&](int total, int w, int of, const int32_t *off, auto &&source, auto &&store) {
+    // a token counts for as many as 32 of them have rows: a warp goes from row to row
+    const long long weight = tokens ? min(8, 1 + (int)(32ll * R / tokens)) : 0;
+    const int page_warps = tokens ? max(1, min(warps - 1, (int)(warps * (long long)pages / (pages + weight * tokens)))) : warps;
+    struct Row {  // the row of the current entry
+        int r, begin, end, held, above;  // above: number on the stack of its first missing block
+        const int32_t *table;
+    };
+    auto entries = [&](int total, int w, int of, const int32_t *off, auto &&block, auto &&store) {
         if (w < 0 || w >= of) return;
         const int per = (int)(((long long)total + of - 1) / of + 31) & ~31;
-        const long long begin = (long long)w * per;
-        if (begin >= total) return;
-        const int end = (int)min((long long)total, begin + per);
-        int r = map_row(off, R, (int)begin);
-        for (int e0 = (int)begin + lane; e0 < end; e0 += 32 * BATCH) {
-            const int32_t *from[BATCH];
-            int row[BATCH], page[BATCH];
+        const long long first = (long long)w * per;
+        if (first >= total) return;
+        const int end = (int)min((long long)total, first + per);
+        Row row;
+        auto enter = [&](int r) {
+            row.r = r;
+            row.begin = off[r];
+            row.end = off[r + 1];
+            row.held = m.held[r];
+            row.above = F + back - 1 - m.taken[r];
+            row.table = a.table + r * a.table_stride;
+        };
+        enter(map_row(off, R, (int)first));
+        for (int e0 = (int)first + lane; e0 < end; e0 += 32 * BATCH) {
+            int page[BATCH];
+            Row at[BATCH];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int e = e0 + 32 * i;
-                from[i] = nullptr;
                 if (e >= end) continue;
-                while (off[r + 1] <= e) ++r;
-                row[i] = r;
-                from[i] = source(r, e);
+                while (row.end <= e) enter(row.r + 1);
+                at[i] = row;
+                const int b = block(row, e);
+                const int up = row.above - (b - row.held);  // its number on the stack if it is missing
+                page[i] = b < 0 ? -1 : b < row.held ? row.table[b] : up < F ? a.free_pages[up] : *given_back_at(up - F);
             }
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) page[i] = from[i] ? *from[i] : -1;
-#pragma unroll
             for (int i = 0; i < BATCH; ++i)
-                if (e0 + 32 * i < end) store(row[i], e0 + 32 * i, page[i]);
+                if (e0 + 32 * i < end) store(at[i], e0 + 32 * i, page[i]);
         }
     };
     entries(
-        pages, my_warp, page_warps, m.kvp, [&](int r, int e) { return page_at(r, e - m.kvp[r]); },
-        [&](int r, int e, int page) {
+        pages, my_warp, page_warps, m.kvp, [&](const Row &row, int e) { return e - row.begin; },
+        [&](const Row &row, int e, int page) {
             a.kvi[e] = page;
-            const int b = e - m.kvp[r];
-            if (b >= m.held[r]) a.table[r * a.table_stride + b] = page;
+            const int b = e - row.begin;
+            if (b >= row.held) a.table[row.r * a.table_stride + b] = page;
         });
     for (int q = id; q < back; q += step) a.free_pages[F + q] = *given_back_at(q);
     if (a.slots || a.positions) {
-        auto position = [&](int r, int t) { return m.seq[r] + t - m.qo[r]; };
+        auto position = [&](const Row &row, int t) { return m.seq[row.r] + t - row.begin; };
         entries(
-            T, my_warp - page_warps, warps - page_warps, m.qo, [&](int r, int t) { return a.slots ? page_at(r, position(r, t) >> a.page_shift) : nullptr; },
-            [&](int r, int t, int page) {
-                const int pos = position(r, t);
+            T, my_warp - page_warps, warps - page_warps, m.qo,
+            [&](const Row &row, int t) { return a.slots ? position(row, t) >> a.page_shift : -1; },
+            [&](const Row &row, int t, int page) {
+                const int pos = position(row, t);
                 if (a.slots) a.slots[t] = (page << a.page_shift) + (pos & (P - 1));
                 if (a.positions) a.positions[t] = pos;
             });
@@ -227,13 +249,17 @@ __global__ void __launch_bounds__(kMapThreads) maps_counts_kernel(const MapsArgs
 
 cudaError_t launch_maps(const MapsArgs &a, cudaStream_t st) {
     const size_t smem = (size_t)6 * (a.rows + 1) * 4;
-    cudaError_t e = set_smem_limit((const void *)dev::maps_kernel, (size_t)6 * (kMapsMaxRows + 1) * 4, st);
-    if (e != cudaSuccess) return e;
     // an entry a thread, or as many CTAs as fit the GPU
     const long long work = (long long)a.indices_capacity + (a.slots || a.positions ? a.token_capacity : 0);
     const int ctas = (int)std::min<long long>(304, 1 + work / dev::kMapThreads);
     const bool in_place = a.held_out == a.held || a.free_count_out == a.free_count;
-    e = launch_pdl(dev::maps_kernel, dim3(ctas), dim3(dev::kMapThreads), smem, st, a, in_place ? 0 : 1);
+    auto launch = [&](auto kernel) {
+        const cudaError_t e = set_smem_limit((const void *)kernel, (size_t)6 * (kMapsMaxRows + 1) * 4, st);
+        return e != cudaSuccess ? e : launch_pdl(kernel, dim3(ctas), dim3(dev::kMapThreads), smem, st, a, in_place ? 0 : 1);
+    };
+    // no sum is above the tokens that full tables hold
+    const bool wide = ((long long)a.rows * a.max_blocks >> (30 - a.page_shift)) > 0;
+    cudaError_t e = wide ? launch(dev::maps_kernel<long long>) : launch(dev::maps_kernel<int>);
     if (e == cudaSuccess && in_place) e = launch_pdl(dev::maps_counts_kernel, dim3(1), dim3(dev::kMapThreads), 0, st, a);
     return e;
 }

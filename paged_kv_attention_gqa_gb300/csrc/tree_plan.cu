@@ -9,9 +9,10 @@
 // Accept.  A CTA per row and a few layers, a thread per node.  A node goes on from its parent if it is the first
 // child whose token is the model's choice there; it is on the path if all nodes above it go on, up to
 // the root, which doubling the parents' pointers tells in log2(depth) rounds; its place is its depth.
-// Every CTA of the row does this for itself, which costs less than a launch that would pass it on.  Then all threads
-// copy the path's keys and values to the row's next slots.  HBM-bound for batches (each accepted vector read
-// and written once), a chain of loads for one row.
+// Every CTA of the row does this for itself, which costs less than a launch that would pass it on.  Then bulk copies
+// take the path's keys and values to the row's next slots (copies by all threads, 16 bytes each, were bound by the
+// instructions of their addresses).  HBM-bound for batches (each accepted vector read and written once), a
+// chain of loads for one row.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -234,20 +235,27 @@ struct AcceptArgs {
     const TreeNode *nodes;
     const int32_t *pages;
     TreeHeader *hdr;
+    int lanes;  // with a buffer, of each warp
     int layers_per_cta, page_size, page_shift, vecs, num_cache_pages;  // vecs: 16-byte vectors of a token's K (or V)
 };
 
-constexpr int kAcceptThreads = 256, kAcceptCtas = 4;  // CTAs an SM
+constexpr int kAcceptThreads = 256, kAcceptWarps = kAcceptThreads / 32, kAcceptBuffer = 2048;
+constexpr int kAcceptBytes = 65536;  // of buffers
+constexpr int kAcceptCtas = 3;  // an SM
 
 static_assert(kAcceptThreads == kTreeMaxNew, "a thread a node");
 
 template <typename Token>
 __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kernel(const AcceptArgs a) {
+    extern __shared__ __align__(128) uint8_t buffers[];
+    __shared__ uint64_t bars[kAcceptThreads];
     __shared__ Token draft[kTreeMaxNew], target[kTreeMaxNew];
     __shared__ int32_t first[kTreeMaxNew], path[kTreeMaxNew];
     __shared__ int2 above[kTreeMaxNew];      // a node above it (-1: none) and whether all below that go on
     __shared__ long long slot[kTreeMaxNew];  // the cache row of K of the row's token ctx + i, -1 = its page is not one
-    const int r = blockIdx.x, tid = threadIdx.x;
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (lane < a.lanes) mbar_init(&bars[warp * a.lanes + lane], 1);
+    fence_barrier_init();
     griddep_wait();
     griddep_launch();
     const TreeRow t = a.rows[r];
@@ -288,47 +296,29 @@ __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kerne
             if (a.x.seq && len) a.x.seq[r] = t.ctx + len;
         }
     }
-    // A vector is K's or V's 16 bytes of a path node in a layer.  The threads take whole nodes, several at a time where
-    // one has fewer vectors than there are threads, and keep their columns; eight vectors are in flight a thread
-    const int l0 = blockIdx.y * a.layers_per_cta, layers = min(a.x.layers - l0, a.layers_per_cta), each = 2 * a.vecs;
-    const int width = min(each, kAcceptThreads), beside = kAcceptThreads / width, c0 = tid % width;
-    int layer = 0, i = tid / width, c = c0;
-    if (len == 0 || i >= beside) return;
-    auto settle = [&] {
-        while (i >= len) {
-            i -= len;
-            ++layer;
-        }
-    };
-    settle();
-    constexpr int BATCH = 8;
-    while (layer < layers) {
-        uint4 v[BATCH];
-        uint4 *to[BATCH];
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            to[b] = nullptr;
-            if (layer >= layers) continue;
-            const bool is_v = c >= a.vecs;
-            const int col = is_v ? c - a.vecs : c;
-            const long long l = l0 + layer, token = t.q_begin + path[i], at = slot[i];
-            const uint4 *from = is_v ? static_cast<const uint4 *>(a.x.v) + (l * a.x.v_layer + token * a.x.v_token) / 8
-                                     : static_cast<const uint4 *>(a.x.k) + (l * a.x.k_layer + token * a.x.k_token) / 8;
-            if (at >= 0) {
-                v[b] = __ldcs(from + col);
-                to[b] = static_cast<uint4 *>(a.x.cache) + l * (a.x.cache_layer / 8) + (at + (is_v ? a.page_size : 0)) * a.vecs + col;
-            }
-            c += width;
-            if (c >= each) {
-                c = c0;
-                i += beside;
-                settle();
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b)
-            if (to[b]) *to[b] = v[b];
+    // A copy is up to 2 KB of K or V of a path node in a layer, through a buffer in shared memory of its lane: four lanes of
+    // each warp have one, more where they are smaller
+    if (lane >= a.lanes) return;
+    const int l0 = blockIdx.y * a.layers_per_cta, layers = min(a.x.layers - l0, a.layers_per_cta);
+    const int bytes = a.vecs * 16, parts = (bytes + kAcceptBuffer - 1) / kAcceptBuffer, each = 2 * parts;
+    const int mine = warp * a.lanes + lane;
+    uint8_t *const buffer = buffers + mine * (kAcceptBytes / (kAcceptWarps * a.lanes));
+    uint64_t *const bar = bars + mine;
+    uint32_t phase = 0;
+    for (int q = mine; q < layers * len * each; q += kAcceptWarps * a.lanes) {
+        const int part = q % parts, v = q / parts & 1, item = q / each, i = item % len;
+        const long long l = l0 + item / len, token = t.q_begin + path[i], at = slot[i];
+        if (at < 0) continue;
+        const int begin = part * kAcceptBuffer, size = min(kAcceptBuffer, bytes - begin);
+        const long long from = v ? l * a.x.v_layer + token * a.x.v_token : l * a.x.k_layer + token * a.x.k_token;  // elements
+        const long long to = l * a.x.cache_layer + (at + (v ? a.page_size : 0)) * a.vecs * 8;
+        if (phase) bulk_store_wait_read();  // the buffer's last store
+        mbar_arrive_expect_tx(bar, size);
+        bulk_load(buffer, static_cast<const uint8_t *>(v ? a.x.v : a.x.k) + from * 2 + begin, size, bar);
+        if (!mbar_wait(bar, phase++ & 1, &a.hdr->err, kErrWaitFull)) break;
+        bulk_store(static_cast<uint8_t *>(a.x.cache) + to * 2 + begin, buffer, size);
     }
+    bulk_store_wait();
 }
 
 }  // namespace dev
@@ -386,9 +376,18 @@ cudaError_t launch_tree_accept(const Shape &s, const TreePlan &p, const TreeAcce
     // a layer a CTA, more where the rows' CTAs would not all run at once
     const int most = std::max(1, dev::kAcceptCtas * s.sm_count / p.batch), chunks = std::max(1, std::min(x.layers, most));
     a.layers_per_cta = std::max(1, (x.layers + chunks - 1) / chunks);
+    a.lanes = 4;
+    while (a.lanes < 32 && a.vecs * 16 * 2 * a.lanes <= dev::kAcceptBytes / dev::kAcceptWarps) a.lanes *= 2;
+    // the copies of a CTA are counted in 32 bits
+    const int parts = (a.vecs * 16 + dev::kAcceptBuffer - 1) / dev::kAcceptBuffer;
+    a.layers_per_cta = std::min(a.layers_per_cta, std::max(1, (1 << 30) / (kTreeMaxNew * 2 * parts)));
     const dim3 grid(p.batch, std::max(1, (x.layers + a.layers_per_cta - 1) / a.layers_per_cta));
-    return x.wide ? launch_pdl(dev::tree_accept_kernel<long long>, grid, dim3(dev::kAcceptThreads), 0, st, a)
-                  : launch_pdl(dev::tree_accept_kernel<int>, grid, dim3(dev::kAcceptThreads), 0, st, a);
+    const size_t smem = dev::kAcceptBytes;
+    auto launch = [&](auto kernel) {
+        const cudaError_t e = set_smem_limit((const void *)kernel, smem, st);
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(dev::kAcceptThreads), smem, st, a);
+    };
+    return x.wide ? launch(dev::tree_accept_kernel<long long>) : launch(dev::tree_accept_kernel<int>);
 }
 
 }  // namespace pkv
