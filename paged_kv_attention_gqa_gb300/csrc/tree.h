@@ -14,9 +14,11 @@ namespace pkv {
 constexpr int kTreeKeys = 64;        // keys of one tile
 constexpr int kTreeMaxNew = 256;     // most drafted tokens of a row
 constexpr int kTreeMinPage = 8;      // a TMA box fills whole 8-row swizzle atoms
-constexpr int kTreePieceCost = 2;    // what a piece costs beside its tiles, in tiles
-constexpr int kTreeLeastCost = 6;    // least share of a CTA
-static_assert(kTreeLeastCost > kTreePieceCost, "the CTAs' first tiles are all different");
+// What the plan shares out, in thirds of a tile: a tile with two query tiles, or the only one, 3; a pair's unit
+// that reaches into one of its query tiles alone 2 a tile (it is bound by its copies, the others by the MMAs too);
+// a piece as much as two tiles beside its own; and a CTA takes no less than four tiles' worth.
+constexpr int kTreeTileCost = 3, kTreeHalfCost = 2, kTreePieceCost = 6, kTreeLeastCost = 12;
+static_assert(kTreeLeastCost > kTreePieceCost + kTreeTileCost, "the CTAs' first tiles are all different");
 constexpr int kMapsMaxRows = 8192;   // rows whose offsets fit the shared memory of the maps kernel
 
 // Device error words of the speculative step (beside those of the bounded waits in ptx.cuh).

@@ -52,14 +52,14 @@ namespace dev {
 
 struct TreePlanArgs {
     TreeIndex x;
-    int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, ctas;
+    int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, tile_tokens, ctas;
     int hi1, hi2;  // heads side by side: with all query tiles in turn, with two classes of them side by side
     TreeHeader *hdr;
     TreeRow *rows;
     TreeStart *starts;
     TreeNode *nodes;
     unsigned long long *masks;
-    longlong2 *cost;  // before row r: of its even query tiles, of the odd ones, one kv head each
+    longlong2 *cost;  // before row r: of the even query units, of the odd ones, one kv head each
 };
 
 // The row's numbers if its index arrays agree (n = 0 and ctx = -1 if not).
@@ -88,6 +88,16 @@ __device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, bool &
     t.nt = t.nc + (t.n + kTreeKeys - 1) / kTreeKeys;
     t.nq = (t.n + a.unit_tokens - 1) / a.unit_tokens;
     return t;
+}
+
+// The cost of a tile of query unit q of a row, and of the row's units q0, q0 + qi, .. of one kv head.
+__device__ __forceinline__ int tile_cost(const TreePlanArgs &a, const TreeRow &t, int q) {
+    return t.n - q * a.unit_tokens <= a.tile_tokens && a.unit_tokens > a.tile_tokens ? kTreeHalfCost : kTreeTileCost;
+}
+__device__ __forceinline__ long long head_cost(const TreePlanArgs &a, const TreeRow &t, int q0, int qi) {
+    if (t.nq <= q0) return 0;
+    const int units = (t.nq - q0 + qi - 1) / qi, last = q0 + (units - 1) * qi;  // only the last may be a half
+    return (long long)(units - 1) * (t.nt * kTreeTileCost + kTreePieceCost) + (long long)t.nt * tile_cost(a, t, last) + kTreePieceCost;
 }
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
@@ -147,8 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
             const TreeRow t = tree_row(a, r, ok);
             if (!ok) atomicCAS(&a.hdr->err, 0, kErrTreeRow);
             a.rows[r] = t;
-            const long long each = t.nt + kTreePieceCost;
-            v = make_longlong2((t.nq + 1) / 2 * each, t.nq / 2 * each);
+            v = make_longlong2(head_cost(a, t, 0, 2), head_cost(a, t, 1, 2));
         }
         longlong2 c = v;
 #pragma unroll
@@ -206,13 +215,17 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
                     hi_row = mid - 1;
             }
             p.r = lo;
-            const long long off = at - part(a.cost[lo]);
-            const int each = a.rows[lo].nt + kTreePieceCost;
-            p.unit = (int)(off / each);
-            p.tile = max(0, (int)(off % each) - kTreePieceCost);
-            const long long begin = at - off % each;  // a CTA begins inside the unit if past its first two
-            p.first = (begin + kTreePieceCost) / share;
-            p.last = (begin + each - 1) / share;
+            const TreeRow t = a.rows[lo];
+            const long long off = at - part(a.cost[lo]), head = head_cost(a, t, s.q0, qi);
+            const long long full = (long long)t.nt * kTreeTileCost + kTreePieceCost;
+            const int units = (t.nq - s.q0 + qi - 1) / qi, q = (int)min((long long)units - 1, off % head / full);
+            const int each = tile_cost(a, t, s.q0 + q * qi);
+            const long long inside = off % head - q * full, begin = at - inside;
+            p.unit = (int)(off / head) * units + q;
+            p.tile = (int)(max(0ll, inside - kTreePieceCost) / each);  // (below nt: inside is below the unit's cost)
+            // a CTA begins inside the unit if it is past the unit's own cost and first tile
+            p.first = (begin + kTreePieceCost + each - 1) / share;
+            p.last = (begin + kTreePieceCost + (long long)t.nt * each - 1) / share;
             return p;
         };
         const bool used = slice < slices;
@@ -337,7 +350,8 @@ cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex 
     a.page_size = s.page_size;
     a.page_shift = s.page_shift();
     a.kv_heads = s.num_kv_heads;
-    a.unit_tokens = tree_tile_tokens(s) * (p.pair ? 2 : 1);
+    a.tile_tokens = tree_tile_tokens(s);
+    a.unit_tokens = a.tile_tokens * (p.pair ? 2 : 1);
     a.ctas = s.sm_count;
     a.hdr = reinterpret_cast<TreeHeader *>(w);
     a.rows = reinterpret_cast<TreeRow *>(w + p.off_rows);
