@@ -45,30 +45,27 @@ constexpr int kTrThreads = 384;
 constexpr int kTrLaunchRegs = 168, kTrSoftmaxRegs = 200, kTrOtherRegs = 96;
 static_assert(128 * kTrOtherRegs + 256 * kTrSoftmaxRegs <= kTrThreads * kTrLaunchRegs, "the split fits the launch");
 enum TreeForm { SPLIT, PAIR, TURNS };
-template <int N>
-struct IntConstant {
-    static constexpr int value = N;
-};
 constexpr float kTrRescale = 8.f;  // log2
 constexpr float kTrLn2 = 0.6931471805599453f;
 
-template <int D>
+template <int D, TreeForm FORM>
 struct TrSmem {
     static constexpr int HALVES = D / 64;
-    static constexpr uint32_t Q_BYTES = 2 * 128u * 128u * (D > 128 ? 2 : HALVES);  // both buffers (at 256: one of 128 rows or two of 64)
+    static constexpr uint32_t Q_TILE = 128u * D * 2;  // one query tile
+    // two pieces' queries (at head_dim 256 one of 128 rows or two of 64)
+    static constexpr uint32_t Q_BYTES = Q_TILE * (FORM == PAIR ? 4 : FORM == TURNS ? 1 : 2);
     static constexpr uint32_t STAGE = kTreeKeys * D * 2u;
-    static constexpr int NS = D == 64 ? 18 : D == 128 ? 8 : 4;  // even: a stage holds K tiles or V tiles
+    // even: a stage holds K tiles or V tiles
+    static constexpr int NS = FORM == TURNS ? 4 : FORM == PAIR ? (D == 64 ? 16 : 6) : (D == 64 ? 18 : 8);
     static_assert(NS % 2 == 0, "each stage has one producer and one reader");
     static constexpr uint32_t HALF = STAGE / HALVES;
     static constexpr uint32_t RING_OFF = Q_BYTES;
     static constexpr uint32_t BAR_OFF = RING_OFF + NS * STAGE;
     static constexpr uint32_t ML_OFF = BAR_OFF + 1024;  // [2][group][128 rows] maximum and sum (SPLIT)
-    static constexpr uint32_t BYTES = ML_OFF + 2 * 2 * 128 * 8;
+    static constexpr uint32_t BYTES = ML_OFF + (FORM == SPLIT ? 2 * 2 * 128 * 8 : 0);
+    static_assert(1024 + BYTES <= 227 * 1024, "the tree kernel fits shared memory");
+    static_assert(1024 + BYTES > 228 * 1024 / 2, "one CTA an SM: each takes all tensor-memory columns");
 };
-static_assert(1024 + TrSmem<64>::BYTES <= 227 * 1024 && 1024 + TrSmem<128>::BYTES <= 227 * 1024 &&
-                  1024 + TrSmem<256>::BYTES <= 227 * 1024,
-              "the tree kernel fits shared memory");
-static_assert(1024 + TrSmem<64>::BYTES > 228 * 1024 / 2, "one CTA an SM: each takes all tensor-memory columns");
 
 struct TreeArgs {
     __nv_bfloat16 *out;
@@ -98,7 +95,7 @@ struct TreePiece {
 };
 
 template <typename F>
-__device__ __forceinline__ void tree_pieces(const TreeArgs &a, const TreeStart &s, F &&piece) {
+__device__ __forceinline__ void tree_pieces(const TreeArgs &a, const TreeStart &s, int unit_tokens, F &&piece) {
     TreePiece p;
     p.row = s.row;
     p.index = 0;
@@ -115,7 +112,7 @@ __device__ __forceinline__ void tree_pieces(const TreeArgs &a, const TreeStart &
         p.kvh = unit / tiles * s.hi + s.h0;
         p.qt = s.q0 + unit % tiles * s.qi;
         p.tile = tile;
-        p.cnt = (cut ? s.tile_end : p.row.nt) - tile;
+        p.cnt = (cut ? s.tile_end : tree_unit_tiles(p.row, p.qt, unit_tokens)) - tile;
         // a unit that began in another CTA, or goes on in the next one
         p.slot = tile > 0 ? 2 * (int)blockIdx.x : cut ? 2 * (int)blockIdx.x + 1 : -1;
         if (!piece(p)) return;
@@ -157,7 +154,7 @@ __device__ __forceinline__ TreeTile tree_tile(const TreeRow &row, int t, int win
 }
 
 // O += P V of one tile without the tensor cores: the row of this thread adds the keys in `vis` alone.
-template <int D>
+template <int D, uint32_t HALF>  // HALF: bytes of 64 columns of the tile
 __device__ __noinline__ void tree_pv_rows(uint32_t o_addr, uint32_t p_addr, const uint8_t *tile, unsigned long long vis,
                                           float alpha, bool first) {
 #pragma unroll 1
@@ -169,7 +166,7 @@ __device__ __noinline__ void tree_pv_rows(uint32_t o_addr, uint32_t p_addr, cons
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = first ? 0.f : __uint_as_float(r[i]) * alpha;
-        const uint8_t *half = tile + (c0 >> 6) * TrSmem<D>::HALF;
+        const uint8_t *half = tile + (c0 >> 6) * HALF;
 #pragma unroll 1
         for (int k = 0; k < kTreeKeys; ++k) {
             const uint32_t w = tmem_ld1(p_addr + (k >> 1));
@@ -201,7 +198,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ TreeArgs a) {
-    using L = TrSmem<D>;
+    using L = TrSmem<D, FORM>;
     constexpr int HALVES = L::HALVES, NS = L::NS;
     constexpr int PART_ROWS = FORM == PAIR ? 256 : 128;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -271,8 +268,10 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     auto takes = [&](const TreePiece &p, int x, int j) {
         return FORM == SPLIT ? (j & 1) == x : FORM == TURNS ? (p.index & 1) == x : x == 0 || second(p);
     };
-    auto q_slot = [&](const TreePiece &p) { return FORM == PAIR || !two_q ? 0 : p.index & 1; };
-    auto q_phase = [&](const TreePiece &p) { return (uint32_t)(FORM == PAIR || !two_q ? p.index : p.index >> 1); };
+    auto q_slot = [&](const TreePiece &p) { return two_q ? p.index & 1 : 0; };
+    auto q_phase = [&](const TreePiece &p) { return (uint32_t)(two_q ? p.index >> 1 : p.index); };
+    // query tile of group x in buffer qs
+    auto q_tile = [&](int qs, int x) { return (uint32_t)(FORM == PAIR ? 2 * qs + x : qs) * q_buf; };
 
     // each group of four warps changes its register share at the top of its own branch
     if (warp >= 8) {
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const bool mine = box < kTreeKeys / R;
         uint32_t i = kv;  // ring position: K of tile it at 2 it, V at 2 it + 1
         bool ok = true;
-        tree_pieces(a, start, [&](const TreePiece &p) {
+        tree_pieces(a, start, unit_tokens, [&](const TreePiece &p) {
             if (!kv) {
                 const int qs = q_slot(p);
                 const uint32_t ph = q_phase(p);
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], (uint32_t)(tiles * HALVES * a.box_q * a.group) * 128u);
                 __syncwarp();
                 if (lane < tiles * HALVES)
-                    tma_load_3d(sm + (FORM == PAIR ? lane / HALVES : qs) * q_buf + lane % HALVES * q_half, &tm_q, &q_full[qs],
+                    tma_load_3d(sm + q_tile(qs, lane / HALVES) + lane % HALVES * q_half, &tm_q, &q_full[qs],
                                 lane % HALVES * 64, p.kvh * a.group,
                                 p.row.q_begin + p.qt * unit_tokens + lane / HALVES * a.tile_tokens);
             }
@@ -348,7 +347,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint64_t dK = smem_desc(smem_u32(sm + L::RING_OFF), 16, 1024, kSwizzle128B);
         uint32_t i = 0, done[2] = {0, 0};  // tiles of each group
         bool ok = true;
-        tree_pieces(a, start, [&](const TreePiece &p) {
+        tree_pieces(a, start, unit_tokens, [&](const TreePiece &p) {
             const int qs = q_slot(p);
             ok = mbar_wait(&q_full[qs], q_phase(p) & 1, err, kErrWaitFull);
             for (int j = 0; j < p.cnt && ok; ++j, i += 2) {
@@ -362,7 +361,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (it >= 2) ok = mbar_wait(&pv_done[2 * x + b], ((it >> 1) - 1) & 1, err, kErrWaitFull);
                     if (!ok) continue;
                     tc_fence_after();
-                    const uint64_t q = add(dQ, (FORM == PAIR ? x : qs) * q_buf), k = add(dK, s * L::STAGE);
+                    const uint64_t q = add(dQ, q_tile(qs, x)), k = add(dK, s * L::STAGE);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         mma_ss_elect(S_col(x, b), add(q, (kk / 4) * q_half + (kk % 4) * 32),
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint64_t dV = smem_desc(smem_u32(sm + L::RING_OFF), L::HALF, 1024, kSwizzle128B);
         uint32_t i = 1, done[2] = {0, 0}, pieces[2] = {0, 0};
         bool ok = true;
-        tree_pieces(a, start, [&](const TreePiece &p) {
+        tree_pieces(a, start, unit_tokens, [&](const TreePiece &p) {
             // O may be overwritten once what it held has been read
             if (FORM == SPLIT) {
                 if (p.index > 0) ok = mbar_wait(&o_free[0], (p.index - 1) & 1, err, kErrWaitEmpty);
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const int tok_in_tile = m / a.group, head = m % a.group;
         uint32_t it = 0, pieces = 0, checks = 0, before = 0;  // before: tiles of the CTA's earlier pieces, both groups'
         bool ok = true;
-        tree_pieces(a, start, [&](const TreePiece &p) {
+        tree_pieces(a, start, unit_tokens, [&](const TreePiece &p) {
             const uint32_t tiles0 = before;
             before += p.cnt;
             if (FORM != SPLIT && !takes(p, x, 0)) return true;
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (rows) {
                         const uint32_t at = 2 * (tiles0 + j) + 1, s = at % NS;  // V's stage (it has landed: `checked`)
                         if (!mbar_wait(&kv_full[s], (at / NS) & 1, err, kErrWaitFull)) return ok = false;
-                        tree_pv_rows<D>(O, S, sm + L::RING_OFF + s * L::STAGE, vis, alpha, first);
+                        tree_pv_rows<D, L::HALF>(O, S, sm + L::RING_OFF + s * L::STAGE, vis, alpha, first);
                     } else {
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -793,14 +792,14 @@ __global__ void __launch_bounds__(JoinShape<D, SETS>::THREADS) tree_join_kernel(
     if (a.lse && c0 == 0) a.lse[out_row] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kTrLn2;
 }
 
-// `units`: at most so many in the step; `rows`: at most so many of a unit.
+// `whole`: no unit is cut; `units`: at most so many in the step; `rows`: at most so many of a unit.
 template <int D, TreeForm FORM>
-static cudaError_t launch(const TreeArgs &a, int ctas, long long units, int rows, const CUtensorMap &tm_kv, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+static cudaError_t launch(const TreeArgs &a, int ctas, bool whole, long long units, int rows, const CUtensorMap &tm_kv, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                           const CUtensorMap &tm_q, cudaStream_t st) {
-    const size_t smem = 1024 + TrSmem<D>::BYTES;
+    const size_t smem = 1024 + TrSmem<D, FORM>::BYTES;
     cudaError_t e = set_smem_limit((const void *)tree_kernel<D, FORM>, smem, st);
     if (e == cudaSuccess) e = launch_pdl(tree_kernel<D, FORM>, dim3(ctas), dim3(kTrThreads), smem, st, tm_kv, tm_k, tm_v, tm_q, a);
-    if (e != cudaSuccess || ctas == 1) return e;
+    if (e != cudaSuccess || ctas == 1 || whole) return e;
     constexpr int UNIT_TILES = FORM == PAIR ? 2 : 1;
     const int unit_tokens = a.tile_tokens * UNIT_TILES, part_rows = 128 * UNIT_TILES;
     const dim3 grid(ctas, rows > a.tile_tokens * a.group ? 8 : (rows + 31) / 32);
@@ -848,12 +847,12 @@ cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm
     const int rows = (p.max_new < unit_tokens ? p.max_new : unit_tokens) * a.group;
     const long long units = (long long)p.batch * s.num_kv_heads * ((p.max_new + unit_tokens - 1) / unit_tokens);
     if (s.head_dim == 64)
-        return p.pair ? dev::launch<64, dev::PAIR>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
-                      : dev::launch<64, dev::SPLIT>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
+        return p.pair ? dev::launch<64, dev::PAIR>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<64, dev::SPLIT>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
     if (s.head_dim == 128)
-        return p.pair ? dev::launch<128, dev::PAIR>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
-                      : dev::launch<128, dev::SPLIT>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
-    return dev::launch<256, dev::TURNS>(a, s.sm_count, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
+        return p.pair ? dev::launch<128, dev::PAIR>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<128, dev::SPLIT>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
+    return dev::launch<256, dev::TURNS>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
 }
 
 }  // namespace pkv

@@ -19,6 +19,11 @@ constexpr int kTreeMinPage = 8;      // a TMA box fills whole 8-row swizzle atom
 // a piece as much as two tiles beside its own; and a CTA takes no less than four tiles' worth.
 constexpr int kTreeTileCost = 3, kTreeHalfCost = 2, kTreePieceCost = 6, kTreeLeastCost = 12;
 static_assert(kTreeLeastCost > kTreePieceCost + kTreeTileCost, "the CTAs' first tiles are all different");
+// Steps leave units whole if their page list holds no more than eight tiles a row (four at head_dim 256, whose tiles take
+// twice as long), of at most four rows, since one row may have all of them: the join of cut units is a kernel
+// more, 2 us, in which a CTA goes through eight tiles.  (Steps of one to 63 short rows 6.8 to 16.2 us cut,
+// 5.6 to 13.2 whole; one row of 517 tokens 9.5 cut, 10.5 whole.)
+constexpr int kTreeWholeTiles = 8, kTreeWholeRows = 4;
 constexpr int kMapsMaxRows = 8192;   // rows whose offsets fit the shared memory of the maps kernel
 
 // Device error words of the speculative step (beside those of the bounded waits in ptx.cuh).
@@ -36,8 +41,8 @@ struct alignas(16) TreeRow {
     int32_t kv_base;  // offset of its first page in the page list
     int32_t kt0;      // first key tile (keys 64 * kt0 ..; after 0 under a window)
     int32_t nc;       // tiles of cached keys
-    int32_t nt;       // tiles, those of the drafted keys behind them
     int32_t nq;       // units per kv head: query tiles (or pairs of them)
+    int32_t pad;
 };
 static_assert(sizeof(TreeRow) == 32, "TreeRow is 8 ints");
 
@@ -59,11 +64,18 @@ struct TreeNode {
     int32_t parent, depth;
 };
 
+// Tiles of unit q of a row: of the cached keys, and behind them of the drafted ones up to its last token's.
+PKV_HOST_DEVICE int tree_unit_tiles(const TreeRow &t, int q, int unit_tokens) {
+    const int end = (q + 1) * unit_tokens;
+    return t.nc + ((end < t.n ? end : t.n) + kTreeKeys - 1) / kTreeKeys;
+}
+
 struct TreePlan {
     int batch = 0, num_tokens = 0, max_new = 0, words = 0;  // words: 64-bit words of a node's mask
     int window_left = -1;
     float scale_log2 = 0.f;
     bool pair = false;                     // two query tiles of 128 rows per unit
+    bool whole = false;                    // no unit is cut
     int part_rows = 0;                     // rows of a partial
     const int32_t *pages = nullptr;        // the caller's page list (device)
     size_t off_rows = 0, off_starts = 0, off_nodes = 0, off_masks = 0, off_cost = 0, off_part_o = 0,
@@ -73,7 +85,7 @@ struct TreePlan {
 // Query tokens of one 128-row tile.
 inline int tree_tile_tokens(const Shape &s) { return 128 / s.group(); }
 // The workspace of a step of `batch` rows, `tokens` tokens and up to `max_new` a row.
-void tree_layout(const Shape &s, int batch, int tokens, int max_new, TreePlan &p);
+void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_indices, TreePlan &p);
 
 struct TreeIndex {  // device arrays
     const int32_t *qo, *kvp, *kvi, *last, *parents;

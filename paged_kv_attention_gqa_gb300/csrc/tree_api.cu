@@ -115,7 +115,7 @@ extern "C" pkv_status pkv_plan_tree(pkv_handle_t h, const int32_t *qo_indptr, co
         if ((bits(qo_indptr) | bits(kv_indptr) | bits(kv_indices) | bits(last_page_len) | bits(parents) | bits(positions)) % 4)
             return fail(h, PKV_ERR_INVALID, "index arrays must be 4-byte aligned");
         TreePlan p;
-        pkv::tree_layout(s, batch, num_tokens, max_new, p);
+        pkv::tree_layout(s, batch, num_tokens, max_new, num_indices, p);
         h->planned_ws = nullptr;
         if (p.total > workspace_bytes)
             return fail(h, PKV_ERR_WORKSPACE,

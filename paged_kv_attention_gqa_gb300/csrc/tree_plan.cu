@@ -29,7 +29,7 @@ static size_t put(size_t &at, size_t bytes) {
     return here;
 }
 
-void tree_layout(const Shape &s, int batch, int tokens, int max_new, TreePlan &p) {
+void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_indices, TreePlan &p) {
     p.batch = batch;
     p.num_tokens = tokens;
     p.max_new = max_new;
@@ -37,6 +37,8 @@ void tree_layout(const Shape &s, int batch, int tokens, int max_new, TreePlan &p
     // head_dim 256 has no tensor memory for two query tiles' accumulators
     p.pair = s.head_dim <= 128 && max_new * s.group() > 128;
     p.part_rows = p.pair ? 256 : 128;
+    const long long whole_tiles = kTreeWholeTiles / (s.head_dim == 256 ? 2 : 1) * std::min(batch, kTreeWholeRows);
+    p.whole = (long long)num_indices * s.page_size <= kTreeKeys * whole_tiles;
     size_t at = kAlign;
     p.off_rows = put(at, (size_t)batch * sizeof(TreeRow));
     p.off_starts = put(at, (size_t)s.sm_count * sizeof(TreeStart));
@@ -53,6 +55,7 @@ namespace dev {
 struct TreePlanArgs {
     TreeIndex x;
     int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, tile_tokens, ctas;
+    int whole;     // no unit is cut
     int hi1, hi2;  // heads side by side: with all query tiles in turn, with two classes of them side by side
     TreeHeader *hdr;
     TreeRow *rows;
@@ -85,19 +88,21 @@ __device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, bool &
     const int lo = a.window_left >= 0 ? max(0, t.ctx - a.window_left) : 0;  // the root's first key
     t.kt0 = lo / kTreeKeys;
     t.nc = (t.ctx + kTreeKeys - 1) / kTreeKeys - t.kt0;
-    t.nt = t.nc + (t.n + kTreeKeys - 1) / kTreeKeys;
     t.nq = (t.n + a.unit_tokens - 1) / a.unit_tokens;
     return t;
 }
 
-// The cost of a tile of query unit q of a row, and of the row's units q0, q0 + qi, .. of one kv head.
+// The cost of a tile of query unit q of a row, of the unit, and of the row's units q0, q0 + qi, .. of one kv head.
 __device__ __forceinline__ int tile_cost(const TreePlanArgs &a, const TreeRow &t, int q) {
     return t.n - q * a.unit_tokens <= a.tile_tokens && a.unit_tokens > a.tile_tokens ? kTreeHalfCost : kTreeTileCost;
 }
+__device__ __forceinline__ long long unit_cost(const TreePlanArgs &a, const TreeRow &t, int q) {
+    return (long long)tree_unit_tiles(t, q, a.unit_tokens) * tile_cost(a, t, q) + kTreePieceCost;
+}
 __device__ __forceinline__ long long head_cost(const TreePlanArgs &a, const TreeRow &t, int q0, int qi) {
-    if (t.nq <= q0) return 0;
-    const int units = (t.nq - q0 + qi - 1) / qi, last = q0 + (units - 1) * qi;  // only the last may be a half
-    return (long long)(units - 1) * (t.nt * kTreeTileCost + kTreePieceCost) + (long long)t.nt * tile_cost(a, t, last) + kTreePieceCost;
+    long long sum = 0;
+    for (int q = q0; q < t.nq; q += qi) sum += unit_cost(a, t, q);
+    return sum;
 }
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
@@ -217,15 +222,21 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
             p.r = lo;
             const TreeRow t = a.rows[lo];
             const long long off = at - part(a.cost[lo]), head = head_cost(a, t, s.q0, qi);
-            const long long full = (long long)t.nt * kTreeTileCost + kTreePieceCost;
-            const int units = (t.nq - s.q0 + qi - 1) / qi, q = (int)min((long long)units - 1, off % head / full);
+            const int units = (t.nq - s.q0 + qi - 1) / qi;
+            int q = 0;  // of the lane's units
+            long long inside = off % head, cost = unit_cost(a, t, s.q0);
+            while (inside >= cost) {
+                inside -= cost;
+                cost = unit_cost(a, t, s.q0 + ++q * qi);
+            }
             const int each = tile_cost(a, t, s.q0 + q * qi);
-            const long long inside = off % head - q * full, begin = at - inside;
+            const long long begin = at - inside;
             p.unit = (int)(off / head) * units + q;
-            p.tile = (int)(max(0ll, inside - kTreePieceCost) / each);  // (below nt: inside is below the unit's cost)
+            if (a.whole) return p;  // every CTA from the beginning of the unit that it would have begun in
+            p.tile = (int)(max(0ll, inside - kTreePieceCost) / each);  // (one of them: inside is below the unit's cost)
             // a CTA begins inside the unit if it is past the unit's own cost and first tile
             p.first = (begin + kTreePieceCost + each - 1) / share;
-            p.last = (begin + kTreePieceCost + (long long)t.nt * each - 1) / share;
+            p.last = (begin + cost - 1) / share;
             return p;
         };
         const bool used = slice < slices;
@@ -353,6 +364,7 @@ cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex 
     a.tile_tokens = tree_tile_tokens(s);
     a.unit_tokens = a.tile_tokens * (p.pair ? 2 : 1);
     a.ctas = s.sm_count;
+    a.whole = p.whole;
     a.hdr = reinterpret_cast<TreeHeader *>(w);
     a.rows = reinterpret_cast<TreeRow *>(w + p.off_rows);
     a.starts = reinterpret_cast<TreeStart *>(w + p.off_starts);
