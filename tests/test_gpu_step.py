@@ -218,8 +218,8 @@ ACCEPT = {
 @pytest.mark.parametrize("kind", [torch.int32, torch.int64])
 @pytest.mark.parametrize("case", sorted(ACCEPT))
 def test_accept(case, kind):
-    for seed, (D, Hkv, P, layers) in enumerate([(64, 2, 16, 3), (128, 8, 8, 5), (256, 1, 64, 1), (64, 3, 16, 33)]):
-        draft, target = walk(ACCEPT[case]["trees"], seed, share=[0.8, 1.0, 0.0, 0.95][seed])
+    for seed, (D, Hkv, P, layers) in enumerate([(64, 2, 16, 3), (128, 8, 8, 5), (256, 1, 64, 1), (64, 3, 16, 33), (256, 9, 8, 2), (64, 1, 32, 4)]):
+        draft, target = walk(ACCEPT[case]["trees"], seed, share=[0.8, 1.0, 0.0, 0.95, 1.0, 0.9][seed])
         a = Accept(draft=draft, target=target, D=D, Hkv=Hkv, P=P, layers=layers, seed=seed, kind=kind, **ACCEPT[case])
         a.plan()
         a.run()

@@ -306,6 +306,42 @@ def test_inconsistent_arrays_are_reported_and_skipped():
         s.check("bad parent")
 
 
+def test_rows_past_the_planned_sizes_are_reported():
+    """More drafted tokens in a row than max_new, more in all than num_tokens: the rows count as empty."""
+    s = Step([100, 60, 30], [R.tree(5, 2), R.tree(9, 2), R.tree(6, 3)], 8, 2, 128, 16, 40, max_new=8)
+    s.plan()
+    s.run()
+    assert s.h.check_device_error(s.ws) == 5
+    assert (s.out[5:14] == 7).all() and (s.lse[5:14] == 7).all()
+    keep = torch.tensor([0, 1, 2, 3, 4, 14, 15, 16, 17, 18, 19])
+    compare(s.out.cpu()[keep], s.lse.cpu()[keep], tuple(y[keep] for y in s.reference()), "the other rows")
+    s = Step([100, 60], [R.tree(5, 2), R.tree(9, 2)], 8, 2, 128, 16, 41, tail=0)
+    s.dev["qo"][2] = 15
+    s.plan()
+    s.run()
+    assert s.h.check_device_error(s.ws) == 5 and (s.out[5:] == 7).all()
+
+
+@pytest.mark.parametrize("D,H,Hkv", [(64, 16, 2), (128, 8, 2), (256, 4, 4)])
+def test_plans_in_turn_on_one_workspace(D, H, Hkv):
+    """Long and short steps, wide and narrow ones, under a window and not, on one handle; each layer is run twice."""
+    steps = [Step([3000, 5], [R.tree(40, 3), R.tree(3, 1)], H, Hkv, D, 16, 50), Step([20], [R.tree(2, 1)], H, Hkv, D, 16, 51),
+             Step([700, 64, 0, 900], [R.tree(100, 4), R.tree(64, 2), [], R.tree(9, 3)], H, Hkv, D, 16, 52, window=33),
+             Step([], [], H, Hkv, D, 16, 53), Step([1, 2, 3], [R.tree(1, 1)] * 3, H, Hkv, D, 16, 54)]
+    pages = max(s.cache.shape[0] for s in steps)
+    h = B.Handle(num_qo_heads=H, num_kv_heads=Hkv, head_dim=D, page_size=16, max_batch=4, max_total_tokens=200, max_num_pages=pages,
+                 num_cache_pages=pages)
+    ws = torch.empty(h.workspace_size(B.MODE_TREE), dtype=torch.uint8, device="cuda")
+    for s in steps + steps[::-1]:
+        more = torch.full((pages - s.cache.shape[0], *s.cache.shape[1:]), NAN, dtype=s.cache.dtype)
+        s.cache, s.h, s.ws = torch.cat([s.cache, more]), h, ws
+        s.plan()
+        s.run()
+        s.check(f"{s.ctx}")
+        s.run()
+        s.check(f"{s.ctx} again")
+
+
 def test_streams_and_workspaces():
     """Two steps with workspaces of their own on two streams, neither the default one."""
     steps = [Step([900, 40], [R.tree(9, 3), R.tree(20, 4)], 8, 2, 128, 16, 23 + i) for i in range(2)]
