@@ -101,16 +101,15 @@ __device__ __forceinline__ void tree_pieces(const TreeArgs &a, const TreeStart &
     p.index = 0;
     int r = s.r, unit = s.unit, tile = s.tile;
     while (r < s.r_end || (r == s.r_end && (unit < s.unit_end || (unit == s.unit_end && tile < s.tile_end)))) {
-        const int tiles = p.row.nq > s.q0 ? (p.row.nq - s.q0 + s.qi - 1) / s.qi : 0;  // query tiles of this lane
-        if (unit >= a.num_kv_heads / s.hi * tiles) {
+        if (unit >= a.num_kv_heads / s.hi * p.row.nq) {
             ++r;
             unit = 0;
             if (r < a.batch) p.row = a.rows[r];
             continue;
         }
         const bool cut = r == s.r_end && unit == s.unit_end;  // the next CTA goes on with it
-        p.kvh = unit / tiles * s.hi + s.h0;
-        p.qt = s.q0 + unit % tiles * s.qi;
+        p.kvh = unit / p.row.nq * s.hi + s.h0;
+        p.qt = unit % p.row.nq;
         p.tile = tile;
         p.cnt = (cut ? s.tile_end : tree_unit_tiles(p.row, p.qt, unit_tokens)) - tile;
         // a unit that began in another CTA, or goes on in the next one
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(JoinShape<D, SETS>::THREADS) tree_join_kernel(
     const int c0 = warp % J::GROUPS * COLS, place = blockIdx.y * 32 + lane;
     // the plan was complete before the attention kernel let this one start
     const TreeStart &s = a.starts[b];
-    const int r = s.r_end, unit = s.unit_end, count = s.tail_count, tile_end = s.tile_end, lanes = s.hi * s.qi;
+    const int r = s.r_end, unit = s.unit_end, count = s.tail_count, tile_end = s.tile_end, lanes = s.hi;
     const bool begins = s.r != r || s.unit != unit || s.tile == 0;  // the unit that goes on begins here
     if (r >= a.batch || tile_end == 0 || !begins) {
         griddep_wait();
@@ -707,7 +706,7 @@ __global__ void __launch_bounds__(JoinShape<D, SETS>::THREADS) tree_join_kernel(
         return;
     }
     const TreeRow row = a.rows[r];
-    const int tiles = (row.nq - s.q0 + s.qi - 1) / s.qi, kvh = unit / tiles * s.hi + s.h0, qt = s.q0 + unit % tiles * s.qi;
+    const int kvh = unit / row.nq * s.hi + s.h0, qt = unit % row.nq;
     const int rows = min(unit_tokens, row.n - qt * unit_tokens) * a.group, tile_rows = a.tile_tokens * a.group;
     const int f = (place >> 7) * tile_rows + (place & 127);  // token * group + head within the unit
     const bool live = (place & 127) < tile_rows && f < rows;

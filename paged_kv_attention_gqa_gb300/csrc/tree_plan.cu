@@ -44,7 +44,7 @@ void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_ind
     p.off_starts = put(at, (size_t)s.sm_count * sizeof(TreeStart));
     p.off_nodes = put(at, (size_t)tokens * sizeof(TreeNode));
     p.off_masks = put(at, (size_t)tokens * p.words * 8);
-    p.off_cost = put(at, (size_t)batch * 16);
+    p.off_cost = put(at, (size_t)batch * 8);
     p.off_part_o = put(at, (size_t)2 * s.sm_count * p.part_rows * s.head_dim * 4);
     p.off_part_lse = put(at, (size_t)2 * s.sm_count * p.part_rows * 4);
     p.total = at;
@@ -56,13 +56,13 @@ struct TreePlanArgs {
     TreeIndex x;
     int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, tile_tokens, ctas;
     int whole;     // no unit is cut
-    int hi1, hi2;  // heads side by side: with all query tiles in turn, with two classes of them side by side
+    int hi;        // kv heads side by side
     TreeHeader *hdr;
     TreeRow *rows;
     TreeStart *starts;
     TreeNode *nodes;
     unsigned long long *masks;
-    longlong2 *cost;  // before row r: of the even query units, of the odd ones, one kv head each
+    long long *cost;  // before row r, of one kv head
 };
 
 // The row's numbers if its index arrays agree (n = 0 and ctx = -1 if not).
@@ -92,16 +92,16 @@ __device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, bool &
     return t;
 }
 
-// The cost of a tile of query unit q of a row, of the unit, and of the row's units q0, q0 + qi, .. of one kv head.
+// The cost of a tile of query unit q of a row, of the unit, and of the row's units of one kv head.
 __device__ __forceinline__ int tile_cost(const TreePlanArgs &a, const TreeRow &t, int q) {
     return t.n - q * a.unit_tokens <= a.tile_tokens && a.unit_tokens > a.tile_tokens ? kTreeHalfCost : kTreeTileCost;
 }
 __device__ __forceinline__ long long unit_cost(const TreePlanArgs &a, const TreeRow &t, int q) {
     return (long long)tree_unit_tiles(t, q, a.unit_tokens) * tile_cost(a, t, q) + kTreePieceCost;
 }
-__device__ __forceinline__ long long head_cost(const TreePlanArgs &a, const TreeRow &t, int q0, int qi) {
+__device__ __forceinline__ long long head_cost(const TreePlanArgs &a, const TreeRow &t) {
     long long sum = 0;
-    for (int q = q0; q < t.nq; q += qi) sum += unit_cost(a, t, q);
+    for (int q = 0; q < t.nq; ++q) sum += unit_cost(a, t, q);
     return sum;
 }
 
@@ -109,7 +109,7 @@ constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanArgs a) {
     __shared__ int32_t parent[kPlanWarps][kTreeMaxNew];
-    __shared__ long long sums[2][kPlanWarps];
+    __shared__ long long sums[kPlanWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch();
@@ -153,57 +153,41 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         return;
     }
     // ------------------------------------------------ the rows, and each CTA's share
-    longlong2 before = make_longlong2(0, 0);
+    long long before = 0;
     for (int r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
         const int r = r0 + threadIdx.x;
-        longlong2 v = make_longlong2(0, 0);
+        long long v = 0;
         if (r < a.batch) {
             bool ok;
             const TreeRow t = tree_row(a, r, ok);
             if (!ok) atomicCAS(&a.hdr->err, 0, kErrTreeRow);
             a.rows[r] = t;
-            v = make_longlong2(head_cost(a, t, 0, 2), head_cost(a, t, 1, 2));
+            v = head_cost(a, t);
         }
-        longlong2 c = v;
+        long long c = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, c.x, o), y = __shfl_up_sync(0xffffffffu, c.y, o);
-            if (lane >= o) {
-                c.x += x;
-                c.y += y;
-            }
+            const long long x = __shfl_up_sync(0xffffffffu, c, o);
+            if (lane >= o) c += x;
         }
-        if (lane == 31) {
-            sums[0][warp] = c.x;
-            sums[1][warp] = c.y;
-        }
+        if (lane == 31) sums[warp] = c;
         __syncthreads();
-        longlong2 mine = before;
+        long long mine = before;
         for (int w = 0; w < kPlanWarps; ++w) {
-            if (w < warp) {
-                mine.x += sums[0][w];
-                mine.y += sums[1][w];
-            }
-            before.x += sums[0][w];
-            before.y += sums[1][w];
+            if (w < warp) mine += sums[w];
+            before += sums[w];
         }
         __syncthreads();
-        if (r < a.batch) a.cost[r] = make_longlong2(mine.x + c.x - v.x, mine.y + c.y - v.y);
+        if (r < a.batch) a.cost[r] = mine + c - v;
     }
     __syncthreads();
-    // Two query tiles of a row side by side read its keys once (L2 keeps them); that wants as many odd tiles as even
-    // ones, or the lanes of the odd ones would idle
-    const int qi = a.hi2 > 0 && before.y * 16 >= before.x * 15 ? 2 : 1, hi = qi == 2 ? a.hi2 : a.hi1;
-    const int lanes = hi * qi, slices = a.ctas / lanes, heads = a.kv_heads / hi;
+    const int lanes = a.hi, slices = a.ctas / lanes, heads = a.kv_heads / lanes;
+    const long long total = heads * before, share = max((total + slices - 1) / slices, (long long)kTreeLeastCost);
     for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
         TreeStart s = {};
         const int slice = c / lanes;
-        s.h0 = c % lanes % hi;
-        s.hi = hi;
-        s.q0 = c % lanes / hi;
-        s.qi = qi;
-        auto part = [&](const longlong2 &v) { return heads * (qi == 1 ? v.x + v.y : s.q0 ? v.y : v.x); };
-        const long long total = part(before), share = max((total + slices - 1) / slices, (long long)kTreeLeastCost);
+        s.h0 = c % lanes;
+        s.hi = lanes;
         struct Place {
             int r, unit, tile;
             long long first, last;  // the slices with the unit's first and last piece
@@ -211,27 +195,26 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         auto place = [&](long long at) {
             Place p = {a.batch, 0, 0, 0, 0};
             if (at >= total) return p;
-            int lo = 0, hi_row = a.batch - 1;  // the last row that begins at or before `at`
-            while (lo < hi_row) {
-                const int mid = (lo + hi_row + 1) >> 1;
-                if (part(a.cost[mid]) <= at)
+            int lo = 0, hi = a.batch - 1;  // the last row that begins at or before `at`
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (heads * a.cost[mid] <= at)
                     lo = mid;
                 else
-                    hi_row = mid - 1;
+                    hi = mid - 1;
             }
             p.r = lo;
             const TreeRow t = a.rows[lo];
-            const long long off = at - part(a.cost[lo]), head = head_cost(a, t, s.q0, qi);
-            const int units = (t.nq - s.q0 + qi - 1) / qi;
-            int q = 0;  // of the lane's units
-            long long inside = off % head, cost = unit_cost(a, t, s.q0);
+            const long long off = at - heads * a.cost[lo], head = head_cost(a, t);
+            int q = 0;
+            long long inside = off % head, cost = unit_cost(a, t, 0);
             while (inside >= cost) {
                 inside -= cost;
-                cost = unit_cost(a, t, s.q0 + ++q * qi);
+                cost = unit_cost(a, t, ++q);
             }
-            const int each = tile_cost(a, t, s.q0 + q * qi);
+            const int each = tile_cost(a, t, q);
             const long long begin = at - inside;
-            p.unit = (int)(off / head) * units + q;
+            p.unit = (int)(off / head) * t.nq + q;
             if (a.whole) return p;  // every CTA from the beginning of the unit that it would have begun in
             p.tile = (int)(max(0ll, inside - kTreePieceCost) / each);  // (one of them: inside is below the unit's cost)
             // a CTA begins inside the unit if it is past the unit's own cost and first tile
@@ -370,18 +353,10 @@ cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex 
     a.starts = reinterpret_cast<TreeStart *>(w + p.off_starts);
     a.nodes = reinterpret_cast<TreeNode *>(w + p.off_nodes);
     a.masks = reinterpret_cast<unsigned long long *>(w + p.off_masks);
-    a.cost = reinterpret_cast<longlong2 *>(w + p.off_cost);
-    // as many heads side by side as leave no more than a 32nd of the CTAs without work
-    auto heads_beside = [&](int classes) {
-        for (int h = s.num_kv_heads; h > 0; --h)
-            if (s.num_kv_heads % h == 0) {
-                const int lanes = h * classes, idle = s.sm_count % lanes;
-                if (lanes <= s.sm_count && idle * 32 <= s.sm_count) return h;
-            }
-        return 0;
-    };
-    a.hi1 = heads_beside(1);  // (1 always does)
-    a.hi2 = heads_beside(2);
+    a.cost = reinterpret_cast<long long *>(w + p.off_cost);
+    // as many heads side by side as leave no more than a 32nd of the CTAs without work (one always does)
+    a.hi = s.num_kv_heads;
+    while (s.num_kv_heads % a.hi || a.hi > s.sm_count || s.sm_count % a.hi * 32 > s.sm_count) --a.hi;
     return launch_pdl(dev::tree_plan_kernel, dim3(1 + (p.batch + dev::kPlanWarps - 1) / dev::kPlanWarps),
                       dim3(dev::kPlanThreads), 0, st, a);
 }

@@ -244,59 +244,48 @@ class Row:
     def cost(self, q):
         return self.tiles(q) * self.each(q) + PIECE
 
-    def head(self, q0, qi):
-        return sum(self.cost(q) for q in range(q0, self.units, qi))
-
-
-def beside(heads, ctas, classes):
-    return next((h for h in range(heads, 0, -1) if heads % h == 0 and h * classes <= ctas and ctas % (h * classes) * 32 <= ctas), 0)
+    def head(self):
+        return sum(self.cost(q) for q in range(self.units))
 
 
 def plan(rows, kv_heads, ctas, whole):
-    before, even, odd = [], 0, 0
+    lanes = next(h for h in range(min(kv_heads, ctas), 0, -1) if kv_heads % h == 0 and ctas % h * 32 <= ctas)
+    heads, slices, before = kv_heads // lanes, ctas // lanes, [0]
     for r in rows:
-        before.append((even, odd))
-        even, odd = even + r.head(0, 2), odd + r.head(1, 2)
-    h2 = beside(kv_heads, ctas, 2)
-    qi = 2 if h2 and odd * 16 >= even * 15 else 1
-    hi = h2 if qi == 2 else beside(kv_heads, ctas, 1)
-    lanes, heads = hi * qi, kv_heads // hi
-    slices, starts = ctas // lanes, []
+        before.append(before[-1] + heads * r.head())
+    total, starts = before.pop(), []
+    share = max(-(-total // slices), LEAST)
     for c in range(ctas):
-        piece, h0, q0 = c // lanes, c % lanes % hi, c % lanes // hi
-        part = lambda v: heads * (sum(v) if qi == 1 else v[q0])
-        total = part((even, odd))
-        share = max(-(-total // slices), LEAST)
+        piece = c // lanes
 
         def place(at):
             if at >= total:
                 return (len(rows), 0, 0), 0, 0
-            r = max(i for i, v in enumerate(before) if part(v) <= at)
-            row, off = rows[r], at - part(before[r])
-            head, units = row.head(q0, qi), len(range(q0, row.units, qi))
-            q, inside = 0, off % head
-            while inside >= row.cost(q0 + q * qi):
-                inside -= row.cost(q0 + q * qi)
+            r = max(i for i, v in enumerate(before) if v <= at)
+            row, off = rows[r], at - before[r]
+            q, inside = 0, off % row.head()
+            while inside >= row.cost(q):
+                inside -= row.cost(q)
                 q += 1
-            each, begin, unit = row.each(q0 + q * qi), at - inside, off // head * units + q
+            each, begin, unit = row.each(q), at - inside, off // row.head() * row.units + q
             if whole:
                 return (r, unit, 0), 0, 0
             return ((r, unit, max(0, inside - PIECE) // each), (begin + PIECE + each - 1) // share,
-                    (begin + row.cost(q0 + q * qi) - 1) // share)
+                    (begin + row.cost(q) - 1) // share)
         a, b = (place((piece + i) * share if piece < slices else total) for i in (0, 1))
-        starts.append(dict(cta=c, h0=h0, hi=hi, q0=q0, qi=qi, begin=a[0], end=b[0], tail=b[2] - b[1] + 1, lanes=lanes))
+        starts.append(dict(cta=c, lane=c % lanes, begin=a[0], end=b[0], tail=b[2] - b[1] + 1, lanes=lanes))
     return starts
 
 
 def pieces(rows, kv_heads, s):
     (r, unit, tile), out = s["begin"], []
     while (r, unit, tile) < s["end"]:
-        units = len(range(s["q0"], rows[r].units, s["qi"]))
-        if unit >= kv_heads // s["hi"] * units:
+        units = rows[r].units
+        if unit >= kv_heads // s["lanes"] * units:
             r, unit = r + 1, 0
             continue
         cut = (r, unit) == s["end"][:2]
-        head, q = unit // units * s["hi"] + s["h0"], s["q0"] + unit % units * s["qi"]
+        head, q = unit // units * s["lanes"] + s["lane"], unit % units
         end = s["end"][2] if cut else rows[r].tiles(q)
         slot = 2 * s["cta"] if tile else 2 * s["cta"] + 1 if cut else None
         assert end > tile
@@ -307,14 +296,13 @@ def pieces(rows, kv_heads, s):
 
 @pytest.mark.parametrize("ctas", [1, 2, 3, 7, 152, 300])
 def test_shares_and_joins(ctas):
-    rng, classes = random.Random(ctas), set()
+    rng = random.Random(ctas)
     for _ in range(120):
         kv_heads, unit, pair, whole = rng.choice([1, 2, 3, 4, 8, 5, 16, 100]), rng.choice([8, 16, 42, 128]), rng.random() < 0.5, rng.random() < 0.2
         same, most = rng.random() < 0.5, rng.choice([1, 16, 60, 256])
         rows = [Row(0, 0, unit, pair) if rng.random() < 0.2 else
                 Row(rng.choice([0, 1, 2, 9, 99, 999]), most if same else rng.randint(1, most), unit, pair) for _ in range(rng.randint(1, 30))]
         starts = plan(rows, kv_heads, ctas, whole)
-        classes.add(starts[0]["qi"])
         got, slots = {}, {}
         for s in starts:
             for what, begin, end, slot in pieces(rows, kv_heads, s):
@@ -336,4 +324,3 @@ def test_shares_and_joins(ctas):
             assert parts[0][0] == 0 and parts[-1][1] == rows[what[0]].tiles(what[2])
             assert all(a[1] == b[0] for a, b in zip(parts, parts[1:]))
             assert joined.get(what) == ([p[2] for p in parts] if len(parts) > 1 else None)
-    assert ctas < 34 or classes == {1, 2}, "steps of both kinds"
