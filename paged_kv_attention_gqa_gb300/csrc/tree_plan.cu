@@ -11,8 +11,10 @@
 // the root, which doubling the parents' pointers tells in log2(depth) rounds; its place is its depth.
 // Every CTA of the row does this for itself, which costs less than a launch that would pass it on.  Then bulk copies
 // take the path's keys and values to the row's next slots (copies by all threads, 16 bytes each, were bound by the
-// instructions of their addresses).  HBM-bound for batches (each accepted vector read and written once), a
-// chain of loads for one row.
+// instructions of their addresses: 12.4 us where bulk copies take 9.0).  HBM-bound for batches (each accepted vector
+// read and written once), a chain of loads for one row.
+// Measured: 64 rows of up to 16 nodes, 32 layers of 8 heads of 128, 43 MB: 10.2 us; 40 rows with paths of 20, 24 layers
+// of 4 heads of 64, 16.5 MB: 6.7 us; one row, 32 layers: 2.7 us.  The plan takes 4 to 9 us a step.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -247,8 +249,8 @@ struct AcceptArgs {
 };
 
 constexpr int kAcceptThreads = 256, kAcceptWarps = kAcceptThreads / 32, kAcceptBuffer = 2048;
-constexpr int kAcceptBytes = 65536;  // of buffers
-constexpr int kAcceptCtas = 3;  // an SM
+constexpr int kAcceptBytes = 32768;  // of buffers
+constexpr int kAcceptCtas = 5;       // an SM (64 rows, 32 layers: 10.2 us; three with twice the buffers 11.3)
 
 static_assert(kAcceptThreads == kTreeMaxNew, "a thread a node");
 
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kerne
             if (a.x.seq && len) a.x.seq[r] = t.ctx + len;
         }
     }
-    // A copy is up to 2 KB of K or V of a path node in a layer, through a buffer in shared memory of its lane: four lanes of
+    // A copy is up to 2 KB of K or V of a path node in a layer, through a buffer in shared memory of its lane: two lanes of
     // each warp have one, more where they are smaller
     if (lane >= a.lanes) return;
     const int l0 = blockIdx.y * a.layers_per_cta, layers = min(a.x.layers - l0, a.layers_per_cta);
@@ -377,7 +379,7 @@ cudaError_t launch_tree_accept(const Shape &s, const TreePlan &p, const TreeAcce
     // a layer a CTA, more where the rows' CTAs would not all run at once
     const int most = std::max(1, dev::kAcceptCtas * s.sm_count / p.batch), chunks = std::max(1, std::min(x.layers, most));
     a.layers_per_cta = std::max(1, (x.layers + chunks - 1) / chunks);
-    a.lanes = 4;
+    a.lanes = 2;
     while (a.lanes < 32 && a.vecs * 16 * 2 * a.lanes <= dev::kAcceptBytes / dev::kAcceptWarps) a.lanes *= 2;
     // the copies of a CTA are counted in 32 bits
     const int parts = (a.vecs * 16 + dev::kAcceptBuffer - 1) / dev::kAcceptBuffer;
