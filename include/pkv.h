@@ -384,7 +384,7 @@ pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t 
  * CUDA graph (after one uncaptured call of each), which then serves every step whose sizes stay within
  * the captured ones.  Arrays that the kernels find inconsistent are skipped and reported:
  * pkv_build_maps by its status, the others by pkv_check_device_error, code 5 (a row's index arrays do
- * not agree: the row counts as empty), 6 (a page id outside the cache: read as zeros, not written) or
+ * not agree, or it begins below an earlier row's first token: the row counts as empty), 6 (a page id outside the cache: read as zeros, not written) or
  * 7 (a parent that does not stand before its child: taken as -1).
  */
 

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int
             const int b = e - row.begin;
             if (b >= row.held) a.table[row.r * a.table_stride + b] = page;
         });
-    for (int q = id; q < back; q += step) a.free_pages[F + q] = *given_back_at(q);
+    for (long long q = id; q < back; q += step) a.free_pages[F + q] = *given_back_at((int)q);
     if (a.slots || a.positions) {
         auto position = [&](const Row &row, int t) { return m.seq[row.r] + t - row.begin; };
         entries(
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kMapThreads) maps_kernel(const MapsArgs a, int
                 if (a.slots) a.slots[t] = (page << a.page_shift) + (pos & (P - 1));
                 if (a.positions) a.positions[t] = pos;
             });
-        for (int t = T + id; t < a.token_capacity; t += step) {
+        for (long long t = (long long)T + id; t < a.token_capacity; t += step) {
             if (a.slots) a.slots[t] = -1;
             if (a.positions) a.positions[t] = 0;
         }

@@ -1,6 +1,6 @@
 // Argument marshalling of the speculative step's calls (the Python module _marshal): each checks its tensors
 // (type, shape, device, layout) and hands their pointers to the C ABI.  The same checks written in Python
-// cost 0.5 us a tensor on the GPU machine's host, 13 to 19 us a call; here a call's are below 1 us.
+// cost 0.5 us a tensor (Grace), 13 to 19 us a call; here a call's are below 1 us.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>

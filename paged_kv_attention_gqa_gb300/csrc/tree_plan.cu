@@ -67,12 +67,25 @@ struct TreePlanArgs {
     long long *cost;  // before row r, of one kv head
 };
 
-// The row's numbers if its index arrays agree (n = 0 and ctx = -1 if not).
-__device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, bool &ok) {
+// A row's first token, 0 if that is no token of the step; and the highest of the rows [from, to), for the whole warp.
+__device__ __forceinline__ int first_token(const TreePlanArgs &a, int r) {
+    const int q = __ldg(a.x.qo + r);
+    return q <= a.tokens ? q : 0;
+}
+__device__ __forceinline__ int highest_token(const TreePlanArgs &a, int from, int to) {
+    int top = 0;
+#pragma unroll 4
+    for (int r = from + (threadIdx.x & 31); r < to; r += 32) top = max(top, first_token(a, r));
+    return __reduce_max_sync(0xffffffffu, top);
+}
+
+// The row's numbers if its index arrays agree (n = 0 and ctx = -1 if not).  `highest`: of the earlier rows' first
+// tokens.  A row that begins below it could have tokens of another one, whose nodes would be written twice.
+__device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, int highest, bool &ok) {
     TreeRow t = {};
     const int q0 = __ldg(a.x.qo + r), q1 = __ldg(a.x.qo + r + 1), k0 = __ldg(a.x.kvp + r), k1 = __ldg(a.x.kvp + r + 1);
     const int fill = __ldg(a.x.last + r);
-    ok = q0 >= 0 && q1 >= q0 && q1 <= a.tokens && q1 - q0 <= a.max_new && k0 >= 0 && k1 >= k0 && k1 <= a.x.num_indices;
+    ok = q0 >= highest && q1 >= q0 && q1 <= a.tokens && q1 - q0 <= a.max_new && k0 >= 0 && k1 >= k0 && k1 <= a.x.num_indices;
     if (r == 0) ok = ok && q0 == 0 && k0 == 0;
     long long length = 0;
     if (ok && k1 > k0) {
@@ -120,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         const int r = (blockIdx.x - 1) * kPlanWarps + warp;
         if (r >= a.batch) return;
         bool ok;
-        const TreeRow t = tree_row(a, r, ok);
+        const TreeRow t = tree_row(a, r, highest_token(a, 0, r), ok);
         int32_t *const p = parent[warp];
         for (int i = lane; i < t.n; i += 32) {
             int32_t up = a.x.parents ? a.x.parents[t.q_begin + i] : i - 1;
@@ -156,12 +169,21 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
     }
     // ------------------------------------------------ the rows, and each CTA's share
     long long before = 0;
+    int highest = 0, known = 0;  // of the rows before `known`
     for (int r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
-        const int r = r0 + threadIdx.x;
+        const int r = r0 + threadIdx.x, first = min(r0 + warp * 32, a.batch);  // (the warp's first row)
+        highest = max(highest, highest_token(a, known, first));
+        known = first;
+        int top = r < a.batch ? first_token(a, r) : 0;  // of the warp's rows up to this one, which is at or above itself
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, top, o);
+            if (lane >= o) top = max(top, x);
+        }
         long long v = 0;
         if (r < a.batch) {
             bool ok;
-            const TreeRow t = tree_row(a, r, ok);
+            const TreeRow t = tree_row(a, r, max(highest, top), ok);
             if (!ok) atomicCAS(&a.hdr->err, 0, kErrTreeRow);
             a.rows[r] = t;
             v = head_cost(a, t);
@@ -253,6 +275,8 @@ constexpr int kAcceptBytes = 32768;  // of buffers
 constexpr int kAcceptCtas = 5;       // an SM (64 rows, 32 layers: 10.2 us; three with twice the buffers 11.3)
 
 static_assert(kAcceptThreads == kTreeMaxNew, "a thread a node");
+constexpr int kAcceptRounds = 8;
+static_assert(1 << kAcceptRounds >= kTreeMaxNew, "as many rounds reach past the root of the longest path");
 
 template <typename Token>
 __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kernel(const AcceptArgs a) {
@@ -284,7 +308,7 @@ __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kerne
     __syncthreads();
     int up = node ? self.parent : -1;
     bool on = tid == 0 || (agrees && first[self.parent] == tid);
-    while (__syncthreads_or(up >= 0)) {
+    for (int round = 0; round < kAcceptRounds && __syncthreads_or(up >= 0); ++round) {
         above[tid] = make_int2(up, on);
         __syncthreads();
         if (up >= 0) {
@@ -324,7 +348,10 @@ __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kerne
         if (phase) bulk_store_wait_read();  // the buffer's last store
         mbar_arrive_expect_tx(bar, size);
         bulk_load(buffer, static_cast<const uint8_t *>(v ? a.x.v : a.x.k) + from * 2 + begin, size, bar);
-        if (!mbar_wait(bar, phase++ & 1, &a.hdr->err, kErrWaitFull)) break;
+        if (!mbar_wait(bar, phase++ & 1, &a.hdr->err, kErrWaitFull)) {
+            for (uint32_t d = 0; d < 1024; ++d) __nanosleep(1000);  // the copy in flight lands before the CTA may end
+            break;
+        }
         bulk_store(static_cast<uint8_t *>(a.x.cache) + to * 2 + begin, buffer, size);
     }
     bulk_store_wait();

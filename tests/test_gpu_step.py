@@ -278,6 +278,35 @@ def test_accept_reports_pages_outside_the_cache():
     assert rows == {int(x) for x in a.kvi[a.kvp[1] + 30 // 16:]}, "row 1's path alone"
 
 
+def test_accept_of_rows_that_overlap():
+    """Offsets that go back: the row after that, which would have tokens of an earlier one, counts as empty too, and its
+    nodes do not mix with theirs."""
+    a = Accept([20, 30, 40, 50], [R.tree(5, 1), R.tree(4, 2), R.tree(5, 1), R.tree(12, 1)], [7] * 26, [7] * 26)
+    a.dev[0][2] = 2  # tokens [0, 5), [5, 2), [2, 14) and [14, 26)
+    a.plan()
+    assert a.h.check_device_error(a.ws) == 5
+    a.run()
+    assert a.count.tolist() == [5, 0, 0, 12] and a.next.tolist() == [7, -1, -1, 7] and a.seq.tolist() == [25, -3, -3, 62]
+    assert a.accepted.tolist() == list(range(5)) + [-4] * 9 + list(range(12)) + [-4] * a.tail
+    want, P = a.cache.clone(), a.cache.shape[3]
+    for r, begin in ((0, 0), (3, 14)):
+        for i in range(a.count[r].item()):
+            pos = a.ctx[r] + i
+            want[:, int(a.kvi[a.kvp[r] + pos // P]), :, pos % P] = a.new[:, begin + i]
+    assert torch.equal(a.got_cache.cpu().view(torch.int16), want.view(torch.int16))
+
+
+def test_accept_of_rows_that_overlap_far_apart():
+    """Offsets that go back behind hundreds of rows."""
+    n = 700
+    a = Accept([3] * n, [R.tree(2, 1)] * n, [7] * (2 * n), [7] * (2 * n))
+    a.dev[0][600], a.dev[0][601] = 4, 6  # row 599 ends before it begins, row 600 has row 2's tokens, row 601 too many
+    a.plan()
+    assert a.h.check_device_error(a.ws) == 5
+    a.run()
+    assert a.count.tolist() == [0 if r in (599, 600, 601) else 2 for r in range(n)]
+
+
 class Loop:
     """Speculative steps one after another, all state on the device; mirror() replays them by the definitions."""
 
