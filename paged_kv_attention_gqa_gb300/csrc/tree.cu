@@ -77,6 +77,7 @@ struct TreeArgs {
     float *lse;
     const TreeRow *rows;
     const TreeStart *starts;
+    const TreeJoin *joins;
     const TreeNode *nodes;
     const unsigned long long *masks;
     const int32_t *pages;
@@ -682,136 +683,138 @@ __global__ void __launch_bounds__(kTrThreads, 1)
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Join of a unit's pieces: with w_i = 2^(lse_i - max lse), o = sum w_i o_i / sum w_i.  Block (b, y) takes 32 rows of
-// the unit that begins in CTA b and goes on in the next ones; a thread has a row (neighbours neighbouring ones)
-// and four vectors of four columns, SETS sets of threads take the pieces in turn.  Bounded by trips to L2 (the plan's
-// record, the partials), so all of a thread's loads are in flight at once: two pieces' where units are cut
-// once or twice, up to four of each set's where few units share many CTAs.  Joining in the CTA that finishes last
-// took longer (wide trees 167 -> 185 us, long chains 42 -> 45): its few warps make those trips one after another.
-template <int D, int SETS>
-struct JoinShape {
-    static constexpr int GROUPS = D / 16;  // of threads with the same columns
-    static constexpr int THREADS = 32 * GROUPS * SETS, BATCH = SETS > 1 || D == 256 ? 4 : 2;
+// Join of a unit's pieces: with w_i = 2^(lse_i - max lse), o = sum w_i o_i / sum w_i.  A block takes up to 32 rows of a
+// cut unit and the columns that its record says; a thread has a row and four vectors of four columns, warps (and
+// parts of a warp, where the unit has few rows) beside that take the pieces in turn.  Bounded by trips to L2
+// (the plan's record, the partials), so all pieces are on their way at once as far as they fit.  Records of the cut
+// units alone, with as many blocks as their pieces ask for, against a column of blocks for every CTA and one rule for all
+// units: 4 rows of one drafted token at head_dim 256 16.4 -> 12.0 us, 16 rows of 352 query rows a head 28.9 -> 23.8,
+// the mean of 48 steps 15.2 -> 14.7 (a third of that by kTreeLeastWhole).
+// Joining in the CTA that finishes last took longer (wide trees 167 -> 185 us, long chains 42 -> 45): its few warps
+// make those trips one after another.
+struct JoinSum {
+    float top, sum;
+    float4 acc[4];
 };
-template <int D, int SETS>
-__global__ void __launch_bounds__(JoinShape<D, SETS>::THREADS) tree_join_kernel(const TreeArgs a, int unit_tokens, int part_rows) {
-    using J = JoinShape<D, SETS>;
-    constexpr int COLS = 4, BATCH = J::BATCH, C = D / 4;
-    __shared__ float4 others[SETS > 1 ? (SETS - 1) * C * 32 : 1];
-    __shared__ float2 sums[SETS > 1 ? (SETS - 1) * 32 : 1];
-    const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, set = warp / J::GROUPS;
-    const int c0 = warp % J::GROUPS * COLS, place = blockIdx.y * 32 + lane;
+__device__ __forceinline__ float4 scaled(const float4 &x, float w) { return make_float4(x.x * w, x.y * w, x.z * w, x.w * w); }
+__device__ __forceinline__ float4 fma4(float w, const float4 &x, const float4 &y) {
+    return make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
+}
+// j: the sums to the maximum `top`
+__device__ __forceinline__ void raise_top(JoinSum &j, float top) {
+    const float w = j.top == -INFINITY ? 0.f : exp2f(j.top - top);
+    j.top = top;
+    j.sum *= w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) j.acc[c] = scaled(j.acc[c], w);
+}
+template <int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) tree_join_kernel(const TreeArgs a, int part_rows) {
+    constexpr int COLS = 4, C = D / 4;
+    __shared__ float4 others[WARPS * COLS * 32];
+    __shared__ float2 sums[WARPS * 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the plan was complete before the attention kernel let this one start
-    const TreeStart &s = a.starts[b];
-    const int r = s.r_end, unit = s.unit_end, count = s.tail_count, tile_end = s.tile_end, lanes = s.hi;
-    const bool begins = s.r != r || s.unit != unit || s.tile == 0;  // the unit that goes on begins here
-    if (r >= a.batch || tile_end == 0 || !begins) {
+    const TreeJoin u = a.joins[blockIdx.x];
+    const int rows = u.tokens * a.group, tile_rows = a.tile_tokens * a.group;
+    const int R = tree_join_rows(rows), place = blockIdx.y * R + (lane & (R - 1)), place0 = blockIdx.y * R;
+    // rows of the unit (token * group + head) at these places of its one or two tiles
+    const int f = (place >> 7) * tile_rows + (place & 127), f0 = (place0 >> 7) * tile_rows + (place0 & 127);
+    if (u.count == 0 || (place0 & 127) >= tile_rows || f0 >= rows) {
         griddep_wait();
         griddep_launch();
         return;
     }
-    const TreeRow row = a.rows[r];
-    const int kvh = unit / row.nq * s.hi + s.h0, qt = unit % row.nq;
-    const int rows = min(unit_tokens, row.n - qt * unit_tokens) * a.group, tile_rows = a.tile_tokens * a.group;
-    const int f = (place >> 7) * tile_rows + (place & 127);  // token * group + head within the unit
     const bool live = (place & 127) < tile_rows && f < rows;
+    const int set = warp >> u.groups, sets = WARPS >> u.groups, side = 32 / R, stride = sets * side;
+    const int c0 = (u.group0 + (warp & ((1 << u.groups) - 1))) * COLS;
+    const size_t out_row = ((size_t)u.token + f / a.group) * a.num_qo_heads + u.kvh * a.group + f % a.group;
     griddep_wait();
     griddep_launch();
-    float top = -INFINITY, sum = 0.f;
-    float4 acc[COLS] = {};
-    for (int i0 = set; live && i0 < count; i0 += BATCH * SETS) {
-        float l[BATCH];
-        float4 v[BATCH][COLS];
+    JoinSum j = {-INFINITY, 0.f, {}};
+    for (int i0 = set * side + lane / R; live && i0 < u.count; i0 += kJoinBatch * stride) {
+        float l[kJoinBatch];
+        float4 v[kJoinBatch][COLS];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int at = i0 + i * SETS;
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const int at = i0 + i * stride;
             l[i] = -INFINITY;
-            if (at >= count) continue;
-            const size_t slot = at == 0 ? 2 * b + 1 : 2 * (b + at * lanes);
+            if (at >= u.count) continue;
+            const size_t slot = at == 0 ? 2 * u.cta + 1 : 2 * (u.cta + at * u.step);
             l[i] = __ldcg(a.part_lse + slot * part_rows + place);
 #pragma unroll
             for (int c = 0; c < COLS; ++c) v[i][c] = __ldcg(a.part_o + (slot * C + c0 + c) * part_rows + place);
         }
-        const float before = top;
+        float top = j.top;
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) top = fmaxf(top, l[i]);
-        const float ref = top == -INFINITY ? 0.f : top, keep = before == -INFINITY ? 0.f : exp2f(before - ref);
-        sum *= keep;
+        for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, l[i]);
+        raise_top(j, top);
+        const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) acc[c] = make_float4(acc[c].x * keep, acc[c].y * keep, acc[c].z * keep, acc[c].w * keep);
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            if (i0 + i * SETS >= count) continue;
+        for (int i = 0; i < kJoinBatch; ++i) {
+            if (i0 + i * stride >= u.count) continue;
             const float w = exp2f(l[i] - ref);
-            sum += w;
+            j.sum += w;
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                acc[c].x = fmaf(w, v[i][c].x, acc[c].x);
-                acc[c].y = fmaf(w, v[i][c].y, acc[c].y);
-                acc[c].z = fmaf(w, v[i][c].z, acc[c].z);
-                acc[c].w = fmaf(w, v[i][c].w, acc[c].w);
-            }
+            for (int c = 0; c < COLS; ++c) j.acc[c] = fma4(w, v[i][c], j.acc[c]);
         }
     }
-    if constexpr (SETS > 1) {
-        if (set > 0) {
-            if (c0 == 0) sums[(set - 1) * 32 + lane] = make_float2(top, sum);
+    // parts of a warp with the same rows
+    for (int o = R; o < 32; o <<= 1) {
+        const float top = fmaxf(j.top, __shfl_xor_sync(0xffffffffu, j.top, o));
+        raise_top(j, top);
+        j.sum += __shfl_xor_sync(0xffffffffu, j.sum, o);
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) others[((set - 1) * C + c0 + c) * 32 + lane] = acc[c];
+        for (int c = 0; c < COLS; ++c) {
+            j.acc[c].x += __shfl_xor_sync(0xffffffffu, j.acc[c].x, o);
+            j.acc[c].y += __shfl_xor_sync(0xffffffffu, j.acc[c].y, o);
+            j.acc[c].z += __shfl_xor_sync(0xffffffffu, j.acc[c].z, o);
+            j.acc[c].w += __shfl_xor_sync(0xffffffffu, j.acc[c].w, o);
+        }
+    }
+    if (sets > 1) {
+        if (set > 0) {
+            sums[threadIdx.x] = make_float2(j.top, j.sum);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) others[(warp * COLS + c) * 32 + lane] = j.acc[c];
         }
         __syncthreads();
-        if (set > 0 || !live) return;
-        float all = top;
-#pragma unroll
-        for (int i = 1; i < SETS; ++i) all = fmaxf(all, sums[(i - 1) * 32 + lane].x);
-        const float ref = all == -INFINITY ? 0.f : all, own = exp2f(top - ref);
-        sum *= own;
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) acc[c] = make_float4(acc[c].x * own, acc[c].y * own, acc[c].z * own, acc[c].w * own);
-#pragma unroll
-        for (int i = 1; i < SETS; ++i) {
-            if (i >= count) break;  // (a set without pieces)
-            const float2 e = sums[(i - 1) * 32 + lane];
+        if (set > 0) return;
+        float top = j.top;
+        for (int i = 1; i < sets; ++i) top = fmaxf(top, sums[(i << u.groups) * 32 + threadIdx.x].x);
+        raise_top(j, top);
+        const float ref = top == -INFINITY ? 0.f : top;
+        for (int i = 1; i < sets; ++i) {
+            const int from = (i << u.groups) + warp;
+            const float2 e = sums[from * 32 + lane];
             const float w = exp2f(e.x - ref);
-            sum = fmaf(w, e.y, sum);
+            j.sum = fmaf(w, e.y, j.sum);
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                const float4 v = others[((i - 1) * C + c0 + c) * 32 + lane];
-                acc[c].x = fmaf(w, v.x, acc[c].x);
-                acc[c].y = fmaf(w, v.y, acc[c].y);
-                acc[c].z = fmaf(w, v.z, acc[c].z);
-                acc[c].w = fmaf(w, v.w, acc[c].w);
-            }
+            for (int c = 0; c < COLS; ++c) j.acc[c] = fma4(w, others[(from * COLS + c) * 32 + lane], j.acc[c]);
         }
-        top = all;
     }
-    if (!live) return;
-    const float inv = 1.f / sum;  // (0 / 0 if every key of the row scores -inf)
-    const size_t out_row = ((size_t)row.q_begin + qt * unit_tokens + f / a.group) * a.num_qo_heads + kvh * a.group + f % a.group;
+    if (!live || lane >= R) return;
+    const float inv = 1.f / j.sum;  // (0 / 0 if every key of the row scores -inf)
     uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + 4 * c0);
 #pragma unroll
-    for (int c = 0; c < COLS; c += 2)
-        dst[c / 2] = make_uint4(pack_bf16(acc[c].x * inv, acc[c].y * inv), pack_bf16(acc[c].z * inv, acc[c].w * inv),
-                                pack_bf16(acc[c + 1].x * inv, acc[c + 1].y * inv), pack_bf16(acc[c + 1].z * inv, acc[c + 1].w * inv));
-    if (a.lse && c0 == 0) a.lse[out_row] = (sum == 0.f ? -INFINITY : top + log2f(sum)) * kTrLn2;
+    for (int c = 0; c < COLS; c += 2) {
+        const float4 x = scaled(j.acc[c], inv), y = scaled(j.acc[c + 1], inv);
+        dst[c / 2] = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+    if (a.lse && c0 == 0) a.lse[out_row] = (j.sum == 0.f ? -INFINITY : j.top + log2f(j.sum)) * kTrLn2;
 }
 
-// `whole`: no unit is cut; `units`: at most so many in the step; `rows`: at most so many of a unit.
 template <int D, TreeForm FORM>
-static cudaError_t launch(const TreeArgs &a, int ctas, bool whole, long long units, int rows, const CUtensorMap &tm_kv, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                          const CUtensorMap &tm_q, cudaStream_t st) {
+static cudaError_t launch(const TreeArgs &a, const TreePlan &p, int ctas, const CUtensorMap &tm_kv, const CUtensorMap &tm_k,
+                          const CUtensorMap &tm_v, const CUtensorMap &tm_q, cudaStream_t st) {
     const size_t smem = 1024 + TrSmem<D, FORM>::BYTES;
     cudaError_t e = set_smem_limit((const void *)tree_kernel<D, FORM>, smem, st);
     if (e == cudaSuccess) e = launch_pdl(tree_kernel<D, FORM>, dim3(ctas), dim3(kTrThreads), smem, st, tm_kv, tm_k, tm_v, tm_q, a);
-    if (e != cudaSuccess || ctas == 1 || whole) return e;
-    constexpr int UNIT_TILES = FORM == PAIR ? 2 : 1;
-    const int unit_tokens = a.tile_tokens * UNIT_TILES, part_rows = 128 * UNIT_TILES;
-    const dim3 grid(ctas, rows > a.tile_tokens * a.group ? 8 : (rows + 31) / 32);
-    // units of many pieces: where there are fewer units than half the CTAs
-    constexpr int SETS = D == 256 ? 1 : 256 / D;
-    if (SETS > 1 && 2 * units <= ctas)
-        return launch_pdl(tree_join_kernel<D, SETS>, grid, dim3(JoinShape<D, SETS>::THREADS), 0, st, a, unit_tokens, part_rows);
-    return launch_pdl(tree_join_kernel<D, 1>, grid, dim3(JoinShape<D, 1>::THREADS), 0, st, a, unit_tokens, part_rows);
+    if (e != cudaSuccess || ctas == 1 || p.whole) return e;
+    constexpr int WARPS = D == 64 ? 4 : 8;
+    const dim3 grid(p.join_blocks, p.join_rows), block(32 * p.join_warps);
+    return launch_pdl(p.join_warps == WARPS ? tree_join_kernel<D, WARPS> : tree_join_kernel<D, 2 * WARPS>, grid, block, 0, st, a,
+                      p.part_rows);
 }
 
 }  // namespace dev
@@ -825,6 +828,7 @@ cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm
     a.lse = lse;
     a.rows = reinterpret_cast<const TreeRow *>(w + p.off_rows);
     a.starts = reinterpret_cast<const TreeStart *>(w + p.off_starts);
+    a.joins = reinterpret_cast<const TreeJoin *>(w + p.off_joins);
     a.nodes = reinterpret_cast<const TreeNode *>(w + p.off_nodes);
     a.masks = reinterpret_cast<const unsigned long long *>(w + p.off_masks);
     a.pages = p.pages;
@@ -847,16 +851,13 @@ cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm
     a.box_q = box_q;
     a.q_rows = s.head_dim == 256 && box_q * a.group <= 64 ? 64 : 128;
     a.oob_row = s.num_cache_pages * 2 * s.page_size;
-    const int unit_tokens = a.tile_tokens * (p.pair ? 2 : 1);
-    const int rows = (p.max_new < unit_tokens ? p.max_new : unit_tokens) * a.group;
-    const long long units = (long long)p.batch * s.num_kv_heads * ((p.max_new + unit_tokens - 1) / unit_tokens);
     if (s.head_dim == 64)
-        return p.pair ? dev::launch<64, dev::PAIR>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
-                      : dev::launch<64, dev::SPLIT>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
+        return p.pair ? dev::launch<64, dev::PAIR>(a, p, s.sm_count, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<64, dev::SPLIT>(a, p, s.sm_count, tm_kv, tm_k, tm_v, tm_q, st);
     if (s.head_dim == 128)
-        return p.pair ? dev::launch<128, dev::PAIR>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st)
-                      : dev::launch<128, dev::SPLIT>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
-    return dev::launch<256, dev::TURNS>(a, s.sm_count, p.whole, units, rows, tm_kv, tm_k, tm_v, tm_q, st);
+        return p.pair ? dev::launch<128, dev::PAIR>(a, p, s.sm_count, tm_kv, tm_k, tm_v, tm_q, st)
+                      : dev::launch<128, dev::SPLIT>(a, p, s.sm_count, tm_kv, tm_k, tm_v, tm_q, st);
+    return dev::launch<256, dev::TURNS>(a, p, s.sm_count, tm_kv, tm_k, tm_v, tm_q, st);
 }
 
 }  // namespace pkv

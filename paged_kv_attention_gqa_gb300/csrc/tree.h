@@ -16,8 +16,11 @@ constexpr int kTreeMaxNew = 256;     // most drafted tokens of a row
 constexpr int kTreeMinPage = 8;      // a TMA box fills whole 8-row swizzle atoms
 // What the plan shares out, in thirds of a tile: a tile with two query tiles, or the only one, 3; a pair's unit
 // that reaches into one of its query tiles alone 2 a tile (it is bound by its copies, the others by the MMAs too);
-// a piece as much as two tiles beside its own; and a CTA takes no less than four tiles' worth.
+// a piece as much as two tiles beside its own; and a CTA takes no less than four tiles' worth.  Where units stay whole
+// it takes no less than the smallest unit, so that none has two while others have none (11 rows of 35 drafted
+// tokens 12.6 us with the other bound, 9.1 with this one).
 constexpr int kTreeTileCost = 3, kTreeHalfCost = 2, kTreePieceCost = 6, kTreeLeastCost = 12;
+constexpr int kTreeLeastWhole = kTreePieceCost + kTreeHalfCost;
 static_assert(kTreeLeastCost > kTreePieceCost + kTreeTileCost, "the CTAs' first tiles are all different");
 // Steps leave units whole if their page list holds no more than eight tiles a row (four at head_dim 256, whose tiles take
 // twice as long), of at most four rows, since one row may have all of them: the join of cut units is a kernel
@@ -55,10 +58,29 @@ struct alignas(16) TreeStart {
     int32_t r, unit, tile;
     int32_t r_end, unit_end, tile_end;
     int32_t h0, hi;
-    int32_t tail_count;  // pieces of the unit (r_end, unit_end), hi CTAs apart, if it begins in this CTA
-    int32_t pad[3];
+    int32_t pad[4];
 };
 static_assert(sizeof(TreeStart) == 80, "TreeStart is 80 bytes");
+
+// A block's part of the join of a cut unit: its warps take 2^groups groups of 16 columns each, from group0 on, and
+// what warps there are beside that take the pieces in turn (see tree_joins).
+struct alignas(16) TreeJoin {
+    int32_t token, tokens, kvh;  // the unit's first token in q, their number, its kv head
+    int32_t cta, step, count;    // its pieces: of CTAs cta, cta + step, .. (count 0: nothing to do)
+    int32_t group0, groups;
+};
+static_assert(sizeof(TreeJoin) == 32, "TreeJoin is 8 ints");
+constexpr int kJoinBatch = 2;  // pieces of a thread on their way at once
+// Rows side by side in a warp; units of few rows have their pieces side by side instead.
+PKV_HOST_DEVICE int tree_join_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// log2 of a block's column groups for a unit of `count` pieces: as many as leave all pieces on their way at once.  A
+// unit so has no more blocks than cuts (twice as many at head_dim 256), which bounds them by the CTAs.
+PKV_HOST_DEVICE int tree_join_groups(int head_dim, int warps, int rows, int count) {
+    int groups = 2;
+    while (16 << (groups + 1) <= head_dim && 2 << groups <= warps) ++groups;
+    while (groups > 0 && (warps >> groups) * (32 / tree_join_rows(rows)) * kJoinBatch < count) --groups;
+    return groups;
+}
 
 struct TreeNode {
     int32_t parent, depth;
@@ -77,8 +99,9 @@ struct TreePlan {
     bool pair = false;                     // two query tiles of 128 rows per unit
     bool whole = false;                    // no unit is cut
     int part_rows = 0;                     // rows of a partial
+    int join_warps = 0, join_blocks = 0, join_rows = 0;  // of the join: a block's warps, most records, blocks of a record
     const int32_t *pages = nullptr;        // the caller's page list (device)
-    size_t off_rows = 0, off_starts = 0, off_nodes = 0, off_masks = 0, off_cost = 0, off_part_o = 0,
+    size_t off_rows = 0, off_starts = 0, off_joins = 0, off_nodes = 0, off_masks = 0, off_cost = 0, off_part_o = 0,
            off_part_lse = 0, total = 0;
 };
 

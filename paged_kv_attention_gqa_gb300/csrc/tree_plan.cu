@@ -14,7 +14,7 @@
 // instructions of their addresses: 12.4 us where bulk copies take 9.0).  HBM-bound for batches (each accepted vector
 // read and written once), a chain of loads for one row.
 // Measured: 64 rows of up to 16 nodes, 32 layers of 8 heads of 128, 43 MB: 10.2 us; 40 rows with paths of 20, 24 layers
-// of 4 heads of 64, 16.5 MB: 6.7 us; one row, 32 layers: 2.7 us.  The plan takes 4 to 9 us a step.
+// of 4 heads of 64, 16.5 MB: 6.7 us; one row, 32 layers: 2.7 us.  The plan takes 7 to 10 us a step, its memset included.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -41,9 +41,19 @@ void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_ind
     p.part_rows = p.pair ? 256 : 128;
     const long long whole_tiles = kTreeWholeTiles / (s.head_dim == 256 ? 2 : 1) * std::min(batch, kTreeWholeRows);
     p.whole = (long long)num_indices * s.page_size <= kTreeKeys * whole_tiles;
+    const int tile = tree_tile_tokens(s), unit = tile * (p.pair ? 2 : 1);  // tokens
+    const long long units = (long long)batch * s.num_kv_heads * ((max_new + unit - 1) / unit);
+    const long long most = (long long)s.sm_count * (s.head_dim == 256 ? 2 : 1);
+    p.join_blocks = (int)std::min(units * (s.head_dim / 16), most);
+    p.join_rows = max_new > tile ? 8 : (max_new * s.group() + 31) / 32;
+    // Blocks of twice the warps where two a unit find room side by side: they take more pieces at once (one row of 517
+    // tokens 9.64 us with the small ones, 9.41 with these; one of 64 heads on 4 8.65 and 8.29), but many of them
+    // run in turns (two rows of 52 drafted tokens, head_dim 256, 14.2 and 18.0; wide trees 152 and 159).
+    p.join_warps = (s.head_dim == 64 ? 4 : 8) * (2 * units * p.join_rows <= s.sm_count ? 2 : 1);
     size_t at = kAlign;
     p.off_rows = put(at, (size_t)batch * sizeof(TreeRow));
     p.off_starts = put(at, (size_t)s.sm_count * sizeof(TreeStart));
+    p.off_joins = put(at, (size_t)most * sizeof(TreeJoin));
     p.off_nodes = put(at, (size_t)tokens * sizeof(TreeNode));
     p.off_masks = put(at, (size_t)tokens * p.words * 8);
     p.off_cost = put(at, (size_t)batch * 8);
@@ -58,10 +68,12 @@ struct TreePlanArgs {
     TreeIndex x;
     int batch, tokens, max_new, words, window_left, page_size, page_shift, kv_heads, unit_tokens, tile_tokens, ctas;
     int whole;     // no unit is cut
+    int group, head_dim, join_warps, join_blocks;
     int hi;        // kv heads side by side
     TreeHeader *hdr;
     TreeRow *rows;
     TreeStart *starts;
+    TreeJoin *joins;
     TreeNode *nodes;
     unsigned long long *masks;
     long long *cost;  // before row r, of one kv head
@@ -125,6 +137,7 @@ constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanArgs a) {
     __shared__ int32_t parent[kPlanWarps][kTreeMaxNew];
     __shared__ long long sums[kPlanWarps];
+    __shared__ int joins;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch();
@@ -204,9 +217,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         __syncthreads();
         if (r < a.batch) a.cost[r] = mine + c - v;
     }
+    if (threadIdx.x == 0) joins = 0;
     __syncthreads();
     const int lanes = a.hi, slices = a.ctas / lanes, heads = a.kv_heads / lanes;
-    const long long total = heads * before, share = max((total + slices - 1) / slices, (long long)kTreeLeastCost);
+    const long long total = heads * before, share = max((total + slices - 1) / slices, (long long)(a.whole ? kTreeLeastWhole : kTreeLeastCost));
     for (int c = threadIdx.x; c < a.ctas; c += kPlanThreads) {
         TreeStart s = {};
         const int slice = c / lanes;
@@ -255,9 +269,28 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         s.r_end = to.r;
         s.unit_end = to.unit;
         s.tile_end = to.tile;
-        s.tail_count = (int)(to.last - to.first) + 1;
         a.starts[c] = s;
+        // the unit that goes on in the next CTA, if it begins here
+        if (to.r < a.batch && to.tile > 0 && (from.r != to.r || from.unit != to.unit || from.tile == 0)) {
+            const TreeRow t = a.rows[to.r];
+            const int q = to.unit % t.nq;
+            TreeJoin j;
+            j.token = t.q_begin + q * a.unit_tokens;
+            j.tokens = min(a.unit_tokens, t.n - q * a.unit_tokens);
+            j.kvh = to.unit / t.nq * lanes + s.h0;
+            j.cta = c;
+            j.step = lanes;
+            j.count = (int)(to.last - to.first) + 1;
+            j.groups = tree_join_groups(a.head_dim, a.join_warps, j.tokens * a.group, j.count);
+            const int blocks = a.head_dim / 16 >> j.groups, at = atomicAdd(&joins, blocks);
+            for (int i = 0; i < blocks; ++i) {
+                j.group0 = i << j.groups;
+                if (at + i < a.join_blocks) a.joins[at + i] = j;
+            }
+        }
     }
+    __syncthreads();
+    for (int i = joins + threadIdx.x; i < a.join_blocks; i += kPlanThreads) a.joins[i].count = 0;
 }
 
 struct AcceptArgs {
@@ -380,6 +413,11 @@ cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex 
     a.hdr = reinterpret_cast<TreeHeader *>(w);
     a.rows = reinterpret_cast<TreeRow *>(w + p.off_rows);
     a.starts = reinterpret_cast<TreeStart *>(w + p.off_starts);
+    a.joins = reinterpret_cast<TreeJoin *>(w + p.off_joins);
+    a.group = s.group();
+    a.head_dim = s.head_dim;
+    a.join_warps = p.join_warps;
+    a.join_blocks = p.join_blocks;
     a.nodes = reinterpret_cast<TreeNode *>(w + p.off_nodes);
     a.masks = reinterpret_cast<unsigned long long *>(w + p.off_masks);
     a.cost = reinterpret_cast<long long *>(w + p.off_cost);

@@ -225,7 +225,7 @@ def test_mistakes_are_caught(form, plant):
 
 # ---------------------------------------------------------------- the plan's shares
 
-TILE, HALF, PIECE, LEAST = 3, 2, 6, 12  # costs, in thirds of a tile
+TILE, HALF, PIECE, LEAST, LEAST_WHOLE = 3, 2, 6, 12, 8  # costs, in thirds of a tile
 
 
 class Row:
@@ -254,7 +254,7 @@ def plan(rows, kv_heads, ctas, whole):
     for r in rows:
         before.append(before[-1] + heads * r.head())
     total, starts = before.pop(), []
-    share = max(-(-total // slices), LEAST)
+    share = max(-(-total // slices), LEAST_WHOLE if whole else LEAST)
     for c in range(ctas):
         piece = c // lanes
 
@@ -275,6 +275,14 @@ def plan(rows, kv_heads, ctas, whole):
         a, b = (place((piece + i) * share if piece < slices else total) for i in (0, 1))
         starts.append(dict(cta=c, lane=c % lanes, begin=a[0], end=b[0], tail=b[2] - b[1] + 1, lanes=lanes))
     return starts
+
+
+def join_blocks(dim, warps, rows, count):
+    """Blocks of the join of a unit: two pieces of a thread on their way at once."""
+    groups, side = min(dim // 16, warps).bit_length() - 1, 4 if rows <= 8 else 2 if rows <= 16 else 1
+    while groups and (warps >> groups) * side * 2 < count:
+        groups -= 1
+    return (dim // 16) >> groups
 
 
 def pieces(rows, kv_heads, s):
@@ -324,3 +332,9 @@ def test_shares_and_joins(ctas):
             assert parts[0][0] == 0 and parts[-1][1] == rows[what[0]].tiles(what[2])
             assert all(a[1] == b[0] for a, b in zip(parts, parts[1:]))
             assert joined.get(what) == ([p[2] for p in parts] if len(parts) > 1 else None)
+        for dim, warps in ((64, 4), (64, 8), (128, 8), (128, 16), (256, 8), (256, 16)):  # the joins' records fit their list
+            blocks = sum(join_blocks(dim, warps, rng.choice([4, 8, 9, 128]), len(mine)) for mine in joined.values())
+            assert blocks <= ctas * (2 if dim == 256 else 1)
+        lanes = starts[0]["lanes"]
+        if whole and kv_heads // lanes * sum(r.head() for r in rows) <= LEAST_WHOLE * (ctas // lanes):
+            assert all(len(pieces(rows, kv_heads, s)) <= 1 for s in starts), "units that stay whole, one a CTA"
