@@ -24,7 +24,7 @@
 //    one ring of 16 KB stages (8 at head_dim 64, 32 at 256): one lane a box of a page and 64 columns.
 //  * warp 9 issues S = Q K^T, warp 10 O += P V (P from tensor memory, over its S).
 //  * A key that a row does not see has weight 0, but 0 * NaN would reach O.  Those that no row sees are
-//    zeroed in shared memory by warp 10; a tile with keys that some rows see and others do not is
+//    left out by 16s or zeroed in shared memory by warp 10; a tile with keys that some rows see and others do not is
 //    looked over by it, and if it holds NaN or infinities each row adds the keys it sees alone.
 //  * The running maximum moves (and O is rescaled) only when it grows by more than 2^8.  Maxima and
 //    sums are 32-bit; P is rounded to bf16 for the MMA (relative 2^-8 a weight at most), the sum adds it unrounded.
@@ -406,30 +406,32 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 ok = mbar_wait(&kv_full[s], (i / NS) & 1, err, kErrWaitFull);
                 if (!ok) break;
                 uint8_t *const tile = sm + L::RING_OFF + s * L::STAGE;
-                const int steps = (k.keys + 15) / 16;  // k-steps of 16 keys
+                // k-steps of 16 keys, without those that no row sees (one at least: it may be the one that begins O)
+                const int steps = (k.keys + 15) / 16, step0 = min(k.first / 16, steps - 1);
                 bool rows = false;
                 if (k.special) {
-                    // keys that no row sees: their P is 0, but 0 * NaN would reach O
-                    const int n_zero = k.first + steps * 16 - k.keys;
+                    // the other keys that no row sees: their P is 0, but 0 * NaN would reach O
+                    const int before = k.first - step0 * 16, n_zero = before + steps * 16 - k.keys;
                     for (int e = lane; e < n_zero * (D / 8); e += 32) {
-                        const int n = e / (D / 8), c = e % (D / 8), key = n < k.first ? n : k.keys + n - k.first;
+                        const int n = e / (D / 8), c = e % (D / 8), key = n < before ? step0 * 16 + n : k.keys + n - before;
                         *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::HALF + swz128(key, c & 7)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
+                    __syncwarp();
+                    // Keys from a multiple of eight on (those before were zeroed): a lane has every eighth of them and every fourth
+                    // 16-byte chunk, so that its addresses differ by constants (one row of 119 drafted tokens of head_dim 256 14.4
+                    // -> 13.4 us, the mean of 48 steps 14.7 -> 14.5; looked over by the tile's softmax group 12.5, but
+                    // that slowed the loop of ordinary tiles by 3 % at head_dim 64; eight sums for two: 14.9)
                     uint32_t f0 = 0, f1 = 0;
-                    const int n = (k.mixed1 - k.mixed0) * (D / 8);
-                    for (int e0 = lane; e0 < n; e0 += 4 * 32) {  // four vectors in flight
-                        uint4 v[4];
+                    const uint8_t *const even = tile + swz128(lane >> 2, lane & 3), *const odd = tile + swz128(lane >> 2, 4 + (lane & 3));
+#pragma unroll (4 / HALVES)
+                    for (int key = k.mixed0 & ~7; key < k.mixed1; key += 8) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int e = min(e0 + 32 * u, n - 1), c = e % (D / 8);
-                            v[u] = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * L::HALF +
-                                                                    swz128(k.mixed0 + e / (D / 8), c & 7));
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            f0 = keep_nonfinite(v[u].x, keep_nonfinite(v[u].y, f0));
-                            f1 = keep_nonfinite(v[u].z, keep_nonfinite(v[u].w, f1));
+                        for (int h = 0; h < HALVES; ++h) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(even + key * 128 + h * L::HALF);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(odd + key * 128 + h * L::HALF);
+                            f0 = keep_nonfinite(v.x, keep_nonfinite(v.y, keep_nonfinite(v.z, keep_nonfinite(v.w, f0))));
+                            f1 = keep_nonfinite(w.x, keep_nonfinite(w.y, keep_nonfinite(w.z, keep_nonfinite(w.w, f1))));
                         }
                     }
                     rows = __any_sync(0xffffffffu, has_nan(f0) || has_nan(f1));
@@ -451,13 +453,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (!rows) {
                         const uint64_t v = add(dV, s * L::STAGE);
                         const uint32_t more = j >= (FORM == SPLIT ? 2 : 1) ? 1u : 0u;  // not the group's first tile
-                        if (steps == kTreeKeys / 16) {
+                        if (steps == kTreeKeys / 16 && step0 == 0) {
 #pragma unroll
                             for (int kk = 0; kk < kTreeKeys / 16; ++kk)
                                 mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, kk > 0 ? 1u : more);
                         } else {
-                            for (int kk = 0; kk < steps; ++kk)
-                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, kk > 0 ? 1u : more);
+                            for (int kk = step0; kk < steps; ++kk)
+                                mma_ts_elect(O_col(x), S_col(x, b) + kk * 8, add(v, kk * 2048), ID_O, kk > step0 ? 1u : more);
                         }
                     }
                     mma_commit_elect(&pv_done[2 * x + b]);
