@@ -93,7 +93,7 @@ extern "C" pkv_status pkv_workspace_size(pkv_handle_t h, int mode, size_t *bytes
         return fail(h, PKV_ERR_INVALID, "unknown mode");
     if (mode == PKV_MODE_TREE) {
         pkv::TreePlan p;
-        pkv::tree_layout(h->shape, h->shape.max_batch, h->shape.max_total_tokens, pkv::kTreeMaxNew, h->shape.max_num_pages, p);
+        pkv::tree_layout(h->shape, h->shape.max_batch, h->shape.max_total_tokens, pkv::kTreeMaxNew, h->shape.max_num_pages, -1, p);
         *bytes = p.total;
         return PKV_OK;
     }

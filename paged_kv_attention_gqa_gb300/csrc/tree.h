@@ -26,7 +26,10 @@ static_assert(kTreeLeastCost > kTreePieceCost + kTreeTileCost, "the CTAs' first 
 // twice as long), of at most four rows, since one row may have all of them: the join of cut units is a kernel
 // more, 2 us, in which a CTA goes through eight tiles.  (Steps of one to 63 short rows 6.8 to 16.2 us cut,
 // 5.6 to 13.2 whole; one row of 517 tokens 9.5 cut, 10.5 whole.)
-constexpr int kTreeWholeTiles = 8, kTreeWholeRows = 4;
+// So do steps of up to two units a CTA whose window leaves each so few tiles, whatever the page list holds (40 windowed
+// steps 10.8 us in the mean cut, 10.4 with one unit a CTA at most, 10.3 with two; 33 rows of 4 heads under a window of
+// 127 tokens 12.3 and 8.2, but one row of 198 drafted tokens 10.4 and 12.0).
+constexpr int kTreeWholeTiles = 8, kTreeWholeRows = 4, kTreeWholeUnits = 2;
 constexpr int kMapsMaxRows = 8192;   // rows whose offsets fit the shared memory of the maps kernel
 
 // Device error words of the speculative step (beside those of the bounded waits in ptx.cuh).
@@ -108,7 +111,7 @@ struct TreePlan {
 // Query tokens of one 128-row tile.
 inline int tree_tile_tokens(const Shape &s) { return 128 / s.group(); }
 // The workspace of a step of `batch` rows, `tokens` tokens and up to `max_new` a row.
-void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_indices, TreePlan &p);
+void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_indices, int window_left, TreePlan &p);
 
 struct TreeIndex {  // device arrays
     const int32_t *qo, *kvp, *kvi, *last, *parents;

@@ -115,14 +115,13 @@ extern "C" pkv_status pkv_plan_tree(pkv_handle_t h, const int32_t *qo_indptr, co
         if ((bits(qo_indptr) | bits(kv_indptr) | bits(kv_indices) | bits(last_page_len) | bits(parents) | bits(positions)) % 4)
             return fail(h, PKV_ERR_INVALID, "index arrays must be 4-byte aligned");
         TreePlan p;
-        pkv::tree_layout(s, batch, num_tokens, max_new, num_indices, p);
+        pkv::tree_layout(s, batch, num_tokens, max_new, num_indices, window_left, p);
         h->planned_ws = nullptr;
         if (p.total > workspace_bytes)
             return fail(h, PKV_ERR_WORKSPACE,
                         "workspace of " + std::to_string(workspace_bytes) + " bytes is too small: this plan needs " +
                             std::to_string(p.total) + " bytes (pkv_workspace_size gives the bound at the maxima)");
-        p.window_left = window_left;
-        p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.f / std::sqrt((float)s.head_dim)) * 1.4426950408889634f;
+            p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.f / std::sqrt((float)s.head_dim)) * 1.4426950408889634f;
         p.pages = kv_indices;
         const pkv::TreeIndex x{qo_indptr, kv_indptr, kv_indices, last_page_len, parents, num_indices, positions};
         const cudaError_t e = pkv::launch_tree_plan(s, p, x, workspace, static_cast<cudaStream_t>(stream));

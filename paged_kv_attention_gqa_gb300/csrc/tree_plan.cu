@@ -31,7 +31,8 @@ static size_t put(size_t &at, size_t bytes) {
     return here;
 }
 
-void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_indices, TreePlan &p) {
+void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_indices, int window_left, TreePlan &p) {
+    p.window_left = window_left;
     p.batch = batch;
     p.num_tokens = tokens;
     p.max_new = max_new;
@@ -39,10 +40,14 @@ void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_ind
     // head_dim 256 has no tensor memory for two query tiles' accumulators
     p.pair = s.head_dim <= 128 && max_new * s.group() > 128;
     p.part_rows = p.pair ? 256 : 128;
-    const long long whole_tiles = kTreeWholeTiles / (s.head_dim == 256 ? 2 : 1) * std::min(batch, kTreeWholeRows);
-    p.whole = (long long)num_indices * s.page_size <= kTreeKeys * whole_tiles;
     const int tile = tree_tile_tokens(s), unit = tile * (p.pair ? 2 : 1);  // tokens
     const long long units = (long long)batch * s.num_kv_heads * ((max_new + unit - 1) / unit);
+    const int whole_tiles = kTreeWholeTiles / (s.head_dim == 256 ? 2 : 1);
+    p.whole = (long long)num_indices * s.page_size <= kTreeKeys * whole_tiles * std::min(batch, kTreeWholeRows);
+    if (window_left >= 0 && units <= kTreeWholeUnits * s.sm_count) {
+        const long long cached = ((long long)window_left + kTreeKeys - 1) / kTreeKeys + 1;  // tiles at most
+        p.whole = p.whole || cached + (max_new + kTreeKeys - 1) / kTreeKeys <= whole_tiles;
+    }
     const long long most = (long long)s.sm_count * (s.head_dim == 256 ? 2 : 1);
     p.join_blocks = (int)std::min(units * (s.head_dim / 16), most);
     p.join_rows = max_new > tile ? 8 : (max_new * s.group() + 31) / 32;
