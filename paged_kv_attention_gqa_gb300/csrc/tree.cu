@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(32 * WARPS) tree_join_kernel(const TreeArgs a,
     // the plan was complete before the attention kernel let this one start
     const TreeJoin u = a.joins[blockIdx.x];
     const int rows = u.tokens * a.group, tile_rows = a.tile_tokens * a.group;
-    const int R = tree_join_rows(rows), place = blockIdx.y * R + (lane & (R - 1)), place0 = blockIdx.y * R;
+    const int R = u.rows, place0 = blockIdx.y * tree_join_rows(rows) + u.row0, place = place0 + (lane & (R - 1));
     // rows of the unit (token * group + head) at these places of its one or two tiles
     const int f = (place >> 7) * tile_rows + (place & 127), f0 = (place0 >> 7) * tile_rows + (place0 & 127);
     if (u.count == 0 || (place0 & 127) >= tile_rows || f0 >= rows) {

@@ -65,24 +65,35 @@ struct alignas(16) TreeStart {
 };
 static_assert(sizeof(TreeStart) == 80, "TreeStart is 80 bytes");
 
-// A block's part of the join of a cut unit: its warps take 2^groups groups of 16 columns each, from group0 on, and
-// what warps there are beside that take the pieces in turn (see tree_joins).
+// A block's part of the join of a cut unit: 2^groups groups of 16 columns from group0 on, and of every 32 rows (or 16 or
+// 8, if the unit has no more) `rows` from row0 on.  Its warps and what places they have beside that take the
+// pieces in turn.
 struct alignas(16) TreeJoin {
     int32_t token, tokens, kvh;  // the unit's first token in q, their number, its kv head
     int32_t cta, step, count;    // its pieces: of CTAs cta, cta + step, .. (count 0: nothing to do)
-    int32_t group0, groups;
+    int16_t group0, groups, row0, rows;
 };
-static_assert(sizeof(TreeJoin) == 32, "TreeJoin is 8 ints");
+static_assert(sizeof(TreeJoin) == 32, "two vectors");
 constexpr int kJoinBatch = 2;  // pieces of a thread on their way at once
-// Rows side by side in a warp; units of few rows have their pieces side by side instead.
 PKV_HOST_DEVICE int tree_join_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
-// log2 of a block's column groups for a unit of `count` pieces: as many as leave all pieces on their way at once.  A
-// unit so has no more blocks than cuts (twice as many at head_dim 256), which bounds them by the CTAs.
-PKV_HOST_DEVICE int tree_join_groups(int head_dim, int warps, int rows, int count) {
-    int groups = 2;
-    while (16 << (groups + 1) <= head_dim && 2 << groups <= warps) ++groups;
-    while (groups > 0 && (warps >> groups) * (32 / tree_join_rows(rows)) * kJoinBatch < count) --groups;
-    return groups;
+// The part of a block for a unit of `count` pieces: as much as leaves all pieces on their way at once, columns before
+// rows (one row of 130,000 tokens among 99 of 500, 8 heads on one of 128: 50 us where every unit of a step has the same
+// number of warps, 24 so; 60,000 among 39, 64 query rows a head of 64: 23.8 by columns alone, 16.3).  A unit so has no more blocks (a multiple of 32 rows each) than cuts, twice as many at head_dim 256, which bounds
+// them by the CTAs.
+struct TreeJoinPart {
+    int groups, rows;
+};
+PKV_HOST_DEVICE TreeJoinPart tree_join_part(int head_dim, int warps, int rows, int count) {
+    TreeJoinPart p{2, tree_join_rows(rows)};
+    while (16 << (p.groups + 1) <= head_dim && 2 << p.groups <= warps) ++p.groups;
+    int room = (warps >> p.groups) * (32 / p.rows) * kJoinBatch;
+    for (; room < count && (p.groups > 0 || p.rows > 8); room *= 2) {
+        if (p.groups > 0)
+            --p.groups;
+        else
+            p.rows /= 2;
+    }
+    return p;
 }
 
 struct TreeNode {

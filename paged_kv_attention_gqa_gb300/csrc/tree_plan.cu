@@ -49,7 +49,7 @@ void tree_layout(const Shape &s, int batch, int tokens, int max_new, int num_ind
         p.whole = p.whole || cached + (max_new + kTreeKeys - 1) / kTreeKeys <= whole_tiles;
     }
     const long long most = (long long)s.sm_count * (s.head_dim == 256 ? 2 : 1);
-    p.join_blocks = (int)std::min(units * (s.head_dim / 16), most);
+    p.join_blocks = (int)std::min(units * (s.head_dim / 16) * 4, most);
     p.join_rows = max_new > tile ? 8 : (max_new * s.group() + 31) / 32;
     // Blocks of twice the warps where two a unit find room side by side: they take more pieces at once (one row of 517
     // tokens 9.64 us with the small ones, 9.41 with these; one of 64 heads on 4 8.65 and 8.29), but many of them
@@ -286,10 +286,14 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
             j.cta = c;
             j.step = lanes;
             j.count = (int)(to.last - to.first) + 1;
-            j.groups = tree_join_groups(a.head_dim, a.join_warps, j.tokens * a.group, j.count);
-            const int blocks = a.head_dim / 16 >> j.groups, at = atomicAdd(&joins, blocks);
+            const TreeJoinPart part = tree_join_part(a.head_dim, a.join_warps, j.tokens * a.group, j.count);
+            j.groups = (int16_t)part.groups;
+            j.rows = (int16_t)part.rows;
+            const int columns = a.head_dim / 16 >> part.groups, blocks = columns * (tree_join_rows(j.tokens * a.group) / part.rows);
+            const int at = atomicAdd(&joins, blocks);
             for (int i = 0; i < blocks; ++i) {
-                j.group0 = i << j.groups;
+                j.group0 = (int16_t)(i % columns << part.groups);
+                j.row0 = (int16_t)(i / columns * part.rows);
                 if (at + i < a.join_blocks) a.joins[at + i] = j;
             }
         }

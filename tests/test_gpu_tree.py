@@ -163,6 +163,14 @@ def test_cut_units(sm_count, D, H, n):
     step([2500, 0, 700, 64, 5000], [R.tree(n, 3, r) for r in range(5)], H, 2, D, 16, sm_count + D, sm_count=sm_count)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 20])
+@pytest.mark.parametrize("D,H,n", [(64, 3, 2), (64, 5, 3), (128, 8, 1), (128, 6, 2), (256, 4, 4), (256, 7, 2), (128, 8, 17)])
+def test_long_rows_cut_into_many_pieces(D, H, n, rows):
+    """One kv head, a row of 400 tiles and short ones: a unit of up to 150 pieces with 6 to 136 query rows, joined side by
+    side in a warp, by several warps and in several rounds."""
+    step([25600] + [70] * (rows - 1), [R.tree(n, 2, r) for r in range(rows)], H, 1, D, 64, 60 + D + H)
+
+
 @pytest.mark.parametrize("window", [0, 1, 2, 5, 63, 64, 100, 1000])
 @pytest.mark.parametrize("D,n", [(64, 30), (128, 90), (256, 20)])
 def test_windows(window, D, n):

@@ -280,9 +280,10 @@ def plan(rows, kv_heads, ctas, whole):
 def join_blocks(dim, warps, rows, count):
     """Blocks of the join of a unit: two pieces of a thread on their way at once."""
     groups, side = min(dim // 16, warps).bit_length() - 1, 4 if rows <= 8 else 2 if rows <= 16 else 1
-    while groups and (warps >> groups) * side * 2 < count:
-        groups -= 1
-    return (dim // 16) >> groups
+    room, cut = (warps >> groups) * side * 2, 1  # cut: blocks that share rows
+    while room < count and (groups or side < 4):
+        groups, side, cut, room = (groups - 1, side, cut, 2 * room) if groups else (0, 2 * side, 2 * cut, 2 * room)
+    return cut * ((dim // 16) >> groups)
 
 
 def pieces(rows, kv_heads, s):
