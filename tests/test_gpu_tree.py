@@ -216,6 +216,11 @@ def test_long_row():
     step([40000], [R.tree(6, 2)], 4, 1, 64, 64, 14)
 
 
+def test_thousands_of_rows():
+    """More units than CTAs by far, rows without tokens among them, units of one query row."""
+    step([r % 90 for r in range(2500)], [R.tree(r % 4, 2, r) for r in range(2500)], 2, 1, 64, 16, 51)
+
+
 def test_a_larger_bound_of_drafted_tokens():
     """max_new says how many there may be at most, not how many there are."""
     for most in (9, 64, 65, 256):
