@@ -30,9 +30,9 @@
 //    sums are 32-bit; P is rounded to bf16 for the MMA (relative 2^-8 a weight at most), the sum adds it unrounded.
 // Measured (32 or 64 query heads on 8 kv heads of 128 unless said): one row of 517 tokens, 8 drafted: 9.4 us; 32 rows
 // of 203 to 8,190, 16 drafted: 94 us, 557 MB, at the copy rate between start and end; 16 rows of 611 to 12,001, 61
-// drafted, 64 query heads: 149 us, 998 TFLOP/s (159 held under the power cap) (S with both operands in shared memory takes 48 cycles a k-step for
-// 32: 1,280 of 1,700 cycles a tile of two query tiles); 3 chains of 5 behind 30,011 to 65,521 tokens, 20 heads on 4
-// of 64: 38 us; 24 rows of head_dim 256 under a window of 2,047: 71 us.
+// drafted, 64 query heads: 149 us, 998 TFLOP/s (159 us held under the power cap; S with both operands in shared memory
+// takes 48 cycles a k-step for 32: 1,280 of 1,700 cycles a tile of two query tiles); 3 chains of 5 behind 30,011 to
+// 65,521 tokens, 20 heads on 4 of 64: 38 us; 24 rows of head_dim 256 under a window of 2,047: 71 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
