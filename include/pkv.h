@@ -282,7 +282,8 @@ pkv_status pkv_gather_kv(pkv_handle_t h, const void *kv_layer, const int32_t *pa
 
 /*
  * Read and clear the workspace's device error word (synchronises `stream`).
- * PKV_OK when no kernel recorded an error since the last plan on it.
+ * PKV_OK when no kernel recorded an error since the last plan on it (since the last such call, where the plans are
+ * pkv_plan_tree's: see there).
  */
 pkv_status pkv_check_device_error(pkv_handle_t h, void *workspace, pkv_stream_t stream, int *code);
 
@@ -384,8 +385,11 @@ pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t 
  * CUDA graph (after one uncaptured call of each), which then serves every step whose sizes stay within
  * the captured ones.  Arrays that the kernels find inconsistent are skipped and reported:
  * pkv_build_maps by its status, the others by pkv_check_device_error, code 5 (a row's index arrays do
- * not agree, or it begins below an earlier row's first token: the row counts as empty), 6 (a page id outside the cache: read as zeros, not written) or
- * 7 (a parent that does not stand before its child: taken as -1).
+ * not agree, or it begins below an earlier row's first token: the row counts as empty), 6 (a page id outside the cache:
+ * read as zeros, not written; the row's length counts its tokens all the same) or 7 (a parent that does not stand before
+ * its child: taken as -1).  The first error since the last pkv_check_device_error stays in the workspace until that reads
+ * it, whatever steps this handle plans or replays there in between; a plan of another kind, or of another handle, on the
+ * same workspace ends it.  pkv_build_maps's status is of each call alone.
  */
 
 /*

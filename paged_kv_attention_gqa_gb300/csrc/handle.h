@@ -37,6 +37,7 @@ struct pkv_handle_s {
     pkv::WeightsPlan weights;  // the score arrays of DECODE_WEIGHTS / WEIGHTS plans
     pkv::EvictPlan evict;      // EVICT plans
     pkv::TreePlan tree;        // TREE plans
+    uint32_t tree_tag = 0;     // of their error words: the handle's own
     void *planned_ws = nullptr;
     PkvStaging staging;
     // side stream + fork/join events of the mixed step's concurrent passes

@@ -35,9 +35,13 @@ constexpr int kMapsMaxRows = 8192;   // rows whose offsets fit the shared memory
 // Device error words of the speculative step (beside those of the bounded waits in ptx.cuh).
 enum TreeError : int { kErrTreeRow = 5, kErrTreePage = 6, kErrTreeParent = 7 };
 
-struct TreeHeader {
-    int32_t err;  // the device error word
+// Errors outlive the plans behind them: a step that is replayed without the host would otherwise lose all but the
+// last one's.  `tag` tells a word that this handle's plans have begun from whatever else the memory held.
+struct alignas(8) TreeHeader {
+    int32_t err;  // the device error word: the first error since it was read
+    uint32_t tag;
 };
+static_assert(sizeof(TreeHeader) == 8, "changed as one 64-bit word");
 
 // One row as the plan read it.  A row without drafted tokens, or an inconsistent one, has n = nq = 0.
 struct alignas(16) TreeRow {
@@ -129,7 +133,7 @@ struct TreeIndex {  // device arrays
     int num_indices;
     int32_t *positions;
 };
-cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex &x, void *ws, cudaStream_t st);
+cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex &x, uint32_t tag, void *ws, cudaStream_t st);
 // `tm_kv`: boxes of 64 columns x min(page_size, 64) slots of the layer slice; `tm_k`, `tm_v`: of 64 columns x
 // box_new rows of the new keys and values; `tm_q`: of 64 columns x the group's heads x box_q tokens.
 cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm_kv, const CUtensorMap &tm_k,

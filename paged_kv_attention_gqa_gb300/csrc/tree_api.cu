@@ -1,6 +1,7 @@
 // The C ABI of the speculative step (pkv_build_maps, pkv_plan_tree, pkv_run_tree, pkv_run_accept in
 // include/pkv.h): checks, tensor maps, launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <exception>
 
@@ -29,6 +30,13 @@ static pkv_status guarded(pkv_handle_t h, F &&f) {
         h->err.clear();
         return PKV_ERR_INVALID;
     }
+}
+
+// The handle's mark in a workspace.  A negative number as an integer, since other plans' words there are counts.
+static uint32_t tag(pkv_handle_t h) {
+    static std::atomic<uint32_t> handles{0};
+    if (!h->tree_tag) h->tree_tag = 0x80000000u | handles.fetch_add(1) * 0x9e3779b1u;
+    return h->tree_tag;
 }
 
 static uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
@@ -124,7 +132,7 @@ extern "C" pkv_status pkv_plan_tree(pkv_handle_t h, const int32_t *qo_indptr, co
             p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.f / std::sqrt((float)s.head_dim)) * 1.4426950408889634f;
         p.pages = kv_indices;
         const pkv::TreeIndex x{qo_indptr, kv_indptr, kv_indices, last_page_len, parents, num_indices, positions};
-        const cudaError_t e = pkv::launch_tree_plan(s, p, x, workspace, static_cast<cudaStream_t>(stream));
+        const cudaError_t e = pkv::launch_tree_plan(s, p, x, tag(h), workspace, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(h, e, "tree plan launch");
         pkv::Plan plan;
         plan.mode = PKV_MODE_TREE;

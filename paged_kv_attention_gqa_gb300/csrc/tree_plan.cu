@@ -14,7 +14,9 @@
 // instructions of their addresses: 12.4 us where bulk copies take 9.0).  HBM-bound for batches (each accepted vector
 // read and written once), a chain of loads for one row.
 // Measured: 64 rows of up to 16 nodes, 32 layers of 8 heads of 128, 43 MB: 10.2 us; 40 rows with paths of 20, 24 layers
-// of 4 heads of 64, 16.5 MB: 6.7 us; one row, 32 layers: 2.7 us.  The plan takes 7 to 10 us a step, its memset included.
+// of 4 heads of 64, 16.5 MB: 6.7 us; one row, 32 layers: 2.7 us.  The plan of 1 to
+// 64 rows takes 3.4 to 7.1 us with trees of up to 61 nodes, 100 us with chains of 200: a lane walks its nodes to the root,
+// a load after the other.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -76,6 +78,7 @@ struct TreePlanArgs {
     int group, head_dim, join_warps, join_blocks;
     int hi;        // kv heads side by side
     TreeHeader *hdr;
+    uint32_t tag;  // the handle's
     TreeRow *rows;
     TreeStart *starts;
     TreeJoin *joins;
@@ -83,6 +86,20 @@ struct TreePlanArgs {
     unsigned long long *masks;
     long long *cost;  // before row r, of one kv head
 };
+
+// Records an error (0: begins the error word).  The plan's blocks do so in any order, so each leaves a word with the
+// handle's tag behind; what a word with another tag says is no error of this handle's.
+__device__ __forceinline__ void plan_error(const TreePlanArgs &a, int code) {
+    unsigned long long *const word = reinterpret_cast<unsigned long long *>(a.hdr);
+    const unsigned long long mine = (unsigned long long)a.tag << 32;
+    unsigned long long old = *reinterpret_cast<volatile unsigned long long *>(word);
+    // three tries do: other blocks of a plan change the word once from a foreign one, and once from no error to one
+    for (int i = 0; i < 4 && ((old >> 32) != a.tag || (code != 0 && (uint32_t)old == 0)); ++i) {
+        const unsigned long long seen = atomicCAS(word, old, mine | (uint32_t)code);
+        if (seen == old) break;
+        old = seen;
+    }
+}
 
 // A row's first token, 0 if that is no token of the step; and the highest of the rows [from, to), for the whole warp.
 __device__ __forceinline__ int first_token(const TreePlanArgs &a, int r) {
@@ -156,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         for (int i = lane; i < t.n; i += 32) {
             int32_t up = a.x.parents ? a.x.parents[t.q_begin + i] : i - 1;
             if (up < -1 || up >= i) {
-                atomicCAS(&a.hdr->err, 0, kErrTreeParent);
+                plan_error(a, kErrTreeParent);
                 up = -1;
             }
             p[i] = up;
@@ -186,6 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         return;
     }
     // ------------------------------------------------ the rows, and each CTA's share
+    if (threadIdx.x == kPlanThreads - 1) plan_error(a, 0);  // (of the warp that most often has no row)
     long long before = 0;
     int highest = 0, known = 0;  // of the rows before `known`
     for (int r0 = 0; r0 < a.batch; r0 += kPlanThreads) {
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlanA
         if (r < a.batch) {
             bool ok;
             const TreeRow t = tree_row(a, r, max(highest, top), ok);
-            if (!ok) atomicCAS(&a.hdr->err, 0, kErrTreeRow);
+            if (!ok) plan_error(a, kErrTreeRow);
             a.rows[r] = t;
             v = head_cost(a, t);
         }
@@ -401,10 +419,8 @@ __global__ void __launch_bounds__(kAcceptThreads, kAcceptCtas) tree_accept_kerne
 
 }  // namespace dev
 
-cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex &x, void *ws, cudaStream_t st) {
+cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex &x, uint32_t tag, void *ws, cudaStream_t st) {
     uint8_t *w = static_cast<uint8_t *>(ws);
-    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(TreeHeader), st);  // the blocks record errors in any order
-    if (e != cudaSuccess) return e;
     dev::TreePlanArgs a;
     a.x = x;
     a.batch = p.batch;
@@ -420,6 +436,7 @@ cudaError_t launch_tree_plan(const Shape &s, const TreePlan &p, const TreeIndex 
     a.ctas = s.sm_count;
     a.whole = p.whole;
     a.hdr = reinterpret_cast<TreeHeader *>(w);
+    a.tag = tag;
     a.rows = reinterpret_cast<TreeRow *>(w + p.off_rows);
     a.starts = reinterpret_cast<TreeStart *>(w + p.off_starts);
     a.joins = reinterpret_cast<TreeJoin *>(w + p.off_joins);
