@@ -382,7 +382,7 @@ pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t 
  * alone, so the step's index arrays are DEVICE arrays and no call waits for the device or reads them on
  * the host: pkv_build_maps (pages, page lists, slots), pkv_plan_tree, pkv_run_tree for every layer,
  * pkv_run_accept, and the next step's pkv_build_maps from the new lengths.  All four may be captured into one
- * CUDA graph (after one uncaptured call of each), which then serves every step whose sizes stay within
+ * CUDA graph (after one uncaptured call of each, of any size), which then serves every step whose sizes stay within
  * the captured ones.  Arrays that the kernels find inconsistent are skipped and reported:
  * pkv_build_maps by its status, the others by pkv_check_device_error, code 5 (a row's index arrays do
  * not agree, or it begins below an earlier row's first token: the row counts as empty), 6 (a page id outside the cache:

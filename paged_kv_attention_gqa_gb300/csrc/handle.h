@@ -38,6 +38,7 @@ struct pkv_handle_s {
     pkv::EvictPlan evict;      // EVICT plans
     pkv::TreePlan tree;        // TREE plans
     uint32_t tree_tag = 0;     // of their error words: the handle's own
+    int tree_ready = -1, maps_ready = -1;  // the device on which prepare_tree / prepare_maps have run
     void *planned_ws = nullptr;
     PkvStaging staging;
     // side stream + fork/join events of the mixed step's concurrent passes

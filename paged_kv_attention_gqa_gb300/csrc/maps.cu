@@ -249,6 +249,15 @@ __global__ void __launch_bounds__(kMapThreads) maps_counts_kernel(const MapsArgs
 
 }  // namespace dev
 
+static cudaError_t raise_limit(const void *kernel, cudaStream_t st) {
+    return set_smem_limit(kernel, (size_t)6 * (kMapsMaxRows + 1) * 4, st);
+}
+
+cudaError_t prepare_maps(cudaStream_t st) {
+    const cudaError_t e = raise_limit((const void *)dev::maps_kernel<int>, st);
+    return e != cudaSuccess ? e : raise_limit((const void *)dev::maps_kernel<long long>, st);
+}
+
 cudaError_t launch_maps(const MapsArgs &a, cudaStream_t st) {
     const size_t smem = (size_t)6 * (a.rows + 1) * 4;
     // an entry a thread, or as many CTAs as fit the GPU
@@ -256,7 +265,7 @@ cudaError_t launch_maps(const MapsArgs &a, cudaStream_t st) {
     const int ctas = (int)std::min<long long>(304, 1 + work / dev::kMapThreads);
     const bool in_place = a.held_out == a.held || a.free_count_out == a.free_count;
     auto launch = [&](auto kernel) {
-        const cudaError_t e = set_smem_limit((const void *)kernel, (size_t)6 * (kMapsMaxRows + 1) * 4, st);
+        const cudaError_t e = raise_limit((const void *)kernel, st);
         return e != cudaSuccess ? e : launch_pdl(kernel, dim3(ctas), dim3(dev::kMapThreads), smem, st, a, in_place ? 0 : 1);
     };
     // no sum is above the tokens that full tables hold

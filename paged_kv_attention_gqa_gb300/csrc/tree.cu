@@ -825,10 +825,15 @@ __global__ void __launch_bounds__(32 * WARPS) tree_join_kernel(const TreeArgs a,
 }
 
 template <int D, TreeForm FORM>
+static cudaError_t raise_limit(cudaStream_t st) {
+    return set_smem_limit((const void *)tree_kernel<D, FORM>, 1024 + TrSmem<D, FORM>::BYTES, st);
+}
+
+template <int D, TreeForm FORM>
 static cudaError_t launch(const TreeArgs &a, const TreePlan &p, int ctas, const CUtensorMap &tm_kv, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const CUtensorMap &tm_q, cudaStream_t st) {
     const size_t smem = 1024 + TrSmem<D, FORM>::BYTES;
-    cudaError_t e = set_smem_limit((const void *)tree_kernel<D, FORM>, smem, st);
+    cudaError_t e = raise_limit<D, FORM>(st);
     if (e == cudaSuccess) e = launch_pdl(tree_kernel<D, FORM>, dim3(ctas), dim3(kTrThreads), smem, st, tm_kv, tm_k, tm_v, tm_q, a);
     if (e != cudaSuccess || ctas == 1 || p.whole) return e;
     constexpr int WARPS = D == 64 ? 4 : 8;
@@ -838,6 +843,13 @@ static cudaError_t launch(const TreeArgs &a, const TreePlan &p, int ctas, const 
 }
 
 }  // namespace dev
+
+cudaError_t prepare_tree(const Shape &s, cudaStream_t st) {
+    if (s.head_dim == 256) return dev::raise_limit<256, dev::TURNS>(st);
+    const cudaError_t e = s.head_dim == 64 ? dev::raise_limit<64, dev::SPLIT>(st) : dev::raise_limit<128, dev::SPLIT>(st);
+    if (e != cudaSuccess) return e;
+    return s.head_dim == 64 ? dev::raise_limit<64, dev::PAIR>(st) : dev::raise_limit<128, dev::PAIR>(st);
+}
 
 cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm_kv, const CUtensorMap &tm_k,
                         const CUtensorMap &tm_v, const CUtensorMap &tm_q, int box_new, int box_q, void *ws, void *out,

@@ -140,6 +140,9 @@ cudaError_t launch_tree(const Shape &s, const TreePlan &p, const CUtensorMap &tm
                         const CUtensorMap &tm_v, const CUtensorMap &tm_q, int box_new, int box_q, void *ws, void *out,
                         float *lse, cudaStream_t st);
 
+// Raise the shared-memory limits of every kernel that a tree step of this head_dim may choose.
+cudaError_t prepare_tree(const Shape &s, cudaStream_t st);
+
 struct TreeAccept {
     const void *draft, *target;
     int wide;  // the tokens are 64-bit
@@ -162,5 +165,6 @@ struct MapsArgs {
     int32_t *held_out, *free_count_out, *qo, *kvp, *kvi, *last, *slots, *positions, *status;
 };
 cudaError_t launch_maps(const MapsArgs &a, cudaStream_t st);
+cudaError_t prepare_maps(cudaStream_t st);  // as prepare_tree
 
 }  // namespace pkv

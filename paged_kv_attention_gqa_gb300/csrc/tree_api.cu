@@ -39,6 +39,20 @@ static uint32_t tag(pkv_handle_t h) {
     return h->tree_tag;
 }
 
+// Kernel attributes are set outside captures alone.  So a handle's first uncaptured call on a device sets those of all
+// kernels that its calls of any size may choose: a captured one may be of another size than those before it.
+template <typename F>
+static cudaError_t prepare(int &ready, cudaStream_t st, F &&raise) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess || device == ready) return e;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &cs) == cudaSuccess && cs != cudaStreamCaptureStatusNone) return cudaSuccess;
+    e = raise();
+    if (e == cudaSuccess) ready = device;
+    return e;
+}
+
 static uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
 extern "C" pkv_status pkv_build_maps(pkv_handle_t h, const int32_t *seq_lens, const int32_t *new_lens, int batch,
@@ -91,7 +105,9 @@ extern "C" pkv_status pkv_build_maps(pkv_handle_t h, const int32_t *seq_lens, co
         a.slots = slots;
         a.positions = positions;
         a.status = status;
-        const cudaError_t e = pkv::launch_maps(a, static_cast<cudaStream_t>(stream));
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        cudaError_t e = prepare(h->maps_ready, st, [&] { return pkv::prepare_maps(st); });
+        if (e == cudaSuccess) e = pkv::launch_maps(a, st);
         return e == cudaSuccess ? PKV_OK : cuda_fail(h, e, "maps launch");
     });
 }
@@ -132,7 +148,9 @@ extern "C" pkv_status pkv_plan_tree(pkv_handle_t h, const int32_t *qo_indptr, co
             p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.f / std::sqrt((float)s.head_dim)) * 1.4426950408889634f;
         p.pages = kv_indices;
         const pkv::TreeIndex x{qo_indptr, kv_indptr, kv_indices, last_page_len, parents, num_indices, positions};
-        const cudaError_t e = pkv::launch_tree_plan(s, p, x, tag(h), workspace, static_cast<cudaStream_t>(stream));
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        cudaError_t e = prepare(h->tree_ready, st, [&] { return pkv::prepare_tree(s, st); });
+        if (e == cudaSuccess) e = pkv::launch_tree_plan(s, p, x, tag(h), workspace, st);
         if (e != cudaSuccess) return cuda_fail(h, e, "tree plan launch");
         pkv::Plan plan;
         plan.mode = PKV_MODE_TREE;
