@@ -1,5 +1,5 @@
-"""Build libpkv.so in-tree: nvcc for sm_103a, one process per translation unit; and the Python module _marshal, which
-hands the tensors of the speculative step's calls to it.
+"""Build libpkv.so in-tree: nvcc for sm_103a, one process per translation unit; and, where torch is installed, the Python
+module _marshal, which hands the tensors of the speculative step's calls to it.
 
     python -m paged_kv_attention_gqa_gb300.build [--force] [--verbose]
 """
@@ -39,9 +39,15 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_folder():
+    """Where torch is installed, found without importing it; None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else None
+
+
 def _marshal_command(out: str):
-    """g++ with torch's headers and libraries, found without importing it."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """g++ with torch's headers and libraries."""
+    torch = _torch_folder()
     lib = os.path.join(torch, "lib")
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-isystem", os.path.join(torch, "include"), "-isystem",
             sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-L" + lib, "-ltorch_python", "-ltorch_cpu",
@@ -54,7 +60,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "pkv.h")]
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), *extra_flags]
     procs, objs, marshal = [], [], None
-    if force or _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(ROOT, "include", "pkv.h")]):
+    if _torch_folder() is None:  # the library itself is plain C and CUDA
+        sys.stderr.write("torch is not installed: _marshal, which the calls of the speculative step need, is not built\n")
+    elif force or _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(ROOT, "include", "pkv.h")]):
         marshal = MARSHAL + f".{os.getpid()}.tmp"
         procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(marshal), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in SOURCES:
@@ -77,15 +85,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(out.decode(errors="replace"))
         if p.returncode:
             failed.append(src)
-    if failed:
+    if any(src in SOURCES for src in failed):
         raise RuntimeError(f"compilation failed of {failed}")
-    if marshal:
+    if marshal and not failed:
         os.replace(marshal, MARSHAL)
     if force or procs or _stale(OUT, objs):
         tmp = OUT + f".{os.getpid()}.tmp"
         subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"],
                        check=True)
         os.replace(tmp, OUT)
+    if failed:
+        raise RuntimeError(f"compilation failed of {failed} (the library is built)")
     return OUT
 
 
