@@ -45,6 +45,28 @@ def _torch_folder():
     return os.path.dirname(spec.origin) if spec else None
 
 
+def _torch_mark() -> str:
+    """Which torch that is: its place and its version file."""
+    folder = _torch_folder()
+    try:
+        with open(os.path.join(folder, "version.py")) as f:
+            return folder + "\n" + f.read()
+    except OSError:
+        return folder + "\n"
+
+
+def _marshal_stale() -> bool:
+    """The module holds torch's inlined headers and its libraries' place, so it is also stale where torch is another one than
+    the one noted beside it."""
+    if _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(ROOT, "include", "pkv.h")]):
+        return True
+    try:
+        with open(MARSHAL + ".torch") as f:
+            return f.read() != _torch_mark()
+    except OSError:
+        return True
+
+
 def _marshal_command(out: str):
     """g++ with torch's headers and libraries."""
     torch = _torch_folder()
@@ -62,7 +84,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     procs, objs, marshal = [], [], None
     if _torch_folder() is None:  # the library itself is plain C and CUDA
         sys.stderr.write("torch is not installed: _marshal, which the calls of the speculative step need, is not built\n")
-    elif force or _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(ROOT, "include", "pkv.h")]):
+    elif force or _marshal_stale():
         marshal = MARSHAL + f".{os.getpid()}.tmp"
         procs.append(("marshal.cpp", subprocess.Popen(_marshal_command(marshal), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in SOURCES:
@@ -89,6 +111,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         raise RuntimeError(f"compilation failed of {failed}")
     if marshal and not failed:
         os.replace(marshal, MARSHAL)
+        with open(marshal, "w") as f:
+            f.write(_torch_mark())
+        os.replace(marshal, MARSHAL + ".torch")
     if force or procs or _stale(OUT, objs):
         tmp = OUT + f".{os.getpid()}.tmp"
         subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"],

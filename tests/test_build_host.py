@@ -41,3 +41,19 @@ def test_the_library_is_built_where_the_module_does_not_compile(made, monkeypatc
     with pytest.raises(RuntimeError, match="marshal.cpp"):
         B.build()
     assert os.path.exists(B.OUT) and not os.path.exists(B.MARSHAL)
+
+
+def test_the_module_follows_torch(made, monkeypatch, tmp_path):
+    """It is compiled against torch's headers: another torch, in another place or in the same, takes another module."""
+    B.build()
+    B.build()
+    assert len(made) == 1 and os.path.exists(B.MARSHAL)
+    folder = tmp_path / "torch"
+    folder.mkdir()
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec",
+                        lambda name, *a: types.SimpleNamespace(origin=str(folder / "__init__.py")) if name == "torch" else find(name, *a))
+    for i, version in enumerate(("1.0", "1.0", "1.1", "1.1")):
+        (folder / "version.py").write_text(f"__version__ = '{version}'\n")
+        B.build()
+        assert len(made) == 2 + i // 2, (i, version)
