@@ -511,16 +511,17 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 constexpr bool ORDINARY = decltype(ordinary)::value;
                 const bool first = j < (FORM == SPLIT ? 2 : 1);  // the group's first tile of the piece
                 const uint32_t b = it & 1, S = S_col(x, b) + lane_off;
-                TreeTile k;
+                TreeTile k = {};
                 unsigned long long vis = ~0ull;
-                if constexpr (!ORDINARY) k = tree_tile(p.row, p.tile + j, a.window_left);
-                if (ORDINARY) {
-                } else if (k.drafted) {
-                    if (live) vis = a.masks[node * a.words + (k.key0 >> 6)];
-                } else if (k.special) {
-                    const int begin = min(max(lo - k.key0, 0), 64);
-                    vis = begin < 64 ? ~0ull << begin : 0ull;
-                    if (k.keys < 64) vis &= (1ull << max(k.keys, 0)) - 1;
+                if constexpr (!ORDINARY) {
+                    k = tree_tile(p.row, p.tile + j, a.window_left);
+                    if (k.drafted) {
+                        if (live) vis = a.masks[node * a.words + (k.key0 >> 6)];
+                    } else if (k.special) {
+                        const int begin = min(max(lo - k.key0, 0), 64);
+                        vis = begin < 64 ? ~0ull << begin : 0ull;
+                        if (k.keys < 64) vis &= (1ull << max(k.keys, 0)) - 1;
+                    }
                 }
                 if (!mbar_wait(&s_full[2 * x + b], (it >> 1) & 1, err, kErrWaitFull)) return false;
                 if (idle) {  // P's rows of this warp stay as they are: O's are never read
