@@ -145,7 +145,7 @@ extern "C" pkv_status pkv_plan_tree(pkv_handle_t h, const int32_t *qo_indptr, co
             return fail(h, PKV_ERR_WORKSPACE,
                         "workspace of " + std::to_string(workspace_bytes) + " bytes is too small: this plan needs " +
                             std::to_string(p.total) + " bytes (pkv_workspace_size gives the bound at the maxima)");
-            p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.f / std::sqrt((float)s.head_dim)) * 1.4426950408889634f;
+        p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.f / std::sqrt((float)s.head_dim)) * 1.4426950408889634f;
         p.pages = kv_indices;
         const pkv::TreeIndex x{qo_indptr, kv_indptr, kv_indices, last_page_len, parents, num_indices, positions};
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
