@@ -101,9 +101,11 @@ __device__ __forceinline__ void plan_error(const TreePlanArgs &a, int code) {
     }
 }
 
+// The index arrays are read by ordinary loads: the kernel before this one, beside which it may already run, writes them,
+// and the read-only path (__ldg) asks for memory that nobody writes while the kernel lives.
 // A row's first token, 0 if that is no token of the step; and the highest of the rows [from, to), for the whole warp.
 __device__ __forceinline__ int first_token(const TreePlanArgs &a, int r) {
-    const int q = __ldg(a.x.qo + r);
+    const int q = a.x.qo[r];
     return q <= a.tokens ? q : 0;
 }
 __device__ __forceinline__ int highest_token(const TreePlanArgs &a, int from, int to) {
@@ -117,8 +119,8 @@ __device__ __forceinline__ int highest_token(const TreePlanArgs &a, int from, in
 // tokens.  A row that begins below it could have tokens of another one, whose nodes would be written twice.
 __device__ __forceinline__ TreeRow tree_row(const TreePlanArgs &a, int r, int highest, bool &ok) {
     TreeRow t = {};
-    const int q0 = __ldg(a.x.qo + r), q1 = __ldg(a.x.qo + r + 1), k0 = __ldg(a.x.kvp + r), k1 = __ldg(a.x.kvp + r + 1);
-    const int fill = __ldg(a.x.last + r);
+    const int q0 = a.x.qo[r], q1 = a.x.qo[r + 1], k0 = a.x.kvp[r], k1 = a.x.kvp[r + 1];
+    const int fill = a.x.last[r];
     ok = q0 >= highest && q1 >= q0 && q1 <= a.tokens && q1 - q0 <= a.max_new && k0 >= 0 && k1 >= k0 && k1 <= a.x.num_indices;
     if (r == 0) ok = ok && q0 == 0 && k0 == 0;
     long long length = 0;
