@@ -735,8 +735,14 @@ __global__ void __launch_bounds__(32 * WARPS) tree_join_kernel(const TreeArgs a,
     __shared__ float4 others[WARPS * COLS * 32];
     __shared__ float2 sums[WARPS * 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the plan was complete before the attention kernel let this one start
-    const TreeJoin u = a.joins[blockIdx.x];
+    // The plan was complete before the attention kernel let this one start.  But nothing has been waited for here, so the
+    // record is read past L1, which may still hold an earlier step's
+    union {
+        int4 part[2];
+        TreeJoin u;
+    } record;
+    for (int i = 0; i < 2; ++i) record.part[i] = __ldcg(reinterpret_cast<const int4 *>(a.joins + blockIdx.x) + i);
+    const TreeJoin u = record.u;
     const int rows = u.tokens * a.group, tile_rows = a.tile_tokens * a.group;
     const int R = u.rows, place0 = blockIdx.y * tree_join_rows(rows) + u.row0, place = place0 + (lane & (R - 1));
     // rows of the unit (token * group + head) at these places of its one or two tiles

@@ -101,3 +101,35 @@ def test_the_uncaptured_maps_may_be_of_another_size():
     """2,500 rows of 2^20 tokens, whose sums are taken in 64 bits and whose offsets need more than 48 KB of shared memory,
     behind two short ones."""
     run(MAPS)
+
+
+CUT = r"""
+import sys
+sys.path[:0] = [".", "tests"]
+import torch
+from test_gpu_step import Loop, trees_of
+
+D, H, most = (int(x) for x in sys.argv[1:])
+loop = Loop([3000, 700, 1500], H, 2, D, 16, 1, 230, 17, most)
+saved = {k: v.clone() for k, v in loop.d.items()}
+loop.step()
+torch.cuda.synchronize()
+for k, v in saved.items():
+    loop.d[k].copy_(v)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+    loop.step()
+for i in range(4):
+    loop.feed(trees_of(i + 1, 3, most), 80 + 5 * i)
+    graph.replay()
+    torch.cuda.synchronize()
+    loop.mirror()
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("D,H,most", [(64, 4, 9), (128, 8, 70), (256, 4, 20)])
+def test_replayed_steps_cut_their_units_elsewhere(D, H, most):
+    """Long rows whose trees change from replay to replay, and with them the join's records."""
+    run(CUT, D, H, most)
