@@ -399,6 +399,7 @@ pkv_status pkv_run_evict(pkv_handle_t h, void *kv_layer, float *scores, int32_t 
  * free_pages[0 .. *free_count) is a stack of free page ids.  First the pages that rows have too many are pushed
  * onto it, rows and blocks ascending; then rows, ascending, pop their missing pages, the topmost going to
  * the row's first missing block.  (A row that has ended has length 0 and no new tokens: all its pages go back.)
+ * A page belongs to one row: what two rows list would be given back by each.
  * Outputs: block_table (the new blocks' entries; others are left as they are), num_blocks_out[batch],
  * *free_count_out, qo_indptr[batch + 1], kv_indptr[batch + 1], kv_indices (the rows' pages one after
  * another; entries behind them are left), last_page_len[batch] (0 for a row without pages), and, where

@@ -10,9 +10,10 @@
 // positions) are then cut evenly over the CTAs, and a warp finds its first row by bisection.
 // The pages held and the free count may be updated in place: a CTA could then overwrite what another has yet to
 // read, so in that case a second kernel writes them.
-// Latency-bound: a chain of loads (lengths, offsets, table) and the stores.  Measured: one row 3.1 us, 200 rows of up to
-// 8,190 tokens in pages of 16 4.5 us, 500 rows of up to 30,011 in pages of 8 (971,000 page ids) 7.2 us, 48 prompts of
-// 8,111 tokens without pages 4.6 us.
+// Latency-bound: a chain of loads (lengths, offsets, table) and the stores.  Measured with the counts written elsewhere, one
+// state replayed in a graph (called with states that change from call to call): one row 3.1 us (4.2), 200 rows of up to
+// 8,190 tokens in pages of 16 4.5 us (4.8), 500 rows of up to 30,011 in pages of 8 (971,000 page ids) 7.2 us (7.4), 48
+// prompts of 8,111 tokens without pages 4.5 us (4.6).  Counts in place: 1.4 to 1.8 us more.
 #include <cuda_runtime.h>
 
 #include <algorithm>

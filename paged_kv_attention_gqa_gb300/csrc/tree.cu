@@ -28,11 +28,13 @@
 //    looked over by it, and if it holds NaN or infinities each row adds the keys it sees alone.
 //  * The running maximum moves (and O is rescaled) only when it grows by more than 2^8.  Maxima and
 //    sums are 32-bit; P is rounded to bf16 for the MMA (relative 2^-8 a weight at most), the sum adds it unrounded.
-// Measured (32 or 64 query heads on 8 kv heads of 128 unless said): one row of 517 tokens, 8 drafted: 9.4 us; 32 rows
-// of 203 to 8,190, 16 drafted: 94 us, 557 MB, at the copy rate between start and end; 16 rows of 611 to 12,001, 61
-// drafted, 64 query heads: 149 us, 998 TFLOP/s (159 us held under the power cap; S with both operands in shared memory
-// takes 48 cycles a k-step for 32: 1,280 of 1,700 cycles a tile of two query tiles); 3 chains of 5 behind 30,011 to
-// 65,521 tokens, 20 heads on 4 of 64: 38 us; 24 rows of head_dim 256 under a window of 2,047: 71 us.
+// Measured, one state replayed in a graph (32 or 64 query heads on 8 kv heads of 128 unless said): one row of 517 tokens, 8
+// drafted: 9.5 us; 32 rows of 203 to 8,190, 16 drafted: 94 to 95 us, 557 MB, at the copy rate between start and end; 16 rows
+// of 611 to 12,001, 61 drafted, 64 query heads: 149 us, 995 TFLOP/s (161 us, 920 TFLOP/s, with states that change and the
+// card under its power cap); 3 chains of 5 behind 30,011 to 65,521 tokens, 20 heads on 4 of 64: 38 us; 24 rows of head_dim
+// 256 under a window of 2,047: 71 us.  Of the wide case's 1,950 cycles a tile of two query tiles the MMAs take 1,280: S over 64
+// keys reads both operands from shared memory, 48 cycles a k-step for 32 of arithmetic (over 128 keys: 64 for 64).  Query
+// rows are padded to 128: 16 rows of 49 drafted tokens, 392 query rows a head, take 170 us, of 48, 384, 149.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -13,10 +13,12 @@
 // take the path's keys and values to the row's next slots (copies by all threads, 16 bytes each, were bound by the
 // instructions of their addresses: 12.4 us where bulk copies take 9.0).  HBM-bound for batches (each accepted vector
 // read and written once), a chain of loads for one row.
-// Measured: 64 rows of up to 16 nodes, 32 layers of 8 heads of 128, 43 MB: 10.2 us; 40 rows with paths of 20, 24 layers
-// of 4 heads of 64, 16.5 MB: 6.7 us; one row, 32 layers: 2.7 us.  The plan of 1 to
-// 64 rows takes 3.4 to 7.1 us with trees of up to 61 nodes, 100 us with chains of 200: a lane walks its nodes to the root,
-// a load after the other.
+// Measured with states that change from call to call (one state replayed in a graph, whose bytes then come from L2): 64 rows
+// of up to 16 nodes, 32 layers of 8 heads of 128, 43 MB: 10.3 us (7.5); 40 rows with paths of 20, 24 layers of 4 heads of 64,
+// 16.5 MB: 6.6 us (6.5); one row, 32 layers: 3.8 us (2.7).
+// The plan, replayed: one row of 8 nodes 4.3 us, 32 rows of 16 5.1, 64 rows of 61 5.4, 40 rows of 61 up to 32
+// deep 7.1.  A lane walks each of its nodes to the root, a load after the other, so deep trees take long: a row's chain of 200
+// 100 us, of 256 136, 64 bushy trees of 200 18.
 #include <cuda_runtime.h>
 
 #include <algorithm>
